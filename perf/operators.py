@@ -302,7 +302,10 @@ def _plain_adamw(s):
 # ------------------------------------------------------- the library's calls
 
 def _own_weight(q, s):
-    return q.QuantizedWeight(q.FMT_INT8, s["O"], s["I"], s["I"], 0, 8, s["codes"], scale=s["scale"])
+    """The weight, as a program keeps it once it has quantized or loaded it."""
+    if "weight" not in s:
+        s["weight"] = q.QuantizedWeight(q.FMT_INT8, s["O"], s["I"], s["I"], 0, 8, s["codes"], scale=s["scale"])
+    return s["weight"]
 
 
 def _own_tensors(q, s):
