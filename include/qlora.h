@@ -30,8 +30,8 @@
  *     (QLORA_ERR_ALIGNMENT otherwise); faster paths that need 16-byte
  *     alignment are chosen only when the pointers have it.
  *   - Work is enqueued on `stream` (a cudaStream_t; NULL = legacy default
- *     stream).  Only qlora_quantize_nf4, qlora_quantize_affine and
- *     qlora_workspace_status synchronize `stream` (to read a device flag).
+ *     stream).  Only qlora_quantize_nf4, qlora_quantize_affine,
+ *     qlora_quantize_int8 and qlora_workspace_status synchronize `stream` (to read a device flag).
  *   - Arguments are validated on the host before anything is launched; a
  *     rejected call returns a status and enqueues nothing.  Nothing aborts
  *     and no exception crosses the ABI.
@@ -68,7 +68,8 @@ typedef enum {
 typedef enum {
   QLORA_FMT_NF4_DQ = 0,        /* NF4 codes + u8 scale codes + fp32 t_g + fp32 mu */
   QLORA_FMT_NF4_FP32SCALE = 1, /* NF4 codes + one fp32 absmax per block (legacy) */
-  QLORA_FMT_AFFINE = 2         /* 4/8-bit codes + fp32 scale and bias per group   */
+  QLORA_FMT_AFFINE = 2,        /* 4/8-bit codes + fp32 scale and bias per group   */
+  QLORA_FMT_INT8 = 3           /* signed 8-bit codes + one fp32 scale per row     */
 } qlora_format;
 
 typedef enum {
@@ -97,8 +98,15 @@ typedef enum {
  *            codes        ceil(N*bits/8) bytes (4-bit: low nibble first)
  *            scale, bias  ceil(N/G) floats each
  *            w_hat = scale_g * code + bias_g
+ *   INT8:    bits = 8; block and group ignored (block >= 1).
+ *            codes        O rows of qlora_int8_pitch(I) signed bytes in
+ *                         [-127, 127]; the bytes from I to the pitch are 0
+ *            scale        O floats, one per output channel (row)
+ *            w_hat = scale_o * code
+ *            The linear entry points multiply in 8-bit integers: see
+ *            qlora_linear_fwd.
  * The fwd/bwd entry points require I % block == 0 (blocks never straddle
- * rows); the quantizers and qlora_dequantize accept any N.
+ * rows; not for INT8); the quantizers and qlora_dequantize accept any N.
  */
 typedef struct {
   int32_t fmt; /* qlora_format */
@@ -220,6 +228,26 @@ qlora_status qlora_quantize_affine(const float* W, int64_t O, int64_t I, int32_t
                                    uint8_t* codes, float* scale, float* bias, void* ws,
                                    size_t ws_bytes, qlora_stream_t stream);
 
+/* HOST.  Bytes of one row of INT8 codes: I rounded up to a multiple of 16. */
+int64_t qlora_int8_pitch(int64_t I);
+
+/* HOST.  Workspace bytes qlora_quantize_int8 needs (the status header). */
+size_t qlora_quantize_int8_workspace_bytes(int64_t O, int64_t I);
+
+/*
+ * Symmetric 8-bit quantization of W [O x I] fp32, one scale per row (output
+ * channel):
+ *   scale_o = fp32(max_i |w_oi| / 127),
+ *   code = clamp(round(fp32(w_oi / scale_o)), -127, 127), round half to
+ *   even; 0 where scale_o = 0.
+ * Outputs: codes [O x qlora_int8_pitch(I)] (the padding is written as 0),
+ * scale [O].  Bit-exact and deterministic.  Synchronizes `stream`;
+ * QLORA_ERR_NONFINITE for NaN/Inf (outputs undefined).  O = 0 or I = 0 is
+ * valid (scales 0).
+ */
+qlora_status qlora_quantize_int8(const float* W, int64_t O, int64_t I, int8_t* codes, float* scale,
+                                 void* ws, size_t ws_bytes, qlora_stream_t stream);
+
 /*
  * Diagnostic dequantization ("QLoRA Fine-Tuning", "NF4 representation":
  * dequantize() is an explicit diagnostic/export operation that the training
@@ -227,7 +255,8 @@ qlora_status qlora_quantize_affine(const float* W, int64_t O, int64_t I, int32_t
  *   NF4_DQ: c[code] * s_hat_b,  s_hat_b = clamp(mu + fp32(fp32(t_g (q_b -
  *           128)) / 127), 0, FLT_MAX);
  *   NF4_FP32SCALE: c[code] * s_b;
- *   AFFINE: fp32(scale_g * code) + bias_g.
+ *   AFFINE: fp32(scale_g * code) + bias_g;
+ *   INT8:   scale_o * code.
  * Bit-exact.  Never used by qlora_linear_fwd / qlora_linear_bwd.
  */
 qlora_status qlora_dequantize(const qlora_weight* w, float* W_hat, qlora_stream_t stream);
@@ -267,6 +296,96 @@ qlora_status qlora_adam_step(float* params, const float* grads, float* m, float*
                              int64_t t, float lr, float beta1, float beta2, float eps,
                              int64_t page_elems, qlora_stream_t stream);
 
+/* Element types of qlora_tensor. */
+typedef enum { QLORA_DTYPE_FP32 = 0, QLORA_DTYPE_BF16 = 1 } qlora_dtype;
+
+/*
+ * One tensor of an optimizer step (a HOST struct holding device pointers).
+ *   param        n values of param_type, updated in place
+ *   grad         n values of grad_type
+ *   32-bit states: m, v are n floats each; m_scale, v_scale ignored
+ *   8-bit states:  in blocks of QLORA_STATE_BLOCK values, M = ceil(n / 256):
+ *     m          n signed bytes k in [-127, 127], m_scale M floats:
+ *                m = m_scale_b * (k/127) |k/127|
+ *     v          n unsigned bytes k, v_scale M floats:
+ *                sqrt(v) = v_scale_b * (k/255)^2
+ *     (all zero bytes and scales stand for zero states)
+ * fp32 arrays on a 4-byte boundary, bf16 arrays on a 2-byte one.  The
+ * tensors of one call must not overlap, and no tensor may be listed twice
+ * (a value updated twice at once has no defined result).
+ */
+typedef struct {
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  int32_t param_type, grad_type; /* qlora_dtype */
+} qlora_tensor;
+
+#define QLORA_STATE_BLOCK 256
+
+/*
+ * What one training step decides on the device (16 bytes of DEVICE memory,
+ * 4-byte aligned, zeroed by the caller before the first step):
+ * qlora_grad_norm writes it and qlora_adamw_step reads it, so that clipping,
+ * skipping and the step count need no host round trip and replay correctly
+ * in a captured graph.
+ */
+typedef struct {
+  float norm;   /* global gradient norm of the last qlora_grad_norm        */
+  float scale;  /* factor for every gradient: min(1, max_norm / norm)      */
+  int32_t skip; /* 1: a gradient was NaN or Inf; the step changes nothing  */
+  int32_t step; /* steps taken (the t of the bias corrections)             */
+} qlora_step_control;
+
+/* HOST.  Workspace bytes of qlora_grad_norm (0 on bad arguments). */
+size_t qlora_grad_norm_workspace_bytes(const qlora_tensor* tensors, int32_t count);
+
+/*
+ * Global L2 norm of all gradients, and the decisions taken on it:
+ *   norm  = fp32(sqrt(sum of grad^2)), squares and sums in 64 bits, in an
+ *           order that depends on the sizes alone (deterministic);
+ *   scale = max_norm / norm where max_norm > 0 and norm > max_norm, else 1;
+ *   skip  = norm is NaN or Inf (a NaN or Inf gradient, or a norm above
+ *           FLT_MAX); scale is then 1;
+ *   step += 1 unless skip.
+ * tensors: HOST array of `count` >= 0 (only grad, n and grad_type are read;
+ * copied into the launches, so it may be freed after the call).  max_norm
+ * finite, <= 0 for no clipping.
+ */
+qlora_status qlora_grad_norm(const qlora_tensor* tensors, int32_t count, float max_norm,
+                             qlora_step_control* control, void* ws, size_t ws_bytes,
+                             qlora_stream_t stream);
+
+/*
+ * One AdamW step over `count` tensors at once (decoupled weight decay), every
+ * fp32 operation rounded once:
+ *   g = grad * scale                            (scale of `control`, else 1)
+ *   m = b1 m + fp32(1 - b1) g
+ *   v = b2 v + fp32(1 - b2) g^2
+ *   p = p fp32(1 - lr wd) - (fp32(lr / bc1) m) / (fp32(1 / sqrt(bc2)) sqrt(v) + eps)
+ * with bc1 = 1 - b1^t, bc2 = 1 - b2^t in 64 bits; a bf16 param is rounded to
+ * nearest even once.  state_bits = 32: fp32 states.  state_bits = 8: the
+ * step uses the m and v above, then stores them as codes of the new block
+ * maxima m_scale = max |m|, v_scale = max sqrt(v):
+ *   k = round(127 sqrt(|m| fp32(1 / m_scale))) with the sign of m,
+ *   k = round(255 sqrt(sqrt(v) fp32(1 / v_scale))), at least 1 where v > 0
+ * (so no moving value is divided by a second moment that was rounded to
+ * zero); a block whose maximum is below FLT_MIN gets codes of 0.  A NaN
+ * gradient in a step that is not skipped makes its block of 256 states NaN.
+ * tensors: HOST array (see qlora_grad_norm).  control (DEVICE, nullable):
+ * gives scale, skip and t; when NULL, t >= 1 is the argument.  Requires
+ * 0 <= beta < 1, eps > 0, finite lr and weight_decay >= 0.  In place; with
+ * more tensors than fit one launch (about 500) it takes several.
+ */
+qlora_status qlora_adamw_step(const qlora_tensor* tensors, int32_t count, int32_t state_bits,
+                              int64_t t, float lr, float beta1, float beta2, float eps,
+                              float weight_decay, const qlora_step_control* control,
+                              qlora_stream_t stream);
+
 /* op codes for qlora_linear_workspace_bytes */
 #define QLORA_OP_FWD 0
 #define QLORA_OP_BWD 1
@@ -300,6 +419,16 @@ size_t qlora_linear_workspace_bytes(const qlora_weight* w, int64_t R, int32_t r,
  * Deterministic: the same inputs give the same bits (every reduction
  * across blocks is summed in a fixed order).
  * Requires 1 <= r <= 64 and I % block == 0.
+ *
+ * INT8 weights: the base product is taken in 8-bit integers, with a scale
+ * for each token and channel.  Each token of X is quantized as
+ * qlora_quantize_int8 quantizes a row (codes n_x, scale s_x), then
+ *   Y = (s_x (n_x n_w^T)) scale_o + s U B^T,
+ * the integer sum exact, everything after it in fp32, one rounding to the
+ * type of Y; U uses the unquantized X.  `compute` is the type of X and Y.  A
+ * token that holds a NaN or Inf gives a row of NaN; other tokens do not see
+ * it.  Requires codes on a 16-byte boundary and 1 <= O, I <= 131072 (above
+ * which the 32-bit sum could overflow: QLORA_ERR_UNSUPPORTED).
  */
 qlora_status qlora_linear_fwd(const qlora_weight* w, const void* X, int64_t R, const float* A,
                               const float* B, int32_t r, float alpha, int32_t compute, void* Y,
@@ -316,6 +445,10 @@ qlora_status qlora_linear_fwd(const qlora_weight* w, const void* X, int64_t R, c
  * U_in (nullable) is U = X A^T from the forward; when NULL it is
  * recomputed.  Types as in qlora_linear_fwd; dA and dB are fp32 and
  * overwritten.
+ * INT8 weights: the base product is taken in 8-bit integers too.  Each row
+ * of fp32(dY * scale_o) is quantized as a token is in the forward (codes
+ * n_g, scale s_g), and dX = s_g (n_g n_w) + s V A.  V, dA and dB use the
+ * unquantized dY and X.
  */
 qlora_status qlora_linear_bwd(const qlora_weight* w, const void* X, const void* dY, int64_t R,
                               const float* A, const float* B, int32_t r, float alpha,

@@ -9,25 +9,29 @@ fallback: without the built library or a CUDA device the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
-from typing import Optional, Tuple
+from typing import List, Optional, Sequence, Tuple
 
 import torch
 
 from . import _ffi
-from ._ffi import (COMPUTE_BF16, COMPUTE_FP32, FMT_AFFINE, FMT_NF4_DQ, FMT_NF4_FP32SCALE, OP_BWD,
-                   OP_FWD, qlora_weight)
+from ._ffi import (COMPUTE_BF16, COMPUTE_FP32, DTYPE_BF16, DTYPE_FP32, FMT_AFFINE, FMT_INT8,
+                   FMT_NF4_DQ, FMT_NF4_FP32SCALE, OP_BWD, OP_FWD, STATE_BLOCK, qlora_tensor, qlora_weight)
 
 __all__ = [
     "QLoraError", "QuantizedWeight", "qlora_status_string", "qlora_nf4_codebook",
     "qlora_nf4_payload_bytes", "qlora_quantize_nf4", "qlora_quantize_nf4_noalloc", "qlora_quantize_affine",
     "qlora_nf4_fp32scale_payload_bytes", "qlora_quantize_nf4_fp32scale",
+    "qlora_int8_pitch", "qlora_quantize_int8",
     "qlora_dequantize", "qlora_merge", "qlora_adam_step",
+    "OptimTensors", "step_control", "qlora_grad_norm_workspace_bytes", "qlora_grad_norm", "qlora_adamw_step",
     "qlora_linear_workspace_bytes", "qlora_linear_fwd", "qlora_linear_bwd",
     "qlora_workspace_status", "qlora_selftest_wait_timeout", "qlora_kernel_launch_count",
     "qlora_kernel_timing_enable", "qlora_kernel_timing_collect",
-    "COMPUTE_FP32", "COMPUTE_BF16", "FMT_NF4_DQ", "FMT_NF4_FP32SCALE", "FMT_AFFINE", "workspace",
+    "COMPUTE_FP32", "COMPUTE_BF16", "FMT_NF4_DQ", "FMT_NF4_FP32SCALE", "FMT_AFFINE", "FMT_INT8",
+    "STATE_BLOCK", "workspace",
 ]
 
 
@@ -53,6 +57,14 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(dev):
+    """Makes the tensors' device the current one for a call."""
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _need(where: str, name: str, t: Optional[torch.Tensor], dev, shape=None, dtype=None):
@@ -109,6 +121,8 @@ class QuantizedWeight:
                     "group_absmax": (S, torch.float32), "mean": (1, torch.float32)}
         if self.fmt == FMT_NF4_FP32SCALE:
             return {"codes": ((N + 1) // 2, torch.uint8), "scale": (-(-N // self.block), torch.float32)}
+        if self.fmt == FMT_INT8:
+            return {"codes": (self.O * qlora_int8_pitch(self.I), torch.int8), "scale": (self.O, torch.float32)}
         ng = -(-N // self.block)
         return {"codes": (N if self.bits == 8 else (N + 1) // 2, torch.uint8),
                 "scale": (ng, torch.float32), "bias": (ng, torch.float32)}
@@ -131,9 +145,10 @@ class QuantizedWeight:
         import numpy as np
         w = cls(int(d["fmt"]), int(d["O"]), int(d["I"]), int(d["block"]), int(d["group"]), int(d["bits"]),
                 codes=torch.empty(0, dtype=torch.uint8))
-        if w.fmt not in (FMT_NF4_DQ, FMT_NF4_FP32SCALE, FMT_AFFINE) or w.O < 0 or w.I < 0 or w.block < 1 \
+        if w.fmt not in (FMT_NF4_DQ, FMT_NF4_FP32SCALE, FMT_AFFINE, FMT_INT8) or w.O < 0 or w.I < 0 or w.block < 1 \
                 or (w.fmt == FMT_NF4_DQ and (w.group < 1 or w.bits != 4)) \
-                or (w.fmt == FMT_NF4_FP32SCALE and w.bits != 4) or (w.fmt == FMT_AFFINE and w.bits not in (4, 8)):
+                or (w.fmt == FMT_NF4_FP32SCALE and w.bits != 4) or (w.fmt == FMT_AFFINE and w.bits not in (4, 8)) \
+                or (w.fmt == FMT_INT8 and w.bits != 8):
             raise ValueError("inconsistent format fields")
         for k, (n, dt) in w.expected_sizes().items():
             if k not in d or d[k] is None:
@@ -253,6 +268,31 @@ def qlora_quantize_affine(W: torch.Tensor, bits: int = 4, G: int = 64, stream=No
     return QuantizedWeight(FMT_AFFINE, O, I, G, 0, bits, codes, scale=scale, bias=bias)
 
 
+def qlora_int8_pitch(I: int) -> int:
+    """Bytes of one row of INT8 codes (I rounded up to a multiple of 16)."""
+    return (int(I) + 15) // 16 * 16
+
+
+def qlora_quantize_int8(W: torch.Tensor, stream=None) -> QuantizedWeight:
+    """Symmetric 8-bit codes with one fp32 scale per row (output channel) of a
+    CUDA fp32 [O x I] matrix (synchronizes the stream).  The linear layer
+    multiplies such a weight in 8-bit integers."""
+    lib = _ffi.load()
+    if W.dim() != 2 or W.dtype != torch.float32 or not W.is_cuda:
+        raise ValueError("W must be a CUDA float32 matrix")
+    W = W.contiguous()
+    O, I = W.shape
+    dev = W.device
+    codes = torch.empty((O, qlora_int8_pitch(I)), dtype=torch.int8, device=dev)
+    scale = torch.empty(O, dtype=torch.float32, device=dev)
+    with _on(dev):
+        ws = workspace(lib.qlora_quantize_int8_workspace_bytes(O, I), dev)
+        st = lib.qlora_quantize_int8(_ptr(W), O, I, _ptr(codes), _ptr(scale), _ptr(ws), ws.numel(),
+                                     _stream(stream))
+    _check(st, "qlora_quantize_int8")
+    return QuantizedWeight(FMT_INT8, O, I, max(I, 1), 0, 8, codes, scale=scale)
+
+
 def qlora_dequantize(w: QuantizedWeight, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Diagnostic fp32 reconstruction of the whole weight (never used by fwd/bwd)."""
     lib = _ffi.load()
@@ -298,6 +338,144 @@ def qlora_adam_step(params: torch.Tensor, grads: torch.Tensor, m: torch.Tensor, 
     _check(st, "qlora_adam_step")
 
 
+_DTYPES = {torch.float32: DTYPE_FP32, torch.bfloat16: DTYPE_BF16}
+
+
+class OptimTensors:
+    """The tensors of an optimizer step, checked once: gradients and, for
+    qlora_adamw_step, parameters and their AdamW states.  grads and params are
+    fp32 or bf16, each pair of one size.  States in 32 bits: m and v are fp32
+    of the parameter's size.  States in 8 bits: m is int8 and v uint8 of that
+    size, with fp32 scales m_scale and v_scale for each STATE_BLOCK values
+    (zeros stand for zero states).  with_states() allocates zero states.
+
+    The tensors are kept and used in place: keep writing gradients into the
+    same storage (or build a new object for new tensors).  No two parameters
+    or states may overlap."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], params: Optional[Sequence[torch.Tensor]] = None,
+                 m: Optional[Sequence[torch.Tensor]] = None, v: Optional[Sequence[torch.Tensor]] = None,
+                 m_scale: Optional[Sequence[torch.Tensor]] = None,
+                 v_scale: Optional[Sequence[torch.Tensor]] = None):
+        self.grads = list(grads)
+        self.params = None if params is None else list(params)
+        self.m, self.v = (None if x is None else list(x) for x in (m, v))
+        self.m_scale, self.v_scale = (None if x is None else list(x) for x in (m_scale, v_scale))
+        self.device = self.grads[0].device if self.grads else None
+        n = len(self.grads)
+        for name in ("params", "m", "v", "m_scale", "v_scale"):
+            x = getattr(self, name)
+            if x is not None and len(x) != n:
+                raise ValueError(f"OptimTensors: {name} must list {n} tensors, one for each gradient")
+        if self.params is not None and (self.m is None or self.v is None):
+            raise ValueError("OptimTensors: params need the states m and v")
+        if (self.m_scale is None) != (self.v_scale is None):
+            raise ValueError("OptimTensors: 8-bit states need both m_scale and v_scale")
+        self.state_bits = 8 if self.m_scale is not None else 32
+        self._c = (qlora_tensor * max(n, 1))()
+        f = "OptimTensors"
+        for i, g in enumerate(self.grads):
+            if g.dtype not in _DTYPES:
+                raise ValueError(f"{f}: grads must be float32 or bfloat16, got {g.dtype}")
+            _need(f, f"grads[{i}]", g, self.device)
+            c = self._c[i]
+            c.grad, c.n, c.grad_type = g.data_ptr(), g.numel(), _DTYPES[g.dtype]
+            if self.params is None:
+                continue
+            p = self.params[i]
+            if p.dtype not in _DTYPES:
+                raise ValueError(f"{f}: params must be float32 or bfloat16, got {p.dtype}")
+            _need(f, f"params[{i}]", p, self.device, g.shape)
+            bits8 = self.state_bits == 8
+            blocks = -(-g.numel() // STATE_BLOCK)
+            for name, dt, size in (("m", torch.int8 if bits8 else torch.float32, g.numel()),
+                                   ("v", torch.uint8 if bits8 else torch.float32, g.numel()),
+                                   ("m_scale", torch.float32, blocks), ("v_scale", torch.float32, blocks)):
+                x = getattr(self, name)
+                if x is None:
+                    continue
+                _need(f, f"{name}[{i}]", x[i], self.device, dtype=dt)
+                if x[i].numel() != size:
+                    raise ValueError(f"{f}: {name}[{i}] must have {size} values, got {x[i].numel()}")
+                setattr(c, name, x[i].data_ptr())
+            c.param, c.param_type = p.data_ptr(), _DTYPES[p.dtype]
+        if self.params is not None:
+            self._refuse_overlap()
+
+    def _refuse_overlap(self):
+        spans = []
+        for name in ("params", "m", "v", "m_scale", "v_scale"):
+            for x in getattr(self, name) or ():
+                if x.numel() > 0:
+                    spans.append((x.data_ptr(), x.data_ptr() + x.numel() * x.element_size()))
+        spans.sort()
+        if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
+            raise ValueError("OptimTensors: parameters or states overlap (a tensor listed twice?)")
+
+    @classmethod
+    def with_states(cls, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
+                    state_bits: int = 32) -> "OptimTensors":
+        """The parameters and gradients with new zero states of 32 or 8 bits."""
+        params = list(params)
+        if state_bits == 32:
+            z = lambda: [torch.zeros(p.shape, dtype=torch.float32, device=p.device) for p in params]  # noqa: E731
+            return cls(grads, params, z(), z())
+        if state_bits != 8:
+            raise ValueError("state_bits must be 8 or 32")
+        z = lambda dt: [torch.zeros(p.shape, dtype=dt, device=p.device) for p in params]  # noqa: E731
+        s = lambda: [torch.zeros(-(-p.numel() // STATE_BLOCK), dtype=torch.float32, device=p.device)  # noqa: E731
+                     for p in params]
+        return cls(grads, params, z(torch.int8), z(torch.uint8), s(), s())
+
+
+def step_control(device="cuda") -> torch.Tensor:
+    """A zeroed qlora_step_control: int32[4] holding norm (fp32 bits), scale
+    (fp32 bits), skip and step."""
+    return torch.zeros(4, dtype=torch.int32, device=device)
+
+
+def qlora_grad_norm_workspace_bytes(tensors: OptimTensors) -> int:
+    return int(_ffi.load().qlora_grad_norm_workspace_bytes(tensors._c, len(tensors.grads)))
+
+
+def qlora_grad_norm(tensors: OptimTensors, max_norm: float, control: torch.Tensor,
+                    ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Global L2 norm of the gradients into control (see step_control), with
+    the clip factor, the skip flag and the advanced step count; nothing is
+    read back to the host.  max_norm <= 0: no clipping."""
+    dev = tensors.device if tensors.device is not None else control.device
+    f = "qlora_grad_norm"
+    _need(f, "control", control, dev, (4,), torch.int32)
+    with _on(dev):
+        if ws is None:
+            ws = workspace(qlora_grad_norm_workspace_bytes(tensors), dev)
+        _need(f, "ws", ws, dev)
+        st = _ffi.load().qlora_grad_norm(tensors._c, len(tensors.grads), float(max_norm), _ptr(control),
+                                         _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+    _check(st, f)
+    return control
+
+
+def qlora_adamw_step(tensors: OptimTensors, t: int = 0, lr: float = 1e-3, beta1: float = 0.9,
+                     beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0,
+                     control: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One in-place AdamW step over every tensor at once.  The step count, the
+    gradient factor and the skip flag come from control where it is given
+    (written by qlora_grad_norm), else the step count is t >= 1."""
+    f = "qlora_adamw_step"
+    if tensors.params is None:
+        raise ValueError(f"{f}: the OptimTensors hold gradients only")
+    dev = tensors.device
+    if dev is None:
+        return
+    _need(f, "control", control, dev, (4,), torch.int32)
+    with _on(dev):
+        st = _ffi.load().qlora_adamw_step(tensors._c, len(tensors.grads), tensors.state_bits, int(t), float(lr),
+                                          float(beta1), float(beta2), float(eps), float(weight_decay),
+                                          _ptr(control), _stream(stream))
+    _check(st, f)
+
+
 def qlora_linear_workspace_bytes(w: QuantizedWeight, R: int, r: int, op: int, compute: int) -> int:
     cw = w.c_struct()
     return int(_ffi.load().qlora_linear_workspace_bytes(ctypes.byref(cw), R, r, op, compute))
@@ -334,8 +512,9 @@ def qlora_linear_fwd(w: QuantizedWeight, X: torch.Tensor, A: torch.Tensor, B: to
     _need(f, "U_out", U_out, dev, (R, r), torch.float32)
     _need(f, "ws", ws, dev)
     cw = w.c_struct()
-    st = lib.qlora_linear_fwd(ctypes.byref(cw), _ptr(X), R, _ptr(A), _ptr(B), r, float(alpha), compute,
-                              _ptr(Y), _ptr(U_out), _ptr(ws), ws.numel(), _stream(stream))
+    with _on(dev):
+        st = lib.qlora_linear_fwd(ctypes.byref(cw), _ptr(X), R, _ptr(A), _ptr(B), r, float(alpha), compute,
+                                  _ptr(Y), _ptr(U_out), _ptr(ws), ws.numel(), _stream(stream))
     _check(st, "qlora_linear_fwd")
     return Y, U_out
 
@@ -370,9 +549,10 @@ def qlora_linear_bwd(w: QuantizedWeight, X: Optional[torch.Tensor], dY: torch.Te
     _need(f, "dB", dB if want_db else None, wd, (w.O, r), torch.float32)
     _need(f, "ws", ws, wd)
     cw = w.c_struct()
-    st = lib.qlora_linear_bwd(ctypes.byref(cw), _ptr(X), _ptr(dY), R, _ptr(A), _ptr(B), r, float(alpha),
-                              _ptr(U), compute, _ptr(dX if want_dx else None), _ptr(dA if want_da else None),
-                              _ptr(dB if want_db else None), _ptr(ws), ws.numel(), _stream(stream))
+    with _on(wd):
+        st = lib.qlora_linear_bwd(ctypes.byref(cw), _ptr(X), _ptr(dY), R, _ptr(A), _ptr(B), r, float(alpha),
+                                  _ptr(U), compute, _ptr(dX if want_dx else None), _ptr(dA if want_da else None),
+                                  _ptr(dB if want_db else None), _ptr(ws), ws.numel(), _stream(stream))
     _check(st, "qlora_linear_bwd")
     return (dX if want_dx else None), (dA if want_da else None), (dB if want_db else None)
 

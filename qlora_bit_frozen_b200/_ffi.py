@@ -23,10 +23,14 @@ ERR_WORKSPACE = 8
 FMT_NF4_DQ = 0
 FMT_NF4_FP32SCALE = 1
 FMT_AFFINE = 2
+FMT_INT8 = 3
 COMPUTE_FP32 = 0
 COMPUTE_BF16 = 1
 OP_FWD = 0
 OP_BWD = 1
+DTYPE_FP32 = 0
+DTYPE_BF16 = 1
+STATE_BLOCK = 256
 
 
 class qlora_weight(ctypes.Structure):
@@ -46,9 +50,24 @@ class qlora_weight(ctypes.Structure):
     ]
 
 
+class qlora_tensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("param_type", ctypes.c_int32),
+        ("grad_type", ctypes.c_int32),
+    ]
+
+
 # name -> (restype, argtypes)
 _P = ctypes.c_void_p
 _W = ctypes.POINTER(qlora_weight)
+_T = ctypes.POINTER(qlora_tensor)
 _i64, _i32, _u32, _f32, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_float, ctypes.c_size_t
 SIGNATURES = {
     "qlora_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -62,9 +81,15 @@ SIGNATURES = {
     "qlora_quantize_nf4_fp32scale": (ctypes.c_int, [_P, _i64, _i64, _i32, _P, _P, _P, _sz, _P]),
     "qlora_quantize_affine_workspace_bytes": (_sz, [_i64, _i32, _i32]),
     "qlora_quantize_affine": (ctypes.c_int, [_P, _i64, _i64, _i32, _i32, _P, _P, _P, _P, _sz, _P]),
+    "qlora_int8_pitch": (_i64, [_i64]),
+    "qlora_quantize_int8_workspace_bytes": (_sz, [_i64, _i64]),
+    "qlora_quantize_int8": (ctypes.c_int, [_P, _i64, _i64, _P, _P, _P, _sz, _P]),
     "qlora_dequantize": (ctypes.c_int, [_W, _P, _P]),
     "qlora_merge": (ctypes.c_int, [_W, _P, _P, _i32, _f32, _P, _P]),
     "qlora_adam_step": (ctypes.c_int, [_P, _P, _P, _P, _i64, _i64, _f32, _f32, _f32, _f32, _i64, _P]),
+    "qlora_grad_norm_workspace_bytes": (_sz, [_T, _i32]),
+    "qlora_grad_norm": (ctypes.c_int, [_T, _i32, _f32, _P, _P, _sz, _P]),
+    "qlora_adamw_step": (ctypes.c_int, [_T, _i32, _i32, _i64, _f32, _f32, _f32, _f32, _f32, _P, _P]),
     "qlora_linear_workspace_bytes": (_sz, [_W, _i64, _i32, _i32, _i32]),
     "qlora_linear_fwd": (ctypes.c_int, [_W, _P, _i64, _P, _P, _i32, _f32, _i32, _P, _P, _P, _sz, _P]),
     "qlora_linear_bwd": (ctypes.c_int, [_W, _P, _P, _i64, _P, _P, _i32, _f32, _P, _i32, _P, _P, _P, _P,

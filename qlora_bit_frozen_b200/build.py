@@ -16,12 +16,12 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libqlora.so")
 
 SOURCES = ["api.cu", "quantize.cu", "simt.cu", "adapter.cu", "tc_gemm.cu", "smallr.cu", "noalloc.cu",
-           "merge.cu", "adam.cu"]
-HEADERS = ["common.cuh", "internal.h", "tc_gemm.h", "smallr.h"]
+           "merge.cu", "adam.cu", "int8.cu", "optim.cu"]
+HEADERS = ["common.cuh", "internal.h", "tc_gemm.h", "smallr.h", "int8.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]
-EXTRA = {"quantize.cu": ["--fmad=false"], "adam.cu": ["--fmad=false"]}
+EXTRA = {"quantize.cu": ["--fmad=false"], "adam.cu": ["--fmad=false"], "optim.cu": ["--fmad=false"]}
 
 
 def _nvcc():

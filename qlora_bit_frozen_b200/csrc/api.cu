@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "int8.h"
 #include "internal.h"
 #include "smallr.h"
 #include "tc_gemm.h"
@@ -121,6 +122,16 @@ qlora_status check_weight(const qlora_weight* w, bool for_linear) {
     if (w->bits != 4 && w->bits != 8) return QLORA_ERR_SHAPE;
     if (N > 0 && (!w->codes || !w->scale || !w->bias)) return QLORA_ERR_INVALID_ARG;
     if (!al4(w->scale) || !al4(w->bias)) return QLORA_ERR_ALIGNMENT;
+  } else if (w->fmt == QLORA_FMT_INT8) {
+    if (w->bits != 8) return QLORA_ERR_SHAPE;
+    if (N > 0 && (!w->codes || !w->scale)) return QLORA_ERR_INVALID_ARG;
+    if (!al4(w->scale)) return QLORA_ERR_ALIGNMENT;
+    if (for_linear) {
+      if (w->O < 1 || w->I < 1) return QLORA_ERR_SHAPE;
+      if (w->O > kInt8MaxK || w->I > kInt8MaxK) return QLORA_ERR_UNSUPPORTED;
+      if (!aligned(w->codes, 16)) return QLORA_ERR_ALIGNMENT;
+    }
+    return QLORA_OK;
   } else {
     return QLORA_ERR_INVALID_ARG;
   }
@@ -210,6 +221,128 @@ BwdLayout bwd_layout(const qlora_weight* w, int64_t R, int32_t r, int32_t comput
   if (compute == QLORA_COMPUTE_BF16) off += tc_dx_ws(view_of(w), R);
   L.total = off;
   return L;
+}
+
+// INT8 weights: the scratch of the side products (u, v, bt, red, split,
+// red2, split2), then the quantized activation rows and the product's own.
+struct Int8Layout {
+  size_t u = 0, v = 0, bt = 0, red = 0, split = 0, red2 = 0, split2 = 0, rows = 0, total = 0;
+};
+
+Int8Layout int8_layout(const qlora_weight* w, int64_t R, int32_t r, bool bwd) {
+  Int8Layout L;
+  size_t off = kWsZeroed;
+  L.u = off;
+  off += align_up((size_t)R * r * 4, 256);
+  L.v = off;
+  if (bwd) off += align_up((size_t)R * r * 4, 256);
+  L.bt = off;
+  if (bwd) off += align_up((size_t)r * w->O * 4, 256);
+  L.red = off;
+  size_t red = rowdot_ws(R, w->I, r);
+  if (bwd) {
+    const size_t more[3] = {coldot_ws(R, w->I, r), coldot_ws(R, w->O, r), rowdot_ws(R, w->O, r)};
+    for (size_t m : more)
+      if (m > red) red = m;
+  }
+  off += red;
+  L.split = off;
+  size_t sp = adapter_split_ws(w->I, r);
+  if (bwd) {
+    const size_t more[2] = {adapter_split_ws(w->O, r), adapter_split_ws(R, r)};
+    for (size_t m : more)
+      if (m > sp) sp = m;
+  }
+  off += sp;
+  L.red2 = off;
+  if (bwd) off += coldot_ws(R, w->O, r);
+  L.split2 = off;
+  if (bwd) off += adapter_split_ws(R, r);
+  L.rows = off;
+  off += int8_ws(bwd, R, w->O, w->I);
+  L.total = off;
+  return L;
+}
+
+Int8Call int8_call(const qlora_weight* w, bool dx, bool bf16, int64_t R, const void* P, const float* T,
+                   const float* L, int32_t r, float s, void* out) {
+  Int8Call c;
+  c.dx = dx;
+  c.bf16 = bf16;
+  c.R = R;
+  c.O = w->O;
+  c.I = w->I;
+  c.codes = (const int8_t*)w->codes;
+  c.wscale = w->scale;
+  c.P = P;
+  c.T = T;
+  c.L = L;
+  c.r = r;
+  c.s = s;
+  c.out = out;
+  return c;
+}
+
+cudaError_t int8_fwd(const qlora_weight* w, const void* X, int64_t R, const float* A, const float* B,
+                     int32_t r, float sc, bool bf16, void* Y, float* U_out, void* ws, cudaStream_t s) {
+  const Int8Layout L = int8_layout(w, R, r, false);
+  unsigned* tickets = (unsigned*)((char*)ws + kWsHeader);
+  float* U = U_out ? U_out : (float*)((char*)ws + L.u);
+  const Int8Call c = int8_call(w, false, bf16, R, X, U, B, r, sc, Y);
+  cudaError_t e = launch_int8_rows(c, (char*)ws + L.rows, s);
+  if (e == cudaSuccess)
+    e = launch_rowdot(X, bf16, R, w->I, A, false, r, U, s, nullptr, nullptr, 0, 0, 1.0f, nullptr, nullptr,
+                      (float*)((char*)ws + L.red), tickets, (uint16_t*)((char*)ws + L.split));
+  if (e == cudaSuccess) e = launch_int8_product(c, (char*)ws + L.rows, (uint32_t*)ws, s);
+  return e;
+}
+
+// dA = s V^T X and dB = s dY^T U: one launch where the kernels take both,
+// else one each.
+cudaError_t adapter_grads(bool bf16, const void* X, int64_t I, const float* V, float* dA, const void* dY,
+                          int64_t O, const float* U, float* dB, int64_t R, int32_t r, float sc, void* red,
+                          void* red2, uint16_t* split, uint16_t* split2, unsigned* tickets,
+                          cudaStream_t s) {
+  bool paired = false;
+  cudaError_t e = cudaSuccess;
+  if (dA && dB && bf16)
+    e = launch_coldot_pair(X, I, V, false, dA, red, split, dY, O, U, true, dB, red2, split2, R, r, sc, s,
+                           tickets, &paired);
+  if (e == cudaSuccess && dA && !paired)
+    e = launch_coldot(X, bf16, R, I, V, r, sc, false, dA, red, s, tickets, split);
+  if (e == cudaSuccess && dB && !paired)
+    e = launch_coldot(dY, bf16, R, O, U, r, sc, true, dB, red, s, tickets, split);
+  return e;
+}
+
+cudaError_t int8_bwd(const qlora_weight* w, const void* X, const void* dY, int64_t R, const float* A,
+                     const float* B, int32_t r, float sc, const float* U_in, bool bf16, void* dX,
+                     float* dA, float* dB, void* ws, cudaStream_t s) {
+  const Int8Layout L = int8_layout(w, R, r, true);
+  unsigned* tickets = (unsigned*)((char*)ws + kWsHeader);
+  float* V = (float*)((char*)ws + L.v);
+  float* red = (float*)((char*)ws + L.red);
+  uint16_t* split = (uint16_t*)((char*)ws + L.split);
+  cudaError_t e = cudaSuccess;
+  if (R > 0 && (dX || dA))
+    e = launch_rowdot(dY, bf16, R, w->O, B, true, r, V, s, nullptr, nullptr, 0, 0, 1.0f, nullptr,
+                      (float*)((char*)ws + L.bt), red, tickets, split);
+  const float* U = U_in;
+  if (e == cudaSuccess && R > 0 && dB && !U) {
+    float* Uw = (float*)((char*)ws + L.u);
+    e = launch_rowdot(X, bf16, R, w->I, A, false, r, Uw, s, nullptr, nullptr, 0, 0, 1.0f, nullptr, nullptr,
+                      red, tickets, split);
+    U = Uw;
+  }
+  if (e == cudaSuccess)
+    e = adapter_grads(bf16, X, w->I, V, dA, dY, w->O, U, dB, R, r, sc, red, (char*)ws + L.red2, split,
+                      (uint16_t*)((char*)ws + L.split2), tickets, s);
+  if (e == cudaSuccess && R > 0 && dX) {
+    const Int8Call c = int8_call(w, true, bf16, R, dY, V, A, r, sc, dX);
+    e = launch_int8_rows(c, (char*)ws + L.rows, s);
+    if (e == cudaSuccess) e = launch_int8_product(c, (char*)ws + L.rows, (uint32_t*)ws, s);
+  }
+  return e;
 }
 
 }  // namespace
@@ -336,6 +469,34 @@ qlora_status qlora_quantize_affine(const float* W, int64_t O, int64_t I, int32_t
   return h[0] ? (qlora_status)h[0] : QLORA_OK;
 }
 
+int64_t qlora_int8_pitch(int64_t I) {
+  return I < 0 || I > kMaxWeights ? 0 : int8_pitch(I);
+}
+
+size_t qlora_quantize_int8_workspace_bytes(int64_t O, int64_t I) {
+  return weight_count_ok(O, I) ? kWsHeader : 0;
+}
+
+qlora_status qlora_quantize_int8(const float* W, int64_t O, int64_t I, int8_t* codes, float* scale,
+                                 void* ws, size_t ws_bytes, qlora_stream_t stream) {
+  if (O < 0 || I < 0 || O > 0x7fffffffLL) return QLORA_ERR_SHAPE;
+  if (!weight_count_ok(O, I)) return QLORA_ERR_SHAPE;
+  if (!ws) return QLORA_ERR_INVALID_ARG;
+  if (O > 0 && (!scale || (I > 0 && (!W || !codes)))) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(ws, 256) || !al4(W) || !al4(scale)) return QLORA_ERR_ALIGNMENT;
+  if (ws_bytes < kWsHeader) return QLORA_ERR_WORKSPACE;
+  qlora_status st = device_ready();
+  if (st != QLORA_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  st = cuda_status(launch_int8_quantize(W, O, I, codes, scale, ws, s));
+  if (st != QLORA_OK) return st;
+  uint32_t h[3];
+  st = read_header(ws, s, h);
+  if (st != QLORA_OK) return st;
+  if (h[2]) return QLORA_ERR_NONFINITE;
+  return h[0] ? (qlora_status)h[0] : QLORA_OK;
+}
+
 qlora_status qlora_dequantize(const qlora_weight* w, float* W_hat, qlora_stream_t stream) {
   qlora_status st = check_weight(w, false);
   if (st != QLORA_OK) return st;
@@ -343,6 +504,9 @@ qlora_status qlora_dequantize(const qlora_weight* w, float* W_hat, qlora_stream_
   if (!al4(W_hat)) return QLORA_ERR_ALIGNMENT;
   st = device_ready();
   if (st != QLORA_OK) return st;
+  if (w->fmt == QLORA_FMT_INT8)
+    return cuda_status(launch_int8_dequantize((const int8_t*)w->codes, w->scale, w->O, w->I, W_hat,
+                                              (cudaStream_t)stream));
   return cuda_status(launch_dequantize(view_of(w), W_hat, (cudaStream_t)stream));
 }
 
@@ -375,10 +539,72 @@ qlora_status qlora_adam_step(float* params, const float* grads, float* m, float*
                                  (cudaStream_t)stream));
 }
 
+// Shared checks of the many-tensor calls; `step`: the AdamW step's arrays too.
+static qlora_status check_tensors(const qlora_tensor* t, int32_t count, bool step, int32_t bits) {
+  if (count < 0) return QLORA_ERR_SHAPE;
+  if (count > 0 && !t) return QLORA_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < count; ++i) {
+    const qlora_tensor& d = t[i];
+    if (d.n < 0 || d.n > kMaxTensor) return QLORA_ERR_SHAPE;
+    if (d.grad_type != QLORA_DTYPE_FP32 && d.grad_type != QLORA_DTYPE_BF16) return QLORA_ERR_INVALID_ARG;
+    if (step && d.param_type != QLORA_DTYPE_FP32 && d.param_type != QLORA_DTYPE_BF16)
+      return QLORA_ERR_INVALID_ARG;
+    if (d.n == 0) continue;
+    if (!d.grad || (step && (!d.param || !d.m || !d.v))) return QLORA_ERR_INVALID_ARG;
+    if (step && bits == 8 && (!d.m_scale || !d.v_scale)) return QLORA_ERR_INVALID_ARG;
+    if (!aligned(d.grad, d.grad_type == QLORA_DTYPE_BF16 ? 2 : 4)) return QLORA_ERR_ALIGNMENT;
+    if (step && !aligned(d.param, d.param_type == QLORA_DTYPE_BF16 ? 2 : 4)) return QLORA_ERR_ALIGNMENT;
+    if (step && bits == 32 && (!al4(d.m) || !al4(d.v))) return QLORA_ERR_ALIGNMENT;
+    if (step && bits == 8 && (!al4(d.m_scale) || !al4(d.v_scale))) return QLORA_ERR_ALIGNMENT;
+  }
+  return QLORA_OK;
+}
+
+size_t qlora_grad_norm_workspace_bytes(const qlora_tensor* tensors, int32_t count) {
+  if (check_tensors(tensors, count, false, 32) != QLORA_OK) return 0;
+  return grad_norm_ws(tensors, count);
+}
+
+qlora_status qlora_grad_norm(const qlora_tensor* tensors, int32_t count, float max_norm,
+                             qlora_step_control* control, void* ws, size_t ws_bytes,
+                             qlora_stream_t stream) {
+  qlora_status st = check_tensors(tensors, count, false, 32);
+  if (st != QLORA_OK) return st;
+  if (!isfinite(max_norm) || !control || !ws) return QLORA_ERR_INVALID_ARG;
+  if (!al4(control) || !aligned(ws, 256)) return QLORA_ERR_ALIGNMENT;
+  if (ws_bytes < grad_norm_ws(tensors, count)) return QLORA_ERR_WORKSPACE;
+  st = device_ready();
+  if (st != QLORA_OK) return st;
+  return cuda_status(launch_grad_norm(tensors, count, max_norm, control, ws, (cudaStream_t)stream));
+}
+
+qlora_status qlora_adamw_step(const qlora_tensor* tensors, int32_t count, int32_t state_bits, int64_t t,
+                              float lr, float beta1, float beta2, float eps, float weight_decay,
+                              const qlora_step_control* control, qlora_stream_t stream) {
+  if (state_bits != 8 && state_bits != 32) return QLORA_ERR_INVALID_ARG;
+  qlora_status st = check_tensors(tensors, count, true, state_bits);
+  if (st != QLORA_OK) return st;
+  if (!control && t < 1) return QLORA_ERR_SHAPE;
+  if (!(beta1 >= 0.0f && beta1 < 1.0f) || !(beta2 >= 0.0f && beta2 < 1.0f))
+    return QLORA_ERR_INVALID_ARG;
+  if (!(eps > 0.0f) || !isfinite(eps) || !isfinite(lr)) return QLORA_ERR_INVALID_ARG;
+  if (!(weight_decay >= 0.0f) || !isfinite(weight_decay)) return QLORA_ERR_INVALID_ARG;
+  if (!al4(control)) return QLORA_ERR_ALIGNMENT;
+  st = device_ready();
+  if (st != QLORA_OK) return st;
+  return cuda_status(launch_adamw(tensors, count, state_bits, t, lr, beta1, beta2, eps, weight_decay,
+                                  control, (cudaStream_t)stream));
+}
+
 size_t qlora_linear_workspace_bytes(const qlora_weight* w, int64_t R, int32_t r, int32_t op,
                                     int32_t compute) {
   if (!w || R < 0 || r < 1 || r > 64) return 0;
   if (compute != QLORA_COMPUTE_FP32 && compute != QLORA_COMPUTE_BF16) return 0;
+  if (w->fmt == QLORA_FMT_INT8) {
+    if (w->O < 1 || w->I < 1 || w->O > kInt8MaxK || w->I > kInt8MaxK) return 0;
+    if (op != QLORA_OP_FWD && op != QLORA_OP_BWD) return 0;
+    return int8_layout(w, R, r, op == QLORA_OP_BWD).total;
+  }
   if (op == QLORA_OP_FWD) return fwd_layout(w, R, r, compute).total;
   if (op == QLORA_OP_BWD) return bwd_layout(w, R, r, compute).total;
   return 0;
@@ -405,8 +631,10 @@ qlora_status qlora_linear_fwd(const qlora_weight* w, const void* X, int64_t R, c
   if (R > 0 && (!X || !Y)) return QLORA_ERR_INVALID_ARG;
   const size_t esz = compute == QLORA_COMPUTE_BF16 ? 2 : 4;
   if (!aligned(X, esz) || !aligned(Y, esz) || !al4(U_out)) return QLORA_ERR_ALIGNMENT;
-  const FwdLayout L = fwd_layout(w, R, r, compute);
-  if (ws_bytes < L.total) return QLORA_ERR_WORKSPACE;
+  const bool int8 = w->fmt == QLORA_FMT_INT8;
+  if (int8 && R > INT32_MAX) return QLORA_ERR_SHAPE;
+  const FwdLayout L = int8 ? FwdLayout() : fwd_layout(w, R, r, compute);
+  if (ws_bytes < (int8 ? int8_layout(w, R, r, false).total : L.total)) return QLORA_ERR_WORKSPACE;
   st = device_ready();
   if (st != QLORA_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
@@ -414,8 +642,11 @@ qlora_status qlora_linear_fwd(const qlora_weight* w, const void* X, int64_t R, c
   if (e != cudaSuccess) return QLORA_ERR_CUDA;
   if (R == 0) return QLORA_OK;
   unsigned* tickets = (unsigned*)((char*)ws + kWsHeader);
-  float* red = (float*)((char*)ws + L.red);
   const float sc = alpha / (float)r;
+  if (int8)
+    return cuda_status(
+        int8_fwd(w, X, R, A, B, r, sc, compute == QLORA_COMPUTE_BF16, Y, U_out, ws, s));
+  float* red = (float*)((char*)ws + L.red);
   float* U = U_out ? U_out : (float*)((char*)ws + L.u);
   const WView v = view_of(w);
   const bool bf16 = compute == QLORA_COMPUTE_BF16;
@@ -455,8 +686,10 @@ qlora_status qlora_linear_bwd(const qlora_weight* w, const void* X, const void* 
   if (!aligned(X, esz) || !aligned(dY, esz) || !aligned(dX, esz) || !al4(U_in) || !al4(dA) ||
       !al4(dB))
     return QLORA_ERR_ALIGNMENT;
-  const BwdLayout L = bwd_layout(w, R, r, compute);
-  if (ws_bytes < L.total) return QLORA_ERR_WORKSPACE;
+  const bool int8 = w->fmt == QLORA_FMT_INT8;
+  if (int8 && R > INT32_MAX) return QLORA_ERR_SHAPE;
+  const BwdLayout L = int8 ? BwdLayout() : bwd_layout(w, R, r, compute);
+  if (ws_bytes < (int8 ? int8_layout(w, R, r, true).total : L.total)) return QLORA_ERR_WORKSPACE;
   st = device_ready();
   if (st != QLORA_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
@@ -465,6 +698,8 @@ qlora_status qlora_linear_bwd(const qlora_weight* w, const void* X, const void* 
   unsigned* tickets = (unsigned*)((char*)ws + kWsHeader);
   const bool bf16 = compute == QLORA_COMPUTE_BF16;
   const float sc = alpha / (float)r;
+  if (int8)
+    return cuda_status(int8_bwd(w, X, dY, R, A, B, r, sc, U_in, bf16, dX, dA, dB, ws, s));
   const WView v = view_of(w);
   float* V = (float*)((char*)ws + L.v);
   void* red = (char*)ws + L.red;

@@ -1,0 +1,45 @@
+// int8.h -- host interface of the 8-bit integer linear kernels (int8.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "qlora.h"
+
+namespace qlora {
+
+// Longest reduction whose 32-bit sum cannot overflow: 127^2 * 2^17 < 2^31.
+constexpr int64_t kInt8MaxK = 131072;
+
+constexpr int64_t int8_pitch(int64_t n) { return (n + 15) / 16 * 16; }
+
+// codes [O x pitch], scale [O] of W [O x I]; ws: the status header.
+cudaError_t launch_int8_quantize(const float* W, int64_t O, int64_t I, int8_t* codes, float* scale,
+                                 void* ws, cudaStream_t st);
+cudaError_t launch_int8_dequantize(const int8_t* codes, const float* scale, int64_t O, int64_t I,
+                                   float* out, cudaStream_t st);
+
+// The base product of one call: `rows` activation rows over `K`, `N` outputs.
+// Forward (dx false): K = I, N = O, row factor scale s_x, column factor
+// scale_o, adapter rows L = B [N x r].  Input gradient: K = O, N = I, scale_o
+// folded into the rows before they are quantized, adapter L = A [r x N].
+struct Int8Call {
+  bool dx;
+  bool bf16;             // type of the activations and of the output
+  int64_t R, O, I;
+  const int8_t* codes;   // [O x int8_pitch(I)]
+  const float* wscale;   // [O]
+  const void* P;         // activations [R x K]
+  const float* T;        // U or V [R x r]
+  const float* L;        // B [O x r] or A [r x I]
+  int32_t r;
+  float s;
+  void* out;             // [R x N]
+};
+size_t int8_ws(bool dx, int64_t R, int64_t O, int64_t I);
+// Quantizes the activation rows into the workspace (before or after T is
+// computed), then multiplies.
+cudaError_t launch_int8_rows(const Int8Call& c, void* ws, cudaStream_t st);
+cudaError_t launch_int8_product(const Int8Call& c, void* ws, uint32_t* hdr, cudaStream_t st);
+
+}  // namespace qlora

@@ -28,6 +28,10 @@ inline bool weight_count_ok(int64_t O, int64_t I) {
   return O <= kMaxWeights / I;
 }
 
+// Most values of one tensor of an optimizer step (2^38: its blocks of 256
+// fit 31 bits).
+constexpr int64_t kMaxTensor = (int64_t)1 << 38;
+
 // Zeroed ticket counters after the workspace status header (1024 x u32):
 // zeroed with the header at the start of every linear call; kernels that
 // take one leave it zero again.
@@ -57,6 +61,15 @@ cudaError_t launch_merge(const WView& w, const float* A, const float* B, int32_t
 cudaError_t launch_adam(float* p, const float* g, float* m, float* v, int64_t n, int64_t t,
                         float lr, float beta1, float beta2, float eps, int64_t page,
                         cudaStream_t st);
+
+// optim.cu -- the gradient norm and the AdamW step over many tensors (host
+// descriptors, passed as kernel parameters)
+size_t grad_norm_ws(const qlora_tensor* t, int32_t count);
+cudaError_t launch_grad_norm(const qlora_tensor* t, int32_t count, float max_norm,
+                             qlora_step_control* control, void* ws, cudaStream_t st);
+cudaError_t launch_adamw(const qlora_tensor* t, int32_t count, int32_t bits, int64_t step, float lr,
+                         float beta1, float beta2, float eps, float weight_decay,
+                         const qlora_step_control* control, cudaStream_t st);
 
 // simt.cu -- generic (SIMT) linear kernels, both compute modes
 cudaError_t launch_simt_fwd(const WView& w, const void* X, int64_t R, const float* A,

@@ -15,6 +15,7 @@
 // float4 stores when every row starts on a 16-byte boundary; the bound is
 // the 4 bytes per element written (plus 0.5-1 byte of codes read).
 #include "common.cuh"
+#include "int8.h"
 #include "internal.h"
 
 namespace qlora {
@@ -110,8 +111,15 @@ __device__ __forceinline__ void weight4(const WView& w, uint64_t n0, const float
   for (int j = 0; j < 4; ++j) v[j] = __fadd_rn(__fmul_rn(sc, (float)q[j]), bi);
 }
 
-// VEC: I % 4 == 0, block % 4 == 0 and out 16-byte aligned.
-template <bool NARROW, bool VEC>
+// INT8 weights: scale_o * code, rows of codes int8_pitch(I) bytes apart.
+__device__ __forceinline__ float weight_int8(const WView& w, int64_t o, int64_t i) {
+  const int8_t* row = (const int8_t*)w.codes + o * int8_pitch(w.I);
+  return __fmul_rn((float)row[i], __ldg(w.scale + o));
+}
+
+// VEC: I % 4 == 0, block % 4 == 0 and out 16-byte aligned.  INT8: the weight
+// has that format (VEC false).
+template <bool NARROW, bool VEC, bool INT8 = false>
 __global__ void __launch_bounds__(kThreads) merge_kernel(MergeArgs a) {
   __shared__ __align__(16) float As[kRank][kCols];  // A[k0 + k, i0 + c]
   __shared__ float Bs[kRank][kRows + 1];            // B[o0 + row, k0 + k]
@@ -175,7 +183,8 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(MergeArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (ib + j < I)
-          a.out[n0 + j] = __fadd_rn(weight1<NARROW>(a.w, n0 + j, lut), __fmul_rn(a.s, acc[q][j]));
+          a.out[n0 + j] = __fadd_rn(INT8 ? weight_int8(a.w, o, ib + j) : weight1<NARROW>(a.w, n0 + j, lut),
+                                    __fmul_rn(a.s, acc[q][j]));
       }
     }
   }
@@ -200,7 +209,8 @@ cudaError_t launch_merge(const WView& w, const float* A, const float* B, int32_t
   const bool narrow = N <= 0xffffffffLL;
   const bool vec = (w.I % 4 == 0) && (w.block % 4 == 0) && ((uintptr_t)out % 16 == 0);
   const dim3 grid((unsigned)tiles);
-  if (narrow && vec) merge_kernel<true, true><<<grid, kThreads, 0, st>>>(a);
+  if (w.fmt == QLORA_FMT_INT8) merge_kernel<false, false, true><<<grid, kThreads, 0, st>>>(a);
+  else if (narrow && vec) merge_kernel<true, true><<<grid, kThreads, 0, st>>>(a);
   else if (narrow) merge_kernel<true, false><<<grid, kThreads, 0, st>>>(a);
   else if (vec) merge_kernel<false, true><<<grid, kThreads, 0, st>>>(a);
   else merge_kernel<false, false><<<grid, kThreads, 0, st>>>(a);

@@ -1,0 +1,470 @@
+// optim.cu -- one training step's optimizer work over many tensors at once:
+// the global gradient norm and AdamW with states in 32 or in 8 bits
+// ("QLoRA Fine-Tuning", "Training lifecycle": only the LoRA factors are
+// optimizer inputs; a model has two small factors for every adapted linear,
+// so hundreds of tensors, each far too small to fill the GPU alone).
+//
+// The tensors' descriptors travel as kernel parameters (no device table, no
+// copy, and a captured graph holds them); each warp finds the tensor of its
+// 256-value block by bisection over the descriptors' first blocks.
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace qlora {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBlock = QLORA_STATE_BLOCK;  // values per warp and per 8-bit scale
+
+struct Desc {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+  int64_t n;
+  uint32_t first;  // first block of this tensor in the launch
+  uint8_t pbf16, gbf16, vec, pad;
+};
+
+// Descriptors of one launch.  A kernel takes up to 32764 bytes of
+// parameters; a launch of few tensors takes the smaller form, whose
+// parameters cost less to copy.
+template <int CAP>
+struct Batch {
+  int32_t count;
+  uint32_t blocks;
+  Desc d[CAP];
+};
+constexpr int kFew = 60;
+constexpr int kMany = 500;
+static_assert(sizeof(Batch<kMany>) + 128 <= 32764, "kernel parameter limit");
+
+template <int CAP>
+__device__ __forceinline__ int find(const Batch<CAP>& b, uint32_t blk) {
+  int lo = 0, hi = b.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (b.d[mid].first <= blk) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// A lane's eight values of a block: two runs of four where the arrays take
+// vector accesses, else every 32nd value.
+template <bool VEC>
+__device__ __forceinline__ int place(int lane, int j) {
+  return VEC ? (j >> 2) * 128 + 4 * lane + (j & 3) : lane + 32 * j;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load_f32(const float* a, int lane, int left, float (&x)[8]) {
+  if (VEC && left >= kBlock) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 t = __ldcs(reinterpret_cast<const float4*>(a) + 32 * h + lane);
+      x[4 * h] = t.x; x[4 * h + 1] = t.y; x[4 * h + 2] = t.z; x[4 * h + 3] = t.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = place<VEC>(lane, j) < left ? a[place<VEC>(lane, j)] : 0.0f;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load_bf16(const uint16_t* a, int lane, int left, float (&x)[8]) {
+  if (VEC && left >= kBlock) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint2 t = __ldcs(reinterpret_cast<const uint2*>(a) + 32 * h + lane);
+      x[4 * h] = __uint_as_float(t.x << 16);
+      x[4 * h + 1] = __uint_as_float(t.x & 0xffff0000u);
+      x[4 * h + 2] = __uint_as_float(t.y << 16);
+      x[4 * h + 3] = __uint_as_float(t.y & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      x[j] = place<VEC>(lane, j) < left ? bf16_bits_to_float(a[place<VEC>(lane, j)]) : 0.0f;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load_any(const void* a, bool bf16, int64_t at, int lane, int left,
+                                         float (&x)[8]) {
+  if (bf16) load_bf16<VEC>((const uint16_t*)a + at, lane, left, x);
+  else load_f32<VEC>((const float*)a + at, lane, left, x);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_f32(float* a, int lane, int left, const float (&x)[8]) {
+  if (VEC && left >= kBlock) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      reinterpret_cast<float4*>(a)[32 * h + lane] =
+          make_float4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (place<VEC>(lane, j) < left) a[place<VEC>(lane, j)] = x[j];
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_any(void* a, bool bf16, int64_t at, int lane, int left,
+                                          const float (&x)[8]) {
+  if (!bf16) {
+    store_f32<VEC>((float*)a + at, lane, left, x);
+    return;
+  }
+  uint16_t* o = (uint16_t*)a + at;
+  if (VEC && left >= kBlock) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      reinterpret_cast<uint2*>(o)[32 * h + lane] =
+          make_uint2(pack_bf16x2(x[4 * h], x[4 * h + 1]), pack_bf16x2(x[4 * h + 2], x[4 * h + 3]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (place<VEC>(lane, j) < left)
+        o[place<VEC>(lane, j)] = (uint16_t)(pack_bf16x2(x[j], 0.0f) & 0xffffu);
+  }
+}
+
+// Eight code bytes of a lane, byte j of the pair of words = code of value j.
+template <bool VEC>
+__device__ __forceinline__ void load_codes(const uint8_t* a, int lane, int left, uint32_t (&w)[2]) {
+  if (VEC && left >= kBlock) {
+    w[0] = __ldcs(reinterpret_cast<const uint32_t*>(a) + lane);
+    w[1] = __ldcs(reinterpret_cast<const uint32_t*>(a) + 32 + lane);
+  } else {
+    w[0] = w[1] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (place<VEC>(lane, j) < left)
+        w[j >> 2] |= (uint32_t)a[place<VEC>(lane, j)] << (8 * (j & 3));
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_codes(uint8_t* a, int lane, int left, const uint32_t (&w)[2]) {
+  if (VEC && left >= kBlock) {
+    reinterpret_cast<uint32_t*>(a)[lane] = w[0];
+    reinterpret_cast<uint32_t*>(a)[32 + lane] = w[1];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (place<VEC>(lane, j) < left)
+        a[place<VEC>(lane, j)] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+  }
+}
+
+// ------------------------------------------------------------------ AdamW
+
+struct AdamWArgs {
+  float b1, b2, omb1, omb2, eps, decay;
+  float step_size, inv_rbc2;  // lr / bc1, 1 / sqrt(bc2) (when control is null)
+  double lr, b1d, b2d;
+  const qlora_step_control* control;
+};
+
+// b^t by squaring: the same 64-bit products on the host and on the device.
+__host__ __device__ inline double power(double b, int64_t t) {
+  double r = 1.0;
+  for (; t > 0; t >>= 1) {
+    if (t & 1) r *= b;
+    b *= b;
+  }
+  return r;
+}
+
+__host__ __device__ inline void bias_terms(double lr, double b1, double b2, int64_t t, float* step_size,
+                                           float* inv_rbc2) {
+  *step_size = (float)(lr / (1.0 - power(b1, t)));
+  *inv_rbc2 = (float)(1.0 / sqrt(1.0 - power(b2, t)));
+}
+
+__device__ __forceinline__ float inverse_of(float scale) {
+  return scale < 1.17549435e-38f ? 0.0f : __fdiv_rn(1.0f, scale);  // NaN stays NaN
+}
+
+// Largest of non-negative values by their bits, so that a NaN wins.
+__device__ __forceinline__ float warp_max_bits(float x) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+}
+
+template <int BITS, bool VEC>
+__device__ __forceinline__ void adamw_block(const Desc& d, int64_t blk, int lane, const AdamWArgs& a,
+                                            float scale, float step_size, float inv_rbc2) {
+  const int64_t at = blk * kBlock;
+  const int left = d.n - at < kBlock ? (int)(d.n - at) : kBlock;
+  float g[8], p[8], m[8], v[8];
+  uint32_t mw[2], vw[2];
+  float ms = 0.0f, vs = 0.0f;
+  load_any<VEC>(d.g, d.gbf16, at, lane, left, g);
+  load_any<VEC>(d.p, d.pbf16, at, lane, left, p);
+  if (BITS == 32) {
+    load_f32<VEC>((const float*)d.m + at, lane, left, m);
+    load_f32<VEC>((const float*)d.v + at, lane, left, v);
+  } else {
+    load_codes<VEC>((const uint8_t*)d.m + at, lane, left, mw);
+    load_codes<VEC>((const uint8_t*)d.v + at, lane, left, vw);
+    ms = d.ms[blk];
+    vs = d.vs[blk];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float km = __fmul_rn((float)(int)(int8_t)(mw[j >> 2] >> (8 * (j & 3))), 1.0f / 127.0f);
+      const float kv = __fmul_rn((float)((vw[j >> 2] >> (8 * (j & 3))) & 255u), 1.0f / 255.0f);
+      m[j] = __fmul_rn(__fmul_rn(km, fabsf(km)), ms);
+      const float r = __fmul_rn(__fmul_rn(kv, kv), vs);
+      v[j] = __fmul_rn(r, r);
+    }
+  }
+  float mmax = 0.0f, rmax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float gj = __fmul_rn(g[j], scale);
+    m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gj, a.omb1));
+    v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gj, gj), a.omb2));
+    const float r = __fsqrt_rn(v[j]);
+    const float step = __fdiv_rn(__fmul_rn(m[j], step_size), __fadd_rn(__fmul_rn(r, inv_rbc2), a.eps));
+    p[j] = __fsub_rn(__fmul_rn(p[j], a.decay), step);
+    if (BITS == 8) {
+      v[j] = r;  // what the codes hold
+      mmax = __uint_as_float(max(__float_as_uint(mmax), __float_as_uint(fabsf(m[j]))));
+      rmax = __uint_as_float(max(__float_as_uint(rmax), __float_as_uint(r)));
+    }
+  }
+  store_any<VEC>(d.p, d.pbf16, at, lane, left, p);
+  if (BITS == 32) {
+    store_f32<VEC>((float*)d.m + at, lane, left, m);
+    store_f32<VEC>((float*)d.v + at, lane, left, v);
+    return;
+  }
+  mmax = warp_max_bits(mmax);
+  rmax = warp_max_bits(rmax);
+  const float im = inverse_of(mmax), iv = inverse_of(rmax);
+  mw[0] = mw[1] = vw[0] = vw[1] = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int k = __float2int_rn(__fmul_rn(__fsqrt_rn(__fmul_rn(fabsf(m[j]), im)), 127.0f));
+    int u = __float2int_rn(__fmul_rn(__fsqrt_rn(__fmul_rn(v[j], iv)), 255.0f));
+    if (u == 0 && v[j] > 0.0f && iv > 0.0f) u = 1;
+    mw[j >> 2] |= ((uint32_t)(m[j] < 0.0f ? -k : k) & 255u) << (8 * (j & 3));
+    vw[j >> 2] |= ((uint32_t)u & 255u) << (8 * (j & 3));
+  }
+  store_codes<VEC>((uint8_t*)d.m + at, lane, left, mw);
+  store_codes<VEC>((uint8_t*)d.v + at, lane, left, vw);
+  if (lane == 0) {
+    d.ms[blk] = mmax;
+    d.vs[blk] = rmax;
+  }
+}
+
+template <int BITS, int CAP>
+__global__ void __launch_bounds__(kThreads)
+    adamw_kernel(const __grid_constant__ Batch<CAP> b, const AdamWArgs a) {
+  __shared__ float terms[2];
+  const int lane = threadIdx.x & 31;
+  float scale = 1.0f, step_size = a.step_size, inv_rbc2 = a.inv_rbc2;
+  if (a.control) {
+    if (a.control->skip) return;
+    scale = a.control->scale;
+    if (threadIdx.x == 0) bias_terms(a.lr, a.b1d, a.b2d, a.control->step, &terms[0], &terms[1]);
+    __syncthreads();
+    step_size = terms[0];
+    inv_rbc2 = terms[1];
+  }
+  const uint32_t warps = gridDim.x * (kThreads / 32);
+  for (uint32_t blk = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); blk < b.blocks; blk += warps) {
+    const Desc& d = b.d[find(b, blk)];
+    if (d.vec) adamw_block<BITS, true>(d, blk - d.first, lane, a, scale, step_size, inv_rbc2);
+    else adamw_block<BITS, false>(d, blk - d.first, lane, a, scale, step_size, inv_rbc2);
+  }
+}
+
+// ------------------------------------------------------------------- norm
+
+// Each CTA adds the squares of its blocks in 64 bits and leaves one sum.
+template <int CAP>
+__global__ void __launch_bounds__(kThreads)
+    sumsq_kernel(const __grid_constant__ Batch<CAP> b, double* __restrict__ part) {
+  __shared__ double sums[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t warps = gridDim.x * (kThreads / 32);
+  double acc = 0.0;
+  for (uint32_t blk = blockIdx.x * (kThreads / 32) + warp; blk < b.blocks; blk += warps) {
+    const Desc& d = b.d[find(b, blk)];
+    const int64_t at = (int64_t)(blk - d.first) * kBlock;
+    const int left = d.n - at < kBlock ? (int)(d.n - at) : kBlock;
+    float g[8];
+    if (d.vec) load_any<true>(d.g, d.gbf16, at, lane, left, g);
+    else load_any<false>(d.g, d.gbf16, at, lane, left, g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc = fma((double)g[j], (double)g[j], acc);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if (lane == 0) sums[warp] = acc;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double s = 0.0;
+    for (int w = 0; w < kThreads / 32; ++w) s += sums[w];
+    part[blockIdx.x] = s;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads)
+    norm_kernel(const double* __restrict__ part, int32_t n, float max_norm, qlora_step_control* c) {
+  __shared__ double sums[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  double acc = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) acc += part[i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if (lane == 0) sums[warp] = acc;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  double s = 0.0;
+  for (int w = 0; w < kThreads / 32; ++w) s += sums[w];
+  const float norm = (float)sqrt(s);
+  const bool ok = isfinite(norm);
+  c->norm = norm;
+  c->scale = (ok && max_norm > 0.0f && norm > max_norm) ? __fdiv_rn(max_norm, norm) : 1.0f;
+  c->skip = ok ? 0 : 1;
+  c->step += ok ? 1 : 0;
+}
+
+// ------------------------------------------------------------------- host
+
+bool on(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 148;
+  return n;
+}
+
+constexpr int kCtasPerSm = 8;
+
+// Calls f(batch) for the tensors from `i` on that fit one launch; returns
+// where the next one begins.
+template <int CAP>
+int32_t fill(Batch<CAP>& b, const qlora_tensor* t, int32_t count, int32_t i, int bits, bool grads_only) {
+  b.count = 0;
+  uint64_t blocks = 0;
+  for (; i < count && b.count < CAP; ++i) {
+    if (t[i].n == 0) continue;
+    const uint64_t nb = (uint64_t)(t[i].n + kBlock - 1) / kBlock;
+    if (b.count > 0 && blocks + nb > 0x7fffffffull) break;
+    Desc& d = b.d[b.count++];
+    d.p = t[i].param;
+    d.g = t[i].grad;
+    d.m = t[i].m;
+    d.v = t[i].v;
+    d.ms = t[i].m_scale;
+    d.vs = t[i].v_scale;
+    d.n = t[i].n;
+    d.first = (uint32_t)blocks;
+    d.pbf16 = t[i].param_type == QLORA_DTYPE_BF16;
+    d.gbf16 = t[i].grad_type == QLORA_DTYPE_BF16;
+    d.vec = on(d.g, d.gbf16 ? 8 : 16) &&
+            (grads_only || (on(d.p, d.pbf16 ? 8 : 16) && on(d.m, bits == 8 ? 4 : 16) &&
+                            on(d.v, bits == 8 ? 4 : 16)));
+    d.pad = 0;
+    blocks += nb;
+  }
+  b.blocks = (uint32_t)blocks;
+  return i;
+}
+
+unsigned ctas_for(uint32_t blocks, int sms) {
+  const uint32_t need = (blocks + kThreads / 32 - 1) / (kThreads / 32);
+  const uint32_t most = (uint32_t)(sms * kCtasPerSm);
+  return need < most ? need : most;
+}
+
+template <int CAP>
+cudaError_t adamw_all(const qlora_tensor* t, int32_t count, int32_t bits, const AdamWArgs& a,
+                      cudaStream_t st) {
+  const int sms = sm_count();
+  for (int32_t i = 0; i < count;) {
+    Batch<CAP> b;
+    i = fill(b, t, count, i, bits, false);
+    if (b.count == 0) break;
+    if (bits == 8) adamw_kernel<8, CAP><<<ctas_for(b.blocks, sms), kThreads, 0, st>>>(b, a);
+    else adamw_kernel<32, CAP><<<ctas_for(b.blocks, sms), kThreads, 0, st>>>(b, a);
+    count_launch();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <int CAP>
+cudaError_t sumsq_all(const qlora_tensor* t, int32_t count, double* part, int32_t* n, cudaStream_t st) {
+  const int sms = sm_count();
+  *n = 0;
+  for (int32_t i = 0; i < count;) {
+    Batch<CAP> b;
+    i = fill(b, t, count, i, 32, true);
+    if (b.count == 0) break;
+    const unsigned ctas = ctas_for(b.blocks, sms);
+    sumsq_kernel<CAP><<<ctas, kThreads, 0, st>>>(b, part + *n);
+    count_launch();
+    *n += (int32_t)ctas;
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t grad_norm_ws(const qlora_tensor* t, int32_t count) {
+  // one sum per CTA; a launch holds at least kMany tensors (or, past 2^31
+  // blocks, one), so this bounds the launches of either form
+  size_t launches = (size_t)count / kMany + 1;
+  uint64_t blocks = 0;
+  for (int32_t i = 0; i < count; ++i) blocks += (uint64_t)(t[i].n + kBlock - 1) / kBlock;
+  launches += 2 * (size_t)(blocks / 0x7fffffffull);
+  return align_up(launches * (size_t)sm_count() * kCtasPerSm * sizeof(double), 256);
+}
+
+cudaError_t launch_grad_norm(const qlora_tensor* t, int32_t count, float max_norm,
+                             qlora_step_control* control, void* ws, cudaStream_t st) {
+  double* part = (double*)ws;
+  int32_t n = 0;
+  const cudaError_t e = count <= kFew ? sumsq_all<kFew>(t, count, part, &n, st)
+                                      : sumsq_all<kMany>(t, count, part, &n, st);
+  if (e != cudaSuccess) return e;
+  norm_kernel<<<1, kThreads, 0, st>>>(part, n, max_norm, control);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_adamw(const qlora_tensor* t, int32_t count, int32_t bits, int64_t step, float lr,
+                         float beta1, float beta2, float eps, float weight_decay,
+                         const qlora_step_control* control, cudaStream_t st) {
+  AdamWArgs a = {};
+  a.b1 = beta1;
+  a.b2 = beta2;
+  a.omb1 = (float)(1.0 - (double)beta1);
+  a.omb2 = (float)(1.0 - (double)beta2);
+  a.eps = eps;
+  a.decay = (float)(1.0 - (double)lr * (double)weight_decay);
+  a.lr = lr;
+  a.b1d = beta1;
+  a.b2d = beta2;
+  a.control = control;
+  if (!control) bias_terms(a.lr, a.b1d, a.b2d, step, &a.step_size, &a.inv_rbc2);
+  return count <= kFew ? adamw_all<kFew>(t, count, bits, a, st) : adamw_all<kMany>(t, count, bits, a, st);
+}
+
+}  // namespace qlora
