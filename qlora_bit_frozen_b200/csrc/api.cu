@@ -259,7 +259,7 @@ Int8Layout int8_layout(const qlora_weight* w, int64_t R, int32_t r, bool bwd) {
   L.split2 = off;
   if (bwd) off += adapter_split_ws(R, r);
   L.rows = off;
-  off += int8_ws(bwd, R, w->O, w->I);
+  off += int8_ws(bwd, R, w->O, w->I, r);
   L.total = off;
   return L;
 }

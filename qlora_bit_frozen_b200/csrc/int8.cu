@@ -77,58 +77,6 @@ __global__ void __launch_bounds__(kThreads)
   out[n] = __fmul_rn((float)codes[o * pitch + (n - o * I)], scale[o]);
 }
 
-// 64 x 64 outputs per CTA, 64 terms per pass staged in shared memory, 4 x 4
-// outputs per thread with four-way byte dot products.
-template <bool DX, typename T>
-__global__ void __launch_bounds__(kThreads)
-    product_kernel(const int8_t* __restrict__ xq, const float* __restrict__ xs, int64_t xpitch,
-                   const int8_t* __restrict__ w, const float* __restrict__ ws, int64_t wpitch,
-                   int64_t R, int64_t N, int64_t K, const float* __restrict__ Tr,
-                   const float* __restrict__ L, int32_t r, float s, T* __restrict__ out) {
-  __shared__ __align__(16) int8_t as[64][68], bs[64][68];
-  const int64_t r0 = (int64_t)blockIdx.y * 64, n0 = (int64_t)blockIdx.x * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < K; k0 += 64) {
-    for (int e = threadIdx.x; e < 64 * 64; e += kThreads) {
-      const int a = e >> 6, b = e & 63;
-      as[a][b] = (r0 + a < R && k0 + b < K) ? xq[(r0 + a) * xpitch + k0 + b] : (int8_t)0;
-      if (DX) bs[b][a] = (k0 + a < K && n0 + b < N) ? w[(k0 + a) * wpitch + n0 + b] : (int8_t)0;
-      else bs[a][b] = (n0 + a < N && k0 + b < K) ? w[(n0 + a) * wpitch + k0 + b] : (int8_t)0;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 64; k += 4) {
-      int av[4], bv[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        av[i] = *reinterpret_cast<const int*>(&as[ty + 16 * i][k]);
-        bv[i] = *reinterpret_cast<const int*>(&bs[tx + 16 * i][k]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(av[i], bv[j], acc[i][j]);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = r0 + ty + 16 * i;
-    if (t >= R) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t n = n0 + tx + 16 * j;
-      if (n >= N) continue;
-      float v = __fmul_rn((float)acc[i][j], xs[t]);
-      if (!DX) v = __fmul_rn(v, ws[n]);
-      float d = 0.0f;
-      for (int q = 0; q < r; ++q) d = fmaf(Tr[t * r + q], DX ? L[(int64_t)q * N + n] : L[n * r + q], d);
-      out[t * N + n] = from_f32<T>(fmaf(s, d, v));
-    }
-  }
-}
-
 struct Layout {
   size_t scale, codes, total;
 };
@@ -162,13 +110,20 @@ cudaError_t launch_int8_dequantize(const int8_t* codes, const float* scale, int6
   return cudaGetLastError();
 }
 
-size_t int8_ws(bool dx, int64_t R, int64_t O, int64_t I) { return layout(R, dx ? O : I).total; }
+size_t int8_ws(bool dx, int64_t R, int64_t O, int64_t I, int32_t r) {
+  return layout(R, dx ? O : I).total + int8_tc_ws(dx, R, O, I, r);
+}
 
 cudaError_t launch_int8_rows(const Int8Call& c, void* ws, cudaStream_t st) {
   const int64_t K = c.dx ? c.O : c.I;
   const Layout l = layout(c.R, K);
   float* xs = (float*)((char*)ws + l.scale);
   int8_t* xq = (int8_t*)ws + l.codes;
+  const size_t zero = int8_tc_zeroed(c.dx, c.R, c.O, c.I);
+  if (zero) {
+    const cudaError_t e = cudaMemsetAsync((char*)ws + l.total, 0, zero, st);
+    if (e != cudaSuccess) return e;
+  }
   const float* f = c.dx ? c.wscale : nullptr;
   if (c.bf16)
     rows_kernel<__nv_bfloat16><<<(unsigned)c.R, kThreads, 0, st>>>((const __nv_bfloat16*)c.P, K,
@@ -181,27 +136,9 @@ cudaError_t launch_int8_rows(const Int8Call& c, void* ws, cudaStream_t st) {
 }
 
 cudaError_t launch_int8_product(const Int8Call& c, void* ws, uint32_t* hdr, cudaStream_t st) {
-  (void)hdr;
-  const int64_t K = c.dx ? c.O : c.I, N = c.dx ? c.I : c.O;
-  const Layout l = layout(c.R, K);
-  const float* xs = (const float*)((char*)ws + l.scale);
-  const int8_t* xq = (const int8_t*)ws + l.codes;
-  const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((c.R + 63) / 64));
-  if (grid.y > 65535) return cudaErrorInvalidConfiguration;
-  const int64_t xp = int8_pitch(K), wp = int8_pitch(c.I);
-#define QLORA_GO(DX, TY)                                                                        \
-  product_kernel<DX, TY><<<grid, kThreads, 0, st>>>(xq, xs, xp, c.codes, c.wscale, wp, c.R, N, K, \
-                                                   c.T, c.L, c.r, c.s, (TY*)c.out)
-  if (c.dx) {
-    if (c.bf16) QLORA_GO(true, __nv_bfloat16);
-    else QLORA_GO(true, float);
-  } else {
-    if (c.bf16) QLORA_GO(false, __nv_bfloat16);
-    else QLORA_GO(false, float);
-  }
-#undef QLORA_GO
-  count_launch();
-  return cudaGetLastError();
+  const Layout l = layout(c.R, c.dx ? c.O : c.I);
+  return launch_int8_tc(c, (const int8_t*)ws + l.codes, (const float*)((char*)ws + l.scale),
+                        (char*)ws + l.total, hdr, st);
 }
 
 }  // namespace qlora

@@ -36,10 +36,16 @@ struct Int8Call {
   float s;
   void* out;             // [R x N]
 };
-size_t int8_ws(bool dx, int64_t R, int64_t O, int64_t I);
+size_t int8_ws(bool dx, int64_t R, int64_t O, int64_t I, int32_t r);
 // Quantizes the activation rows into the workspace (before or after T is
 // computed), then multiplies.
 cudaError_t launch_int8_rows(const Int8Call& c, void* ws, cudaStream_t st);
+// int8_tc.cu: the product over codes xq [R x int8_pitch(K)] with row scales
+// xs; ws: int8_tc_ws bytes, of which the first int8_tc_zeroed are zero.
+size_t int8_tc_ws(bool dx, int64_t R, int64_t O, int64_t I, int32_t r);
+size_t int8_tc_zeroed(bool dx, int64_t R, int64_t O, int64_t I);
+cudaError_t launch_int8_tc(const Int8Call& c, const int8_t* xq, const float* xs, void* ws, uint32_t* hdr,
+                           cudaStream_t st);
 cudaError_t launch_int8_product(const Int8Call& c, void* ws, uint32_t* hdr, cudaStream_t st);
 
 }  // namespace qlora

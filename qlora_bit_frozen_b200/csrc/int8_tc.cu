@@ -1,0 +1,910 @@
+// int8_tc.cu -- the integer product of the 8-bit base on the tensor cores
+// (tcgen05.mma kind::i8: signed bytes in, exact 32-bit sums in TMEM).
+//
+// Two kernels share the operand layout: 128-byte K steps (one 128-byte
+// swizzle row per operand row), loaded by TMA, zero-filled past the edges.
+// The activations are K-major codes; the weight codes are K-major in the
+// forward and, read from the same [O x I] bytes, MN-major in the input
+// gradient (a 128 x 128 box with the rows along K), so one tensor map and no
+// transposed copy serve both.
+//
+// pair_kernel   many tokens: a CTA pair takes 256 tokens x 256 outputs
+//               (cta_group::2: each CTA loads its half of both operands, 32 KB
+//               a step against the 48 KB that one CTA's 128 x 256 tile needs
+//               for the same work; at the integer rate the latter asks L2 for
+//               more bytes a cycle than an SM can take).  Persistent, two
+//               accumulators in TMEM: the epilogue of one tile runs under the
+//               next one's products.
+// stream_kernel few tokens or few tiles: the weight tile is the MMA's M side
+//               (128 outputs x 16..128 tokens), so few tokens cost no wasted
+//               rows and the kernel runs at the weight's bandwidth; the K
+//               steps of all tiles are dealt out evenly over the SMs, and
+//               what several CTAs add to one tile meets in 32-bit integer
+//               atomics, exact in any order.
+//
+// The adapter term s T L^T is added in the epilogue with fp32 FMAs: at rank r
+// that is r FMAs an output against K integer products, it costs no second
+// accumulator, and it keeps the adapter at fp32 accuracy.
+//
+// Every wait is bounded; on expiry the kernel records QLORA_ERR_TIMEOUT,
+// stops issuing, and still reaches its barriers and frees its TMEM.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "int8.h"
+#include "internal.h"
+
+namespace qlora {
+namespace {
+
+constexpr int kBK = 128;              // K bytes per step
+constexpr int kHalf = 128 * kBK;      // bytes of a 128-row operand tile
+
+struct Epi {
+  int64_t R, N;
+  const float* xs;   // [R] row scale
+  const float* ws;   // [N] channel scale (forward), else null
+  const float* T;    // [R x r] U or V
+  const float* L;    // packed [Npad x RT] s L (pair) or the factor itself (stream)
+  int32_t r;
+  float s;
+  void* out;
+  int32_t tma_out;   // pair
+  int32_t bf16;      // stream
+  uint32_t* err;
+  uint64_t wait_ns;
+};
+
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= 1ull << 46;
+  d |= 2ull << 61;  // 128-byte swizzle
+  return d;
+}
+
+// kind::i8 instruction descriptor: s8 x s8 -> s32.
+__host__ __device__ constexpr uint32_t idesc_i8(int M, int N, bool a_mn, bool b_mn) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+template <int CTAS>
+__device__ __forceinline__ void umma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  if (CTAS == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrives on the barrier at this offset in both CTAs of the pair once every
+// prior MMA of the thread is complete.
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
+      "%1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// TMA load into this CTA, completing on a barrier that may be the peer's.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* tmap, uint32_t bar, int32_t x,
+                                              int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+      "[%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(tmap), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tmap),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// Two fp32 FMAs in one instruction.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ float sum2(uint64_t a) {
+  return __uint_as_float((uint32_t)a) + __uint_as_float((uint32_t)(a >> 32));
+}
+
+__host__ __device__ constexpr int rank_pad(int r) { return r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : 64; }
+
+// ------------------------------------------------------------ pair kernel
+
+constexpr int kPairStages = 6;
+constexpr int kStage = 2 * kHalf;  // A and B half tiles of one CTA
+constexpr int kOutBuf = 4096;      // 32 rows x 128 bytes
+constexpr int kPairSmem = 1024 + kPairStages * kStage + 8 * kOutBuf + 256;
+static_assert(kPairSmem <= 227 * 1024, "one CTA per SM");
+constexpr int kPairThreads = 256;
+
+struct PairArgs {
+  Epi e;
+  int32_t KB, tiles_m, tiles_n;
+};
+
+// Tile t of the persistent order: groups of kGroup token tiles, every output
+// tile of a group before the next, so that what runs at once shares its
+// operands in L2.
+__device__ __forceinline__ void pair_tile(int64_t t, int tiles_m, int tiles_n, int& m, int& n) {
+  constexpr int kGroup = 8;
+  const int64_t per = (int64_t)kGroup * tiles_n;
+  const int first = (int)(t / per) * kGroup, in = (int)(t % per);
+  const int size = min(tiles_m - first, kGroup);
+  m = first + in % size;
+  n = in / size;
+}
+
+template <bool DX, typename OUT, int RT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                const __grid_constant__ CUtensorMap tm_out, const PairArgs p) {
+  constexpr uint32_t kIdesc = idesc_i8(256, 256, false, DX);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* outbuf = smem + kPairStages * kStage;
+  uint64_t* bars = (uint64_t*)(outbuf + 8 * kOutBuf);
+  uint64_t* full = bars;                      // leader: both CTAs' loads landed
+  uint64_t* empty = bars + kPairStages;       // both: the step's products are done
+  uint64_t* acc_full = bars + 2 * kPairStages;
+  uint64_t* acc_empty = acc_full + 2;         // leader: drained by 4 warps of each CTA
+  volatile uint32_t* tmem_slot = (volatile uint32_t*)(acc_empty + 2);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&acc_full[b]), 1);
+      mbar_init(smem_u32(&acc_empty[b]), 8);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tm_x);
+    prefetch_tensormap(&tm_w);
+    prefetch_tensormap(&tm_out);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32((const void*)tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int64_t t = cluster; t < tiles && ok; t += clusters) {
+        int tm, tn;
+        pair_tile(t, p.tiles_m, p.tiles_n, tm, tn);
+        const int m0 = tm * 256 + 128 * (int)rank, n0 = tn * 256 + 128 * (int)rank;
+        for (int kb = 0; kb < p.KB; ++kb) {
+          if (((kb & 7) == 0 && *abort_flag) ||
+              !mbar_wait(smem_u32(&empty[s]), ph ^ 1u, p.e.wait_ns, p.e.err, 0x501)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          const uint32_t fb = smem_u32(&full[s]), dst = smem_u32(smem + s * kStage);
+          if (rank == 0) mbar_arrive_expect_tx(fb, 2 * kStage);
+          const uint32_t lead = at_rank(fb, 0);
+          tma_load_pair(dst, &tm_x, lead, kb * kBK, m0);
+          tma_load_pair(dst + kHalf, &tm_w, lead, DX ? n0 : kb * kBK, DX ? kb * kBK : n0);
+          if (++s == kPairStages) { s = 0; ph ^= 1u; }
+        }
+      }
+      // every copy has landed and every commit to this CTA's barriers has
+      // arrived before the pair may exit
+      for (int i = 0; i < kPairStages; ++i) {
+        mbar_wait(smem_u32(&empty[s]), ph ^ 1u, p.e.wait_ns, ok ? p.e.err : nullptr, 0x502);
+        if (++s == kPairStages) { s = 0; ph ^= 1u; }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // -------------------------------------------------------- MMA issuer
+    if (lane == 0 && rank == 0) {
+      int s = 0, b = 0;
+      uint32_t ph = 0, pa = 0;
+      bool ok = true;
+      for (int64_t t = cluster; t < tiles && ok; t += clusters) {
+        if (!mbar_wait(smem_u32(&acc_empty[b]), pa ^ 1u, p.e.wait_ns, p.e.err, 0x503)) {
+          *abort_flag = 1;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + 256u * (uint32_t)b;
+        for (int kb = 0; kb < p.KB; ++kb) {
+          if (!mbar_wait(smem_u32(&full[s]), ph, p.e.wait_ns, p.e.err, 0x504)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t base = smem_u32(smem + s * kStage);
+          const uint64_t ad = sdesc(base, 16, 1024);
+          const uint64_t bd = DX ? sdesc(base + kHalf, kHalf, 1024) : sdesc(base + kHalf, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 32; ++kk)
+            umma_i8<2>(d, ad + 2 * kk, bd + (DX ? 256 : 2) * kk, kIdesc, (kb | kk) ? 1u : 0u);
+          umma_commit_pair(smem_u32(&empty[s]));
+          if (++s == kPairStages) { s = 0; ph ^= 1u; }
+        }
+        if (ok) umma_commit_pair(smem_u32(&acc_full[b]));
+        if (++b == 2) { b = 0; pa ^= 1u; }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------- epilogue
+    const int quad = warp & 3;
+    const uint32_t buf = smem_u32(outbuf + quad * 2 * kOutBuf);
+    int b = 0, nbuf = 0;
+    uint32_t pa = 0;
+    for (int64_t t = cluster; t < tiles; t += clusters) {
+      int tm, tn;
+      pair_tile(t, p.tiles_m, p.tiles_n, tm, tn);
+      const int64_t row = (int64_t)tm * 256 + 128 * (int)rank + 32 * quad + lane;
+      const int64_t n0 = (int64_t)tn * 256;
+      const float sx = row < p.e.R ? __ldg(p.e.xs + row) : 0.0f;
+      uint64_t u[RT / 2];
+#pragma unroll
+      for (int j = 0; j < RT / 2; ++j) {
+        const float* T = p.e.T + row * p.e.r;
+        u[j] = pack2(row < p.e.R && 2 * j < p.e.r ? __ldg(T + 2 * j) : 0.0f,
+                     row < p.e.R && 2 * j + 1 < p.e.r ? __ldg(T + 2 * j + 1) : 0.0f);
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_full[b]), pa, p.e.wait_ns, p.e.err, 0x505))) {
+        *abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      const int chunks = (int)min((int64_t)8, (p.e.N - n0 + 31) / 32);
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        uint32_t acc[32];
+        tmem_ld_32x32b_x32(tmem + ((uint32_t)(quad * 32) << 16) + 256u * (uint32_t)b + 32u * (uint32_t)c,
+                           acc);
+        tmem_ld_wait();
+        if (c + 1 == chunks) {  // the accumulator may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_remote(at_rank(smem_u32(&acc_empty[b]), 0));
+        }
+        const int64_t n = n0 + 32 * c;
+        const float* L = p.e.L + n * RT;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          uint64_t d = 0;
+#pragma unroll
+          for (int q = 0; q < RT / 4; ++q) {
+            uint64_t l0, l1;
+            asm volatile("ld.global.nc.v2.u64 {%0, %1}, [%2];" : "=l"(l0), "=l"(l1) : "l"(L + j * RT + 4 * q));
+            d = fma2(u[2 * q], l0, d);
+            d = fma2(u[2 * q + 1], l1, d);
+          }
+          float v = __fmul_rn((float)(int)acc[j], sx);
+          if (!DX) v = __fmul_rn(v, n + j < p.e.N ? __ldg(p.e.ws + n + j) : 0.0f);
+          acc[j] = __float_as_uint(__fadd_rn(v, sum2(d)));
+        }
+        if (p.e.tma_out) {
+          constexpr bool kWide = sizeof(OUT) == 4;  // 32 or 64 columns fill 128 bytes
+          if (kWide || (c & 1) == 0) {  // a new buffer: its last store has been read
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            __syncwarp();
+          }
+          const uint32_t line = buf + (uint32_t)(nbuf * kOutBuf) + (uint32_t)lane * 128;
+          if (kWide) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              st_shared_v4(line + (uint32_t)((q ^ (lane & 7)) << 4), acc[4 * q], acc[4 * q + 1],
+                           acc[4 * q + 2], acc[4 * q + 3]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = pack_bf16x2(__uint_as_float(acc[8 * q + 2 * i]), __uint_as_float(acc[8 * q + 2 * i + 1]));
+              st_shared_v4(line + (uint32_t)(((4 * (c & 1) + q) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+            }
+          }
+          if (kWide || (c & 1) == 1 || c + 1 == chunks) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && row < p.e.R) {
+              tma_store_2d(&tm_out, buf + (uint32_t)(nbuf * kOutBuf),
+                           (int32_t)(n0 + (kWide ? 32 * c : 64 * (c >> 1))),
+                           (int32_t)(row));
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            nbuf ^= 1;
+          }
+        } else if (row < p.e.R) {
+          OUT* o = (OUT*)p.e.out + row * p.e.N + n;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (n + j < p.e.N) o[j] = from_f32<OUT>(__uint_as_float(acc[j]));
+        }
+      }
+      if (++b == 2) { b = 0; pa ^= 1u; }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+// The adapter factor as the pair kernel reads it: [Npad x RT], s L, zeros
+// outside.
+template <bool DX>
+__global__ void __launch_bounds__(256)
+    pack_kernel(const float* __restrict__ L, int64_t N, int64_t Npad, int r, int RT, float s,
+                float* __restrict__ out) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= Npad * RT) return;
+  // consecutive threads along n for [r x N], along j for [N x r]
+  const int64_t n = DX ? e % Npad : e / RT;
+  const int j = DX ? (int)(e / Npad) : (int)(e % RT);
+  const float v = n < N && j < r ? s * L[DX ? (int64_t)j * N + n : n * r + j] : 0.0f;
+  out[n * RT + j] = v;
+}
+
+// ---------------------------------------------------------- stream kernel
+
+template <int BN>
+struct StreamCfg {
+  static constexpr int kTok = BN * kBK;
+  static constexpr int kStage = kHalf + kTok;
+  static constexpr int kStages = BN <= 16 ? 11 : BN <= 32 ? 10 : BN <= 64 ? 8 : 6;
+  static constexpr int kCols = BN < 32 ? 32 : BN;  // TMEM columns of one accumulator
+  static constexpr int kSmem = 1024 + kStages * kStage + 512;
+  static_assert(kSmem <= 227 * 1024 && kSmem > 114 * 1024, "one CTA per SM");
+};
+constexpr int kStreamThreads = 192;  // producer, MMA issuer, four epilogue warps
+
+struct StreamArgs {
+  Epi e;
+  int32_t KB, tok_tiles;
+  int64_t tiles;
+  int32_t shared;       // deal out K steps (tiles may be shared by CTAs), else whole tiles
+  int32_t* part;        // [tiles][BN][128] sums of tiles that several CTAs share (zeroed)
+  uint32_t* tickets;    // [tiles] K steps added so far (zeroed)
+};
+
+// Units (K steps, tile after tile) [lo, hi) of this CTA.
+__device__ __forceinline__ void stream_range(const StreamArgs& p, int64_t& lo, int64_t& hi) {
+  const int64_t n = p.shared ? p.tiles * p.KB : p.tiles, one = p.shared ? 1 : p.KB;
+  lo = n * blockIdx.x / gridDim.x * one;
+  hi = n * (blockIdx.x + 1) / gridDim.x * one;
+}
+
+// Whether `ok` holds for all four epilogue warps.
+__device__ __forceinline__ bool all_epilogue(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred.aligned q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+
+template <bool DX, int BN, int RT>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    stream_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                  const StreamArgs p) {
+  using C = StreamCfg<BN>;
+  constexpr uint32_t kIdesc = idesc_i8(128, BN, DX, false);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint64_t* bars = (uint64_t*)(smem + C::kStages * C::kStage);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + C::kStages;
+  uint64_t* acc_full = bars + 2 * C::kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  volatile uint32_t* tmem_slot = (volatile uint32_t*)(acc_empty + 2);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  volatile uint32_t* last_flag = tmem_slot + 2;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t lo, hi;
+  stream_range(p, lo, hi);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&acc_full[b]), 1);
+      mbar_init(smem_u32(&acc_empty[b]), 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tm_x);
+    prefetch_tensormap(&tm_w);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32((const void*)tmem_slot), 2 * C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      // The weight does not depend on the launch before this one, the codes
+      // of the activations do: the first stages' weight tiles are on their
+      // way while that launch still runs.
+      const int64_t ahead = min(hi, lo + C::kStages);
+      auto load = [&](int64_t u, int slot, bool w, bool x) {
+        const int64_t tile = u / p.KB;
+        const int kb = (int)(u - tile * p.KB);
+        const int m0 = (int)(tile / p.tok_tiles) * 128, t0 = (int)(tile % p.tok_tiles) * BN;
+        const uint32_t fb = smem_u32(&full[slot]), dst = smem_u32(smem + slot * C::kStage);
+        if (w) {
+          mbar_arrive_expect_tx(fb, C::kStage);
+          tma_load_2d(dst, &tm_w, fb, DX ? m0 : kb * kBK, DX ? kb * kBK : m0);
+        }
+        if (x) tma_load_2d(dst + kHalf, &tm_x, fb, kb * kBK, t0);
+      };
+      for (int64_t u = lo; u < ahead; ++u) load(u, (int)(u - lo), true, false);
+      griddep_wait();
+      for (int64_t u = lo; u < hi; ++u) {
+        if (u < ahead) {
+          load(u, s, false, true);
+        } else {
+          if (*abort_flag || !mbar_wait(smem_u32(&empty[s]), ph ^ 1u, p.e.wait_ns, p.e.err, 0x601)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          load(u, s, true, true);
+        }
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
+      }
+      // copies in flight land before the CTA exits (the MMA has waited for
+      // them all unless something gave up)
+      if (!ok) {
+        for (int i = 0; i < C::kStages; ++i) {
+          mbar_wait(smem_u32(&full[s]), ph ^ 1u, p.e.wait_ns, nullptr, 0);
+          if (++s == C::kStages) { s = 0; ph ^= 1u; }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int s = 0, b = 0;
+      uint32_t ph = 0, pa = 0;
+      bool ok = true;
+      for (int64_t u = lo; u < hi && ok;) {
+        const int64_t end = min(hi, (u / p.KB + 1) * p.KB);  // this tile's run
+        if (!mbar_wait(smem_u32(&acc_empty[b]), pa ^ 1u, p.e.wait_ns, p.e.err, 0x602)) {
+          *abort_flag = 1;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(C::kCols * b);
+        for (bool first = true; u < end; ++u, first = false) {
+          if (!mbar_wait(smem_u32(&full[s]), ph, p.e.wait_ns, p.e.err, 0x603)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t base = smem_u32(smem + s * C::kStage);
+          const uint64_t ad = DX ? sdesc(base, kHalf, 1024) : sdesc(base, 16, 1024);
+          const uint64_t bd = sdesc(base + kHalf, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 32; ++kk)
+            umma_i8<1>(d, ad + (DX ? 256 : 2) * kk, bd + 2 * kk, kIdesc, (!first || kk) ? 1u : 0u);
+          umma_commit(smem_u32(&empty[s]));
+          if (++s == C::kStages) { s = 0; ph ^= 1u; }
+        }
+        if (ok) umma_commit(smem_u32(&acc_full[b]));
+        if (++b == 2) { b = 0; pa ^= 1u; }
+      }
+    }
+    __syncwarp();
+  } else {
+    // epilogue: lane = output n, TMEM column = token
+    const int quad = warp & 3;
+    griddep_wait();
+    int b = 0;
+    uint32_t pa = 0;
+    for (int64_t u = lo; u < hi;) {
+      const int64_t tile = u / p.KB, end = min(hi, (tile + 1) * p.KB);
+      const int steps = (int)(end - u);
+      u = end;
+      const int64_t n = (tile / p.tok_tiles) * 128 + 32 * quad + lane;
+      const int64_t t0 = (tile % p.tok_tiles) * BN;
+      const int toks = (int)min((int64_t)BN, p.e.R - t0);
+      // one answer for all four warps, which meet at barriers below
+      if (!all_epilogue(mbar_wait(smem_u32(&acc_full[b]), pa, p.e.wait_ns, p.e.err, 0x604))) {
+        *abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      const bool whole = steps == p.KB;
+      int32_t* part = p.part + (tile * BN) * 128 + 32 * quad + lane;
+      const uint32_t acc0 = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(C::kCols * b);
+      bool finish = whole;
+      if (!whole) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < toks; c0 += 32) {
+          uint32_t acc[32];
+          tmem_ld_32x32b_x32(acc0 + (uint32_t)c0, acc);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (c0 + j < toks) atomicAdd(part + (c0 + j) * 128, (int)acc[j]);
+        }
+        __threadfence();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (warp == 2 && lane == 0)
+          *last_flag = atomicAdd(p.tickets + tile, (uint32_t)steps) + (uint32_t)steps == (uint32_t)p.KB;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        finish = *last_flag != 0;
+        __threadfence();
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // all have read the flag
+      }
+      if (finish) {
+        float l[RT];
+        float sw = 1.0f;
+        const bool in = n < p.e.N;
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+          l[j] = in && j < p.e.r ? p.e.s * __ldg(p.e.L + (DX ? (int64_t)j * p.e.N + n : n * p.e.r + j)) : 0.0f;
+        if (!DX && in) sw = __ldg(p.e.ws + n);
+#pragma unroll 1
+        for (int c0 = 0; c0 < toks; c0 += 32) {
+          uint32_t acc[32];
+          if (whole) {
+            tmem_ld_32x32b_x32(acc0 + (uint32_t)c0, acc);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[j] = c0 + j < toks ? (uint32_t)__ldcg(part + (c0 + j) * 128) : 0u;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int64_t t = t0 + c0 + j;
+            if (c0 + j < toks && in) {
+              float d = 0.0f;
+#pragma unroll
+              for (int q = 0; q < RT; ++q)
+                if (q < p.e.r) d = fmaf(l[q], __ldg(p.e.T + t * p.e.r + q), d);
+              float v = __fmul_rn((float)(int)acc[j], __ldg(p.e.xs + t));
+              if (!DX) v = __fmul_rn(v, sw);
+              v = __fadd_rn(v, d);
+              if (p.e.bf16) ((__nv_bfloat16*)p.e.out)[t * p.e.N + n] = __float2bfloat16_rn(v);
+              else ((float*)p.e.out)[t * p.e.N + n] = v;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&acc_empty[b]));
+      if (++b == 2) { b = 0; pa ^= 1u; }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * C::kCols);
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+using EncodeTiled = PFN_cuTensorMapEncodeTiled_v12000;
+
+EncodeTiled encode_fn() {
+  static const EncodeTiled fn = [] {
+    cudaDriverEntryPointQueryResult q;
+    void* f = nullptr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (EncodeTiled)f;
+  }();
+  return fn;
+}
+
+// Row-major [rows x cols] of esize-byte elements, rows `stride` bytes apart,
+// boxes of [br x bc], 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t cols, uint64_t rows,
+              uint64_t stride, uint32_t bc, uint32_t br) {
+  EncodeTiled enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {stride};
+  cuuint32_t box[2] = {bc, br};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMaxDevices = 64;
+
+int sm_count() {
+  static std::atomic<int> count[kMaxDevices];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return 148;
+  n = count[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+    count[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Once per kernel and device: the attribute belongs to the device's context.
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, std::atomic<bool>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kMaxDevices && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < kMaxDevices) done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Plan {
+  bool pair;
+  int bn;          // stream: token tile
+  int64_t tiles;   // stream: tiles;  pair: tiles of 256 x 256
+  int ctas;
+  bool shared;     // stream: some tile is shared between CTAs
+};
+
+// Pair or stream, and how the latter's work is dealt out, by cost in K steps
+// of one SM (512 cycles: what the products of a 128 x 256 half tile take, and
+// also what the 32 KB of a 128 x 128 stream step take from L2).  The pair
+// kernel pays whole rounds of tiles over the CTA pairs and the last tile's
+// epilogue; the stream kernel pays whole rounds of tiles over the SMs, or, with
+// tiles shared, an equal run of steps and the meeting of the partial sums, which
+// grows with the token tile.
+Plan plan_for(int64_t R, int64_t N, int64_t K) {
+  const int64_t sms = sm_count(), KB = up(K, kBK);
+  Plan p;
+  p.bn = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128;
+  const int64_t pair_tiles = up(R, 256) * up(N, 256), tiles = up(R, p.bn) * up(N, 128);
+  const int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
+  const int64_t cost_pair = up(pair_tiles, pairs) * KB + 10;
+  const int64_t cost_whole = up(tiles, sms) * KB + 5;
+  const int64_t cost_shared = up(tiles * KB, sms) + 4 + p.bn / 8;
+  p.shared = cost_shared < cost_whole;
+  p.pair = R > 128 && cost_pair < (p.shared ? cost_shared : cost_whole);
+  if (p.pair) {
+    p.tiles = pair_tiles;
+    p.ctas = (int)(2 * (pair_tiles < pairs ? pair_tiles : pairs));
+    p.shared = false;
+    return p;
+  }
+  p.tiles = tiles;
+  // shared: runs of at least four steps, so that a CTA's start is paid for
+  int64_t ctas = p.shared ? (tiles * KB / 4 > tiles ? tiles * KB / 4 : tiles) : tiles;
+  if (ctas > sms) ctas = sms;
+  p.ctas = (int)ctas;
+  return p;
+}
+
+size_t pair_pack_bytes(int64_t N, int r) {
+  return align_up((size_t)up(N, 256) * 256 * (size_t)rank_pad(r) * 4, 256);
+}
+size_t stream_part_bytes(const Plan& p) { return !p.shared ? 0 : align_up((size_t)p.tiles * (size_t)p.bn * 128 * 4, 256); }
+size_t stream_ticket_bytes(const Plan& p) { return !p.shared ? 0 : align_up((size_t)p.tiles * 4, 256); }
+
+template <bool DX, typename OUT, int RT>
+cudaError_t go_pair(const Plan& pl, const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& o,
+                    const PairArgs& a, cudaStream_t st) {
+  static std::atomic<bool> done[kMaxDevices];
+  cudaError_t e = allow_smem(pair_kernel<DX, OUT, RT>, kPairSmem, done);
+  if (e != cudaSuccess) return e;
+  pair_kernel<DX, OUT, RT><<<pl.ctas, kPairThreads, kPairSmem, st>>>(x, w, o, a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+template <bool DX, int BN, int RT>
+cudaError_t go_stream(const Plan& pl, const CUtensorMap& x, const CUtensorMap& w, const StreamArgs& a,
+                      cudaStream_t st) {
+  static std::atomic<bool> done[kMaxDevices];
+  auto kern = stream_kernel<DX, BN, RT>;
+  cudaError_t e = allow_smem(kern, StreamCfg<BN>::kSmem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)pl.ctas);
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = StreamCfg<BN>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, x, w, a);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool DX, typename OUT, int RT>
+cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& base, int64_t K, void* ws,
+               cudaStream_t st) {
+  Epi e = base;
+  CUtensorMap mx, mw, mo;
+  const int64_t xp = int8_pitch(K), wp = int8_pitch(c.I);
+  if (!make_map(&mw, c.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)wp, (uint64_t)c.O, (uint64_t)wp, 128,
+                128) ||
+      !make_map(&mx, xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)xp, (uint64_t)c.R, (uint64_t)xp, 128,
+                pl.pair ? 128 : (uint32_t)pl.bn))
+    return cudaErrorInvalidValue;
+  if (pl.pair) {
+    float* pk = (float*)ws;
+    const int64_t Npad = up(e.N, 256) * 256;
+    pack_kernel<DX><<<(unsigned)up(Npad * RT, 256), 256, 0, st>>>(e.L, e.N, Npad, e.r, RT, e.s, pk);
+    count_launch();
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    e.L = pk;
+    e.tma_out = ((uintptr_t)c.out % 16 == 0 && (e.N * sizeof(OUT)) % 16 == 0) ? 1 : 0;
+    if (e.tma_out &&
+        !make_map(&mo, c.out, sizeof(OUT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                  (uint64_t)e.N, (uint64_t)c.R, (uint64_t)e.N * sizeof(OUT), 128 / sizeof(OUT), 32))
+      return cudaErrorInvalidValue;
+    if (!e.tma_out) mo = mx;  // not used
+    PairArgs a;
+    a.e = e;
+    a.KB = (int32_t)up(K, kBK);
+    a.tiles_m = (int32_t)up(c.R, 256);
+    a.tiles_n = (int32_t)up(e.N, 256);
+    return go_pair<DX, OUT, RT>(pl, mx, mw, mo, a, st);
+  }
+  constexpr int SRT = RT <= 16 ? 16 : 64;
+  StreamArgs a;
+  a.e = e;
+  a.KB = (int32_t)up(K, kBK);
+  a.tok_tiles = (int32_t)up(c.R, pl.bn);
+  a.tiles = pl.tiles;
+  a.shared = pl.shared ? 1 : 0;
+  a.part = (int32_t*)ws;
+  a.tickets = (uint32_t*)((char*)ws + stream_part_bytes(pl));
+  switch (pl.bn) {
+    case 16: return go_stream<DX, 16, SRT>(pl, mx, mw, a, st);
+    case 32: return go_stream<DX, 32, SRT>(pl, mx, mw, a, st);
+    case 64: return go_stream<DX, 64, SRT>(pl, mx, mw, a, st);
+    default: return go_stream<DX, 128, SRT>(pl, mx, mw, a, st);
+  }
+}
+
+template <bool DX, typename OUT>
+cudaError_t go_rank(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& e, int64_t K, void* ws,
+                    cudaStream_t st) {
+  switch (rank_pad(c.r)) {
+    case 8: return go<DX, OUT, 8>(pl, c, xq, e, K, ws, st);
+    case 16: return go<DX, OUT, 16>(pl, c, xq, e, K, ws, st);
+    case 32: return go<DX, OUT, 32>(pl, c, xq, e, K, ws, st);
+    default: return go<DX, OUT, 64>(pl, c, xq, e, K, ws, st);
+  }
+}
+
+}  // namespace
+
+size_t int8_tc_ws(bool dx, int64_t R, int64_t O, int64_t I, int32_t r) {
+  if (R == 0) return 0;
+  const Plan p = plan_for(R, dx ? I : O, dx ? O : I);
+  return p.pair ? pair_pack_bytes(dx ? I : O, r) : stream_part_bytes(p) + stream_ticket_bytes(p);
+}
+
+size_t int8_tc_zeroed(bool dx, int64_t R, int64_t O, int64_t I) {
+  if (R == 0) return 0;
+  const Plan p = plan_for(R, dx ? I : O, dx ? O : I);
+  return p.pair ? 0 : stream_part_bytes(p) + stream_ticket_bytes(p);
+}
+
+cudaError_t launch_int8_tc(const Int8Call& c, const int8_t* xq, const float* xs, void* ws, uint32_t* hdr,
+                           cudaStream_t st) {
+  const int64_t K = c.dx ? c.O : c.I;
+  const Plan pl = plan_for(c.R, c.dx ? c.I : c.O, K);
+  Epi e;
+  e.R = c.R;
+  e.N = c.dx ? c.I : c.O;
+  e.xs = xs;
+  e.ws = c.dx ? nullptr : c.wscale;
+  e.T = c.T;
+  e.L = c.L;
+  e.r = c.r;
+  e.s = c.s;
+  e.out = c.out;
+  e.tma_out = 0;
+  e.bf16 = c.bf16 ? 1 : 0;
+  e.err = hdr;
+  e.wait_ns = kWaitLimitNs;
+  if (c.dx)
+    return c.bf16 ? go_rank<true, __nv_bfloat16>(pl, c, xq, e, K, ws, st)
+                  : go_rank<true, float>(pl, c, xq, e, K, ws, st);
+  return c.bf16 ? go_rank<false, __nv_bfloat16>(pl, c, xq, e, K, ws, st)
+                : go_rank<false, float>(pl, c, xq, e, K, ws, st);
+}
+
+}  // namespace qlora
