@@ -21,51 +21,218 @@ namespace {
 constexpr int kThreads = 256;
 
 // Largest of non-negative values by their bits, so that a NaN wins over all.
-__device__ __forceinline__ uint32_t block_max_bits(uint32_t x) {
-  __shared__ uint32_t buf[32];
+// buf: two rows of 32 words, used in turn (one barrier a call).
+__device__ __forceinline__ uint32_t block_max_bits(uint32_t x, uint32_t* buf) {
   x = __reduce_max_sync(0xffffffffu, x);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (lane == 0) buf[warp] = x;
+  const int lane = threadIdx.x & 31, warps = (int)(blockDim.x >> 5);
+  if (lane == 0) buf[threadIdx.x >> 5] = x;
   __syncthreads();
-  x = buf[0];
-  for (int w = 1; w < (int)(blockDim.x >> 5); ++w) x = max(x, buf[w]);
-  return x;
+  return __reduce_max_sync(0xffffffffu, lane < warps ? buf[lane] : 0u);
 }
 
-__device__ __forceinline__ int8_t code_of(float x, float s) {
-  if (s == 0.0f) return 0;
-  const float q = rintf(__fdiv_rn(x, s));
-  return (int8_t)(int)fminf(fmaxf(q, -127.0f), 127.0f);
+// Scale of a row whose largest magnitude has these bits; NaN where the row
+// holds a NaN or Inf.
+__device__ __forceinline__ float row_scale(uint32_t top) {
+  return top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(top), 127.0f);
 }
 
-// One CTA per row of P [R x K] (times the column factors f, where given):
-// codes [R x pitch] with zeros in the padding, and the row's scale.  hdr:
-// raise the non-finite flag; otherwise a row with a NaN or Inf gets a NaN
-// scale (and with it a row of NaN outputs).
+// Code of x as the low byte of the result: rint(fl(x / s)).  The product with
+// the reciprocal is within 2^-15 of the quotient (at most 127 in magnitude,
+// two roundings), so it rounds to the same integer unless it lies that close
+// to a half; only then (and for scales whose reciprocal is not a normal
+// number: inv is NaN) is the division done.  Adding 1.5 2^23 rounds to the
+// nearest integer, ties to even, and leaves it in the low bits.
+__device__ __forceinline__ uint32_t code_of(float x, float s, float inv) {
+  const float y = __fmul_rn(x, inv);
+  float t = __fadd_rn(y, 12582912.0f);
+  if (!(fabsf(__fsub_rn(y, __fsub_rn(t, 12582912.0f))) < 0.49995f)) {
+    const float q = s > 0.0f ? fminf(fmaxf(__fdiv_rn(x, s), -127.0f), 127.0f) : 0.0f;
+    t = __fadd_rn(q, 12582912.0f);
+  }
+  return __float_as_uint(t) & 255u;
+}
+__device__ __forceinline__ float reciprocal(float s) {
+  return s >= 1e-37f ? __fdiv_rn(1.0f, s) : __uint_as_float(0x7fc00000u);
+}
+
+struct RowsArgs {
+  const void* P;       // [R x K]
+  int64_t R, K, pitch;
+  const float* f;      // [K] column factors, nullable
+  int8_t* codes;       // [R x pitch], zeros in the padding
+  float* scale;        // [R]
+  uint32_t* hdr;       // non-finite flag, nullable
+  uint4* zero;         // nzero 16-byte words to clear (for the kernel after)
+  int64_t nzero;
+};
+
+__device__ __forceinline__ void clear_part(const RowsArgs& a) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < a.nzero;
+       i += (int64_t)gridDim.x * blockDim.x)
+    a.zero[i] = make_uint4(0, 0, 0, 0);
+}
+
+// 16 bytes of activations as floats (8 bf16 or 4 fp32).
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    rows_kernel(const T* __restrict__ P, int64_t K, int64_t pitch, const float* __restrict__ f,
-                int8_t* __restrict__ codes, float* __restrict__ scale, uint32_t* __restrict__ hdr) {
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  __device__ static void open(uint4 v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  __device__ static void open(uint4 v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x);
+    x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z);
+    x[3] = __uint_as_float(v.w);
+  }
+};
+
+// Rows that take 16-byte accesses (K a multiple of 16, P aligned): a thread
+// keeps its NV vectors of the row in registers between the maximum and the
+// codes, so the row is read once; its column factors stay in registers over
+// all the rows the CTA takes, and the next row is on its way while this one
+// is reduced.
+template <typename T, int NV, bool FACTOR>
+__global__ void __launch_bounds__(512) rows_kernel(const RowsArgs a) {
+  constexpr int N = Vec<T>::N;
+  __shared__ uint32_t buf[2][32];
+  const int64_t nvec = a.K / N;
+  float f[FACTOR ? NV * N : 1];
+  if (FACTOR) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t v = threadIdx.x + (int64_t)i * blockDim.x;
+#pragma unroll
+      for (int j = 0; j < N; ++j) f[i * N + j] = v < nvec ? __ldg(a.f + v * N + j) : 0.0f;
+    }
+  }
+  uint4 next[NV];
+  auto load = [&](int64_t row) {
+    const uint4* x = reinterpret_cast<const uint4*>((const T*)a.P + row * a.K);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t v = threadIdx.x + (int64_t)i * blockDim.x;
+      next[i] = v < nvec ? __ldg(x + v) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  int64_t row = blockIdx.x;
+  if (row < a.R) load(row);
+  clear_part(a);
+  for (int k = 0; row < a.R; k ^= 1) {
+    uint4 cur[NV];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      cur[i] = next[i];
+      float x[N];
+      Vec<T>::open(cur[i], x);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        top = max(top, __float_as_uint(fabsf(FACTOR ? __fmul_rn(x[j], f[i * N + j]) : x[j])));
+    }
+    const int64_t now = row;
+    row += gridDim.x;
+    if (row < a.R) load(row);
+    top = block_max_bits(top, buf[k]);
+    const float s = row_scale(top);
+    const float inv = reciprocal(s);
+    if (threadIdx.x == 0) {
+      a.scale[now] = s;
+      if (a.hdr && top >= 0x7f800000u) atomicOr(a.hdr + 2, 1u);
+    }
+    uint32_t* q = reinterpret_cast<uint32_t*>(a.codes + now * a.pitch);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t v = threadIdx.x + (int64_t)i * blockDim.x;
+      float x[N];
+      uint32_t c[N / 4];
+      Vec<T>::open(cur[i], x);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint32_t b = code_of(FACTOR ? __fmul_rn(x[j], f[i * N + j]) : x[j], s, inv);
+        c[j / 4] = j % 4 == 0 ? b : c[j / 4] | (b << (8 * (j % 4)));
+      }
+      if (v < nvec) {
+        if (N == 8) reinterpret_cast<uint2*>(q)[v] = make_uint2(c[0], c[N / 4 - 1]);
+        else q[v] = c[0];
+      }
+    }
+  }
+}
+
+// Any other row: one CTA per row, read twice.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) rows_any_kernel(const RowsArgs a) {
+  __shared__ uint32_t buf[32];
+  clear_part(a);
   const int64_t row = blockIdx.x;
-  const T* x = P + row * K;
+  if (row >= a.R) return;
+  const T* x = (const T*)a.P + row * a.K;
   uint32_t top = 0;
-  for (int64_t k = threadIdx.x; k < K; k += kThreads) {
-    const float v = f ? __fmul_rn(to_f32(x[k]), f[k]) : to_f32(x[k]);
+  for (int64_t k = threadIdx.x; k < a.K; k += kThreads) {
+    const float v = a.f ? __fmul_rn(to_f32(x[k]), a.f[k]) : to_f32(x[k]);
     top = max(top, __float_as_uint(fabsf(v)));
   }
-  top = block_max_bits(top);
-  const bool bad = top >= 0x7f800000u;
-  const float s = bad ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(top), 127.0f);
+  top = block_max_bits(top, buf);
+  const float s = row_scale(top);
+  const float inv = reciprocal(s);
   if (threadIdx.x == 0) {
-    scale[row] = s;
-    if (bad && hdr) atomicOr(hdr + 2, 1u);
+    a.scale[row] = s;
+    if (a.hdr && top >= 0x7f800000u) atomicOr(a.hdr + 2, 1u);
   }
-  int8_t* q = codes + row * pitch;
-  for (int64_t k = threadIdx.x; k < pitch; k += kThreads) {
-    int8_t c = 0;
-    if (k < K && !bad) c = code_of(f ? __fmul_rn(to_f32(x[k]), f[k]) : to_f32(x[k]), s);
-    q[k] = c;
+  int8_t* q = a.codes + row * a.pitch;
+  for (int64_t k = threadIdx.x; k < a.pitch; k += kThreads) {
+    uint32_t c = 0;
+    if (k < a.K) c = code_of(a.f ? __fmul_rn(to_f32(x[k]), a.f[k]) : to_f32(x[k]), s, inv);
+    q[k] = (int8_t)c;
   }
+}
+
+template <typename T, int NV>
+void rows_go(const RowsArgs& a, unsigned ctas, int threads, cudaStream_t st) {
+  if (a.f) rows_kernel<T, NV, true><<<ctas, threads, 0, st>>>(a);
+  else rows_kernel<T, NV, false><<<ctas, threads, 0, st>>>(a);
+}
+
+// Vector rows: up to 512 threads and 8 vectors a thread (fp32 weights of
+// 16384 columns, bf16 activations of 32768).  The CTAs are as many as the SMs
+// hold at once, each over rows in turn; few rows get extra CTAs for clearing.
+template <typename T>
+cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
+  constexpr int N = Vec<T>::N;
+  const int64_t nvec = a.K / N;
+  const unsigned clear = (unsigned)(a.nzero > 0 ? (a.nzero + 2047) / 2048 < 592 ? (a.nzero + 2047) / 2048 : 592 : 0);
+  if (a.K % 16 == 0 && a.K > 0 && (uintptr_t)a.P % 16 == 0 && (uintptr_t)a.codes % 8 == 0 &&
+      nvec <= 8 * 512) {
+    int nv = 1;
+    while (nv < 4 && nvec > (int64_t)nv * 256) nv *= 2;
+    if (nvec > (int64_t)nv * 512) nv = 8;
+    const int threads = (int)((nvec + nv - 1) / nv + 31) / 32 * 32;
+    const int64_t most = (int64_t)148 * (1536 / threads);
+    unsigned ctas = (unsigned)(a.R < most ? a.R : most);
+    if (ctas < clear) ctas = clear;
+    switch (nv) {
+      case 1: rows_go<T, 1>(a, ctas, threads, st); break;
+      case 2: rows_go<T, 2>(a, ctas, threads, st); break;
+      case 4: rows_go<T, 4>(a, ctas, threads, st); break;
+      default: rows_go<T, 8>(a, ctas, threads, st); break;
+    }
+  } else {
+    rows_any_kernel<T><<<(unsigned)(a.R > clear ? a.R : clear), kThreads, 0, st>>>(a);
+  }
+  count_launch();
+  return cudaGetLastError();
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -94,10 +261,15 @@ cudaError_t launch_int8_quantize(const float* W, int64_t O, int64_t I, int8_t* c
                                  void* ws, cudaStream_t st) {
   cudaError_t e = cudaMemsetAsync(ws, 0, kWsHeader, st);
   if (e != cudaSuccess || O == 0) return e;
-  rows_kernel<float><<<(unsigned)O, kThreads, 0, st>>>(W, I, int8_pitch(I), nullptr, codes, scale,
-                                                       (uint32_t*)ws);
-  count_launch();
-  return cudaGetLastError();
+  RowsArgs a = {};
+  a.P = W;
+  a.R = O;
+  a.K = I;
+  a.pitch = int8_pitch(I);
+  a.codes = codes;
+  a.scale = scale;
+  a.hdr = (uint32_t*)ws;
+  return launch_rows<float>(a, st);
 }
 
 cudaError_t launch_int8_dequantize(const int8_t* codes, const float* scale, int64_t O, int64_t I,
@@ -117,22 +289,17 @@ size_t int8_ws(bool dx, int64_t R, int64_t O, int64_t I, int32_t r) {
 cudaError_t launch_int8_rows(const Int8Call& c, void* ws, cudaStream_t st) {
   const int64_t K = c.dx ? c.O : c.I;
   const Layout l = layout(c.R, K);
-  float* xs = (float*)((char*)ws + l.scale);
-  int8_t* xq = (int8_t*)ws + l.codes;
-  const size_t zero = int8_tc_zeroed(c.dx, c.R, c.O, c.I);
-  if (zero) {
-    const cudaError_t e = cudaMemsetAsync((char*)ws + l.total, 0, zero, st);
-    if (e != cudaSuccess) return e;
-  }
-  const float* f = c.dx ? c.wscale : nullptr;
-  if (c.bf16)
-    rows_kernel<__nv_bfloat16><<<(unsigned)c.R, kThreads, 0, st>>>((const __nv_bfloat16*)c.P, K,
-                                                                  int8_pitch(K), f, xq, xs, nullptr);
-  else
-    rows_kernel<float><<<(unsigned)c.R, kThreads, 0, st>>>((const float*)c.P, K, int8_pitch(K), f, xq,
-                                                           xs, nullptr);
-  count_launch();
-  return cudaGetLastError();
+  RowsArgs a = {};
+  a.P = c.P;
+  a.R = c.R;
+  a.K = K;
+  a.pitch = int8_pitch(K);
+  a.f = c.dx ? c.wscale : nullptr;
+  a.codes = (int8_t*)ws + l.codes;
+  a.scale = (float*)((char*)ws + l.scale);
+  a.zero = (uint4*)((char*)ws + l.total);  // 256-byte aligned, a multiple of 256 bytes
+  a.nzero = (int64_t)(int8_tc_zeroed(c.dx, c.R, c.O, c.I) / 16);
+  return c.bf16 ? launch_rows<__nv_bfloat16>(a, st) : launch_rows<float>(a, st);
 }
 
 cudaError_t launch_int8_product(const Int8Call& c, void* ws, uint32_t* hdr, cudaStream_t st) {

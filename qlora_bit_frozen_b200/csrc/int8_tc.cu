@@ -49,6 +49,7 @@ struct Epi {
   const float* ws;   // [N] channel scale (forward), else null
   const float* T;    // [R x r] U or V
   const float* L;    // packed [Npad x RT] s L (pair) or the factor itself (stream)
+  const float* wpad; // pair: channel scales [Npad] (1 in the input gradient)
   int32_t r;
   float s;
   void* out;
@@ -138,6 +139,27 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
                : "memory");
 }
 
+// Untiled bulk copy (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// Whether `ok` holds for all THREADS epilogue threads (barrier 1).
+template <int THREADS>
+__device__ __forceinline__ bool all_epilogue(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred.aligned q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "n"(THREADS)
+      : "memory");
+  return r != 0;
+}
+
 // Two fp32 FMAs in one instruction.
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
@@ -155,12 +177,14 @@ __host__ __device__ constexpr int rank_pad(int r) { return r <= 8 ? 8 : r <= 16 
 
 // ------------------------------------------------------------ pair kernel
 
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 5;
 constexpr int kStage = 2 * kHalf;  // A and B half tiles of one CTA
-constexpr int kOutBuf = 4096;      // 32 rows x 128 bytes
-constexpr int kPairSmem = 1024 + kPairStages * kStage + 8 * kOutBuf + 256;
+constexpr int kEpiWarps = 8;       // two to a TMEM lane quarter, 64 columns in turn
+constexpr int kOutBuf = 4096;      // staged output of a warp: 32 rows x 128 bytes
+constexpr int kFactor = 32768;     // staged adapter factor: 256 outputs (128 above rank 32)
+constexpr int kPairSmem = 1024 + kPairStages * kStage + kEpiWarps * kOutBuf + kFactor + 1024 + 256;
 static_assert(kPairSmem <= 227 * 1024, "one CTA per SM");
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 128 + 32 * kEpiWarps;
 
 struct PairArgs {
   Epi e;
@@ -187,12 +211,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* outbuf = smem + kPairStages * kStage;
-  uint64_t* bars = (uint64_t*)(outbuf + 8 * kOutBuf);
+  float* factor = (float*)(outbuf + kEpiWarps * kOutBuf);
+  float* wscale = factor + kFactor / 4;
+  uint64_t* bars = (uint64_t*)(wscale + 256);
   uint64_t* full = bars;                      // leader: both CTAs' loads landed
   uint64_t* empty = bars + kPairStages;       // both: the step's products are done
   uint64_t* acc_full = bars + 2 * kPairStages;
-  uint64_t* acc_empty = acc_full + 2;         // leader: drained by 4 warps of each CTA
-  volatile uint32_t* tmem_slot = (volatile uint32_t*)(acc_empty + 2);
+  uint64_t* acc_empty = acc_full + 2;         // leader: drained by the epilogue warps of both
+  uint64_t* fac_full = acc_empty + 2;         // the factor (and the scales) of a tile landed
+  volatile uint32_t* tmem_slot = (volatile uint32_t*)(fac_full + 1);
   volatile uint32_t* abort_flag = tmem_slot + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -207,8 +234,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&acc_full[b]), 1);
-      mbar_init(smem_u32(&acc_empty[b]), 8);
+      mbar_init(smem_u32(&acc_empty[b]), 2 * kEpiWarps);
     }
+    mbar_init(smem_u32(fac_full), 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_x);
@@ -297,64 +325,114 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncwarp();
   } else if (warp >= 4) {
     // ---------------------------------------------------------- epilogue
-    const int quad = warp & 3;
-    const uint32_t buf = smem_u32(outbuf + quad * 2 * kOutBuf);
-    int b = 0, nbuf = 0;
-    uint32_t pa = 0;
+    // Lane = token.  Warp `half` of a quarter takes 64-column runs half, half
+    // + 2.  The adapter factor and the channel scales of a tile sit in shared
+    // memory (a bulk copy issued as soon as the tile before has done with
+    // them), read as broadcasts.
+    const int ew = warp - 4, quad = warp & 3, half = ew >> 2;
+    const uint32_t buf = smem_u32(outbuf + ew * kOutBuf);
+    constexpr int kLoads = RT > 32 ? 2 : 1;           // copies a tile's factor takes
+    constexpr uint32_t kFacBytes = 256 / kLoads * RT * 4;
+    auto fetch = [&](int64_t t, int part) {           // one thread
+      int tm, tn;
+      pair_tile(t, p.tiles_m, p.tiles_n, tm, tn);
+      const uint32_t fb = smem_u32(fac_full);
+      mbar_arrive_expect_tx(fb, kFacBytes + (part == 0 ? 1024u : 0u));
+      bulk_load(smem_u32(factor), p.e.L + ((int64_t)tn * 256 + part * (256 / kLoads)) * RT, kFacBytes, fb);
+      if (part == 0) bulk_load(smem_u32(wscale), p.e.wpad + (int64_t)tn * 256, 1024u, fb);
+    };
+    if (ew == 0 && lane == 0 && cluster < tiles) fetch(cluster, 0);
+    int b = 0;
+    uint32_t pa = 0, pf = 0;
+    bool ok = true;
     for (int64_t t = cluster; t < tiles; t += clusters) {
       int tm, tn;
       pair_tile(t, p.tiles_m, p.tiles_n, tm, tn);
       const int64_t row = (int64_t)tm * 256 + 128 * (int)rank + 32 * quad + lane;
       const int64_t n0 = (int64_t)tn * 256;
-      const float sx = row < p.e.R ? __ldg(p.e.xs + row) : 0.0f;
+      const bool in = row < p.e.R;
+      const float sx = in ? __ldg(p.e.xs + row) : 0.0f;
       uint64_t u[RT / 2];
+      const float* T = p.e.T + row * p.e.r;
+      if (in && (p.e.r & 3) == 0 && ((uintptr_t)p.e.T & 15) == 0) {
 #pragma unroll
-      for (int j = 0; j < RT / 2; ++j) {
-        const float* T = p.e.T + row * p.e.r;
-        u[j] = pack2(row < p.e.R && 2 * j < p.e.r ? __ldg(T + 2 * j) : 0.0f,
-                     row < p.e.R && 2 * j + 1 < p.e.r ? __ldg(T + 2 * j + 1) : 0.0f);
+        for (int j = 0; j < RT / 4; ++j) {
+          const float4 v = 4 * j < p.e.r ? __ldg(reinterpret_cast<const float4*>(T) + j)
+                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          u[2 * j] = pack2(v.x, v.y);
+          u[2 * j + 1] = pack2(v.z, v.w);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < RT / 2; ++j)
+          u[j] = pack2(in && 2 * j < p.e.r ? __ldg(T + 2 * j) : 0.0f,
+                       in && 2 * j + 1 < p.e.r ? __ldg(T + 2 * j + 1) : 0.0f);
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_full[b]), pa, p.e.wait_ns, p.e.err, 0x505))) {
+      // one answer for all warps, which meet at barriers below
+      ok = mbar_wait(smem_u32(fac_full), pf, p.e.wait_ns, p.e.err, 0x505) && ok;
+      ok = mbar_wait(smem_u32(&acc_full[b]), pa, p.e.wait_ns, p.e.err, 0x506) && ok;
+      pf ^= 1u;
+      if (!all_epilogue<32 * kEpiWarps>(ok)) {
         *abort_flag = 1;
         break;
       }
       tc_fence_after();
-      const int chunks = (int)min((int64_t)8, (p.e.N - n0 + 31) / 32);
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        uint32_t acc[32];
-        tmem_ld_32x32b_x32(tmem + ((uint32_t)(quad * 32) << 16) + 256u * (uint32_t)b + 32u * (uint32_t)c,
-                           acc);
-        tmem_ld_wait();
-        if (c + 1 == chunks) {  // the accumulator may be overwritten
-          tc_fence_before();
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && kLoads == 2) {
+          ok = mbar_wait(smem_u32(fac_full), pf, p.e.wait_ns, p.e.err, 0x507);
+          pf ^= 1u;
+        }
+        const int c64 = 2 * h + half;
+        const int64_t n = n0 + 64 * c64;
+        const bool some = n < p.e.N;  // the same for the whole warp
+        if (some) {
+          if (p.e.tma_out && lane == 0)  // the buffer's last store has been read
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           __syncwarp();
-          if (lane == 0) arrive_remote(at_rank(smem_u32(&acc_empty[b]), 0));
         }
-        const int64_t n = n0 + 32 * c;
-        const float* L = p.e.L + n * RT;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          uint64_t d = 0;
-#pragma unroll
-          for (int q = 0; q < RT / 4; ++q) {
-            uint64_t l0, l1;
-            asm volatile("ld.global.nc.v2.u64 {%0, %1}, [%2];" : "=l"(l0), "=l"(l1) : "l"(L + j * RT + 4 * q));
-            d = fma2(u[2 * q], l0, d);
-            d = fma2(u[2 * q + 1], l1, d);
-          }
-          float v = __fmul_rn((float)(int)acc[j], sx);
-          if (!DX) v = __fmul_rn(v, n + j < p.e.N ? __ldg(p.e.ws + n + j) : 0.0f);
-          acc[j] = __float_as_uint(__fadd_rn(v, sum2(d)));
-        }
-        if (p.e.tma_out) {
-          constexpr bool kWide = sizeof(OUT) == 4;  // 32 or 64 columns fill 128 bytes
-          if (kWide || (c & 1) == 0) {  // a new buffer: its last store has been read
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t acc[32];
+          tmem_ld_32x32b_x32(tmem + ((uint32_t)(quad * 32) << 16) + 256u * (uint32_t)b +
+                                 (uint32_t)(64 * c64 + 32 * c),
+                             acc);
+          tmem_ld_wait();
+          if (h == 1 && c == 1) {  // the accumulator may be overwritten
+            tc_fence_before();
             __syncwarp();
+            if (lane == 0) arrive_remote(at_rank(smem_u32(&acc_empty[b]), 0));
           }
-          const uint32_t line = buf + (uint32_t)(nbuf * kOutBuf) + (uint32_t)lane * 128;
-          if (kWide) {
+          if (!some) continue;
+          const int col = 64 * c64 + 32 * c;
+          const float* f = factor + (kLoads == 2 ? col - 128 * h : col) * RT;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            uint64_t d = 0;
+#pragma unroll
+            for (int q = 0; q < RT / 4; ++q) {
+              const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(f + j * RT + 4 * q);
+              d = fma2(u[2 * q], l.x, d);
+              d = fma2(u[2 * q + 1], l.y, d);
+            }
+            const float v = __fmul_rn(__fmul_rn((float)(int)acc[j], sx), wscale[col + j]);
+            acc[j] = __float_as_uint(__fadd_rn(v, sum2(d)));
+          }
+          if (!p.e.tma_out) {
+            if (in) {
+              OUT* o = (OUT*)p.e.out + row * p.e.N + n + 32 * c;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (n + 32 * c + j < p.e.N) o[j] = from_f32<OUT>(__uint_as_float(acc[j]));
+            }
+            continue;
+          }
+          const uint32_t line = buf + (uint32_t)lane * 128;
+          if (sizeof(OUT) == 4) {  // 32 columns fill the buffer
+            if (c == 1) {
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              __syncwarp();
+            }
 #pragma unroll
             for (int q = 0; q < 8; ++q)
               st_shared_v4(line + (uint32_t)((q ^ (lane & 7)) << 4), acc[4 * q], acc[4 * q + 1],
@@ -366,25 +444,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 w[i] = pack_bf16x2(__uint_as_float(acc[8 * q + 2 * i]), __uint_as_float(acc[8 * q + 2 * i + 1]));
-              st_shared_v4(line + (uint32_t)(((4 * (c & 1) + q) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+              st_shared_v4(line + (uint32_t)(((4 * c + q) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
             }
           }
-          if (kWide || (c & 1) == 1 || c + 1 == chunks) {
+          if (sizeof(OUT) == 4 || c == 1) {
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && row < p.e.R) {
-              tma_store_2d(&tm_out, buf + (uint32_t)(nbuf * kOutBuf),
-                           (int32_t)(n0 + (kWide ? 32 * c : 64 * (c >> 1))),
-                           (int32_t)(row));
+            if (lane == 0) {
+              const int64_t x = sizeof(OUT) == 4 ? n + 32 * c : n;
+              if (in && x < p.e.N) tma_store_2d(&tm_out, buf, (int32_t)x, (int32_t)row);
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
-            nbuf ^= 1;
           }
-        } else if (row < p.e.R) {
-          OUT* o = (OUT*)p.e.out + row * p.e.N + n;
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (n + j < p.e.N) o[j] = from_f32<OUT>(__uint_as_float(acc[j]));
+        }
+        if (h == 1 || kLoads == 2) {
+          // all epilogue warps have read the factor: fetch the next one
+          asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+          if (ew == 0 && lane == 0) {
+            if (h == 0) fetch(t, 1);
+            else if (t + clusters < tiles) fetch(t + clusters, 0);
+          }
         }
       }
       if (++b == 2) { b = 0; pa ^= 1u; }
@@ -400,13 +479,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-// The adapter factor as the pair kernel reads it: [Npad x RT], s L, zeros
-// outside.
+// The adapter factor and the channel scales as the pair kernel reads them:
+// [Npad x RT], s L, zeros outside; [Npad], 1 where there is no channel scale.
 template <bool DX>
 __global__ void __launch_bounds__(256)
-    pack_kernel(const float* __restrict__ L, int64_t N, int64_t Npad, int r, int RT, float s,
-                float* __restrict__ out) {
+    pack_kernel(const float* __restrict__ L, const float* __restrict__ ws, int64_t N, int64_t Npad, int r,
+                int RT, float s, float* __restrict__ out, float* __restrict__ wpad) {
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e < Npad) wpad[e] = !DX && e < N ? ws[e] : 1.0f;
   if (e >= Npad * RT) return;
   // consecutive threads along n for [r x N], along j for [N x r]
   const int64_t n = DX ? e % Npad : e / RT;
@@ -417,13 +497,14 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------- stream kernel
 
-template <int BN>
+template <int BN, int RT>
 struct StreamCfg {
   static constexpr int kTok = BN * kBK;
   static constexpr int kStage = kHalf + kTok;
-  static constexpr int kStages = BN <= 16 ? 11 : BN <= 32 ? 10 : BN <= 64 ? 8 : 6;
+  static constexpr int kStages = BN <= 16 ? 11 : BN <= 32 ? 10 : BN <= 64 ? (RT > 16 ? 7 : 8) : RT > 16 ? 5 : 6;
   static constexpr int kCols = BN < 32 ? 32 : BN;  // TMEM columns of one accumulator
-  static constexpr int kSmem = 1024 + kStages * kStage + 512;
+  static constexpr int kSide = BN * (RT + 1) * 4;  // the tokens' rows of T and scales
+  static constexpr int kSmem = 1024 + kStages * kStage + kSide + 512;
   static_assert(kSmem <= 227 * 1024 && kSmem > 114 * 1024, "one CTA per SM");
 };
 constexpr int kStreamThreads = 192;  // producer, MMA issuer, four epilogue warps
@@ -444,27 +525,17 @@ __device__ __forceinline__ void stream_range(const StreamArgs& p, int64_t& lo, i
   hi = n * (blockIdx.x + 1) / gridDim.x * one;
 }
 
-// Whether `ok` holds for all four epilogue warps.
-__device__ __forceinline__ bool all_epilogue(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred.aligned q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)ok)
-      : "memory");
-  return r != 0;
-}
 
 template <bool DX, int BN, int RT>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     stream_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                   const StreamArgs p) {
-  using C = StreamCfg<BN>;
+  using C = StreamCfg<BN, RT>;
   constexpr uint32_t kIdesc = idesc_i8(128, BN, DX, false);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint64_t* bars = (uint64_t*)(smem + C::kStages * C::kStage);
+  float* side = (float*)(smem + C::kStages * C::kStage);  // [BN][RT] T, then [BN] scales
+  uint64_t* bars = (uint64_t*)(side + BN * (RT + 1));
   uint64_t* full = bars;
   uint64_t* empty = bars + C::kStages;
   uint64_t* acc_full = bars + 2 * C::kStages;
@@ -581,19 +652,36 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     __syncwarp();
   } else {
     // epilogue: lane = output n, TMEM column = token
-    const int quad = warp & 3;
+    const int quad = warp & 3, et = (int)threadIdx.x - 64;
     griddep_wait();
     int b = 0;
     uint32_t pa = 0;
+    int64_t staged = -1;  // token tile whose T and scales are in shared memory
     for (int64_t u = lo; u < hi;) {
       const int64_t tile = u / p.KB, end = min(hi, (tile + 1) * p.KB);
       const int steps = (int)(end - u);
       u = end;
       const int64_t n = (tile / p.tok_tiles) * 128 + 32 * quad + lane;
-      const int64_t t0 = (tile % p.tok_tiles) * BN;
+      const int64_t tt = tile % p.tok_tiles, t0 = tt * BN;
       const int toks = (int)min((int64_t)BN, p.e.R - t0);
+      // this tile's side inputs, while its products run
+      float l[RT];
+      const bool in = n < p.e.N;
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+        l[j] = in && j < p.e.r ? __ldg(p.e.L + (DX ? (int64_t)j * p.e.N + n : n * p.e.r + j)) : 0.0f;
+      const float sw = !DX && in ? __ldg(p.e.ws + n) : 1.0f;
+      if (tt != staged) {
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // the last tile's are read
+        for (int e = et; e < toks * RT; e += 128) {
+          const int t = e / RT, j = e % RT;
+          side[e] = j < p.e.r ? p.e.s * __ldg(p.e.T + (t0 + t) * p.e.r + j) : 0.0f;
+        }
+        for (int e = et; e < toks; e += 128) side[BN * RT + e] = __ldg(p.e.xs + t0 + e);
+        staged = tt;
+      }
       // one answer for all four warps, which meet at barriers below
-      if (!all_epilogue(mbar_wait(smem_u32(&acc_full[b]), pa, p.e.wait_ns, p.e.err, 0x604))) {
+      if (!all_epilogue<128>(mbar_wait(smem_u32(&acc_full[b]), pa, p.e.wait_ns, p.e.err, 0x604))) {
         *abort_flag = 1;
         break;
       }
@@ -622,13 +710,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         asm volatile("bar.sync 1, 128;" ::: "memory");  // all have read the flag
       }
       if (finish) {
-        float l[RT];
-        float sw = 1.0f;
-        const bool in = n < p.e.N;
-#pragma unroll
-        for (int j = 0; j < RT; ++j)
-          l[j] = in && j < p.e.r ? p.e.s * __ldg(p.e.L + (DX ? (int64_t)j * p.e.N + n : n * p.e.r + j)) : 0.0f;
-        if (!DX && in) sw = __ldg(p.e.ws + n);
 #pragma unroll 1
         for (int c0 = 0; c0 < toks; c0 += 32) {
           uint32_t acc[32];
@@ -641,17 +722,24 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           }
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const int64_t t = t0 + c0 + j;
-            if (c0 + j < toks && in) {
+            if (c0 + j < toks) {
+              const float* T = side + (c0 + j) * RT;
               float d = 0.0f;
 #pragma unroll
-              for (int q = 0; q < RT; ++q)
-                if (q < p.e.r) d = fmaf(l[q], __ldg(p.e.T + t * p.e.r + q), d);
-              float v = __fmul_rn((float)(int)acc[j], __ldg(p.e.xs + t));
-              if (!DX) v = __fmul_rn(v, sw);
-              v = __fadd_rn(v, d);
-              if (p.e.bf16) ((__nv_bfloat16*)p.e.out)[t * p.e.N + n] = __float2bfloat16_rn(v);
-              else ((float*)p.e.out)[t * p.e.N + n] = v;
+              for (int q = 0; q < RT; q += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(T + q);
+                d = fmaf(l[q], v.x, d);
+                d = fmaf(l[q + 1], v.y, d);
+                d = fmaf(l[q + 2], v.z, d);
+                d = fmaf(l[q + 3], v.w, d);
+              }
+              const float v =
+                  __fadd_rn(__fmul_rn(__fmul_rn((float)(int)acc[j], side[BN * RT + c0 + j]), sw), d);
+              const int64_t o = (t0 + c0 + j) * p.e.N + n;
+              if (in) {
+                if (p.e.bf16) ((__nv_bfloat16*)p.e.out)[o] = __float2bfloat16_rn(v);
+                else ((float*)p.e.out)[o] = v;
+              }
             }
           }
         }
@@ -770,7 +858,7 @@ Plan plan_for(int64_t R, int64_t N, int64_t K) {
 }
 
 size_t pair_pack_bytes(int64_t N, int r) {
-  return align_up((size_t)up(N, 256) * 256 * (size_t)rank_pad(r) * 4, 256);
+  return (size_t)up(N, 256) * 256 * ((size_t)rank_pad(r) + 1) * 4;
 }
 size_t stream_part_bytes(const Plan& p) { return !p.shared ? 0 : align_up((size_t)p.tiles * (size_t)p.bn * 128 * 4, 256); }
 size_t stream_ticket_bytes(const Plan& p) { return !p.shared ? 0 : align_up((size_t)p.tiles * 4, 256); }
@@ -791,12 +879,12 @@ cudaError_t go_stream(const Plan& pl, const CUtensorMap& x, const CUtensorMap& w
                       cudaStream_t st) {
   static std::atomic<bool> done[kMaxDevices];
   auto kern = stream_kernel<DX, BN, RT>;
-  cudaError_t e = allow_smem(kern, StreamCfg<BN>::kSmem, done);
+  cudaError_t e = allow_smem(kern, (StreamCfg<BN, RT>::kSmem), done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)pl.ctas);
   cfg.blockDim = dim3(kStreamThreads);
-  cfg.dynamicSmemBytes = StreamCfg<BN>::kSmem;
+  cfg.dynamicSmemBytes = (StreamCfg<BN, RT>::kSmem);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -822,11 +910,14 @@ cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& b
   if (pl.pair) {
     float* pk = (float*)ws;
     const int64_t Npad = up(e.N, 256) * 256;
-    pack_kernel<DX><<<(unsigned)up(Npad * RT, 256), 256, 0, st>>>(e.L, e.N, Npad, e.r, RT, e.s, pk);
+    float* wpad = pk + Npad * RT;
+    pack_kernel<DX><<<(unsigned)up(Npad * RT, 256), 256, 0, st>>>(e.L, e.ws, e.N, Npad, e.r, RT, e.s, pk,
+                                                                  wpad);
     count_launch();
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     e.L = pk;
+    e.wpad = wpad;
     e.tma_out = ((uintptr_t)c.out % 16 == 0 && (e.N * sizeof(OUT)) % 16 == 0) ? 1 : 0;
     if (e.tma_out &&
         !make_map(&mo, c.out, sizeof(OUT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,

@@ -91,6 +91,26 @@ def test_quantize_refuses_nonfinite_weights(bad):
     assert e.value.status == 4
 
 
+@pytest.mark.parametrize("I", [16, 4096, 4112, 8192, 16384, 16400, 40000])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_near_ties(I, dtype):
+    """Quotients on and beside halves, where the rounding decides, for every way a row is read."""
+    X = (torch.randint(-254, 255, (64, I), device="cuda", generator=gen(7)).float() / 2).to(dtype)
+    X[:, 0] = 127
+    X[::2] *= 0.3
+    if dtype == F32:
+        X *= 1 + torch.randint(-2, 3, X.shape, device="cuda", generator=gen(8)) * 2.0 ** -23
+    w = q.QuantizedWeight(q.FMT_INT8, 16, I, I, 0, 8, torch.zeros(16, I, dtype=torch.int8, device="cuda"),
+                          scale=torch.ones(16, device="cuda"))
+    w.codes.fill_diagonal_(1)
+    for k in (0, I - 16):  # 16 columns of codes at either end, read through a unit weight
+        w.codes.zero_()
+        w.codes[torch.arange(16), torch.arange(k, k + 16)] = 1
+        Y, _ = q.qlora_linear_fwd(w, X, torch.zeros(1, I, device="cuda"), torch.zeros(16, 1, device="cuda"), 1.0)
+        n, s = rows64(X.float())
+        assert torch.equal(Y, (n[:, k:k + 16].float() * s[:, None]).to(dtype))
+
+
 def test_quantize_of_nothing():
     assert q.qlora_quantize_int8(torch.empty(0, 5, device="cuda")).scale.numel() == 0
     assert torch.equal(q.qlora_quantize_int8(torch.empty(3, 0, device="cuda")).scale, torch.zeros(3, device="cuda"))
