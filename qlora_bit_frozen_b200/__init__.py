@@ -401,6 +401,7 @@ class OptimTensors:
             c.param, c.param_type = p.data_ptr(), _DTYPES[p.dtype]
         if self.params is not None:
             self._refuse_overlap()
+        self._norm_ws = None  # workspace bytes of qlora_grad_norm
 
     def _refuse_overlap(self):
         spans = []
@@ -435,7 +436,9 @@ def step_control(device="cuda") -> torch.Tensor:
 
 
 def qlora_grad_norm_workspace_bytes(tensors: OptimTensors) -> int:
-    return int(_ffi.load().qlora_grad_norm_workspace_bytes(tensors._c, len(tensors.grads)))
+    if tensors._norm_ws is None:
+        tensors._norm_ws = int(_ffi.load().qlora_grad_norm_workspace_bytes(tensors._c, len(tensors.grads)))
+    return tensors._norm_ws
 
 
 def qlora_grad_norm(tensors: OptimTensors, max_norm: float, control: torch.Tensor,

@@ -5,9 +5,13 @@
 // so hundreds of tensors, each far too small to fill the GPU alone).
 //
 // The tensors' descriptors travel as kernel parameters (no device table, no
-// copy, and a captured graph holds them); each warp finds the tensor of its
-// 256-value block by bisection over the descriptors' first blocks.
+// copy, and a captured graph holds them).  The 256-value blocks of all
+// tensors are dealt out to the CTAs in equal contiguous runs; a warp finds
+// the tensor of its first block by bisection over the descriptors' first
+// blocks and walks on from there.
 #include <math.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
@@ -39,7 +43,8 @@ struct Batch {
   uint32_t blocks;
   Desc d[CAP];
 };
-constexpr int kFew = 60;
+constexpr int kFew = 60;    // below 4 KB of parameters
+constexpr int kSome = 240;
 constexpr int kMany = 500;
 static_assert(sizeof(Batch<kMany>) + 128 <= 32764, "kernel parameter limit");
 
@@ -52,6 +57,15 @@ __device__ __forceinline__ int find(const Batch<CAP>& b, uint32_t blk) {
     else hi = mid - 1;
   }
   return lo;
+}
+
+// The run of blocks of this CTA, which its warps take in turn.
+struct Run {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ Run my_run(uint32_t blocks) {
+  return {(uint32_t)((uint64_t)blocks * blockIdx.x / gridDim.x),
+          (uint32_t)((uint64_t)blocks * (blockIdx.x + 1) / gridDim.x)};
 }
 
 // A lane's eight values of a block: two runs of four where the arrays take
@@ -197,76 +211,125 @@ __device__ __forceinline__ float warp_max_bits(float x) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
 }
 
+// Byte j of w as a float, exactly: the byte becomes the low mantissa bits of
+// 2^23.  Signed bytes come with their top bit flipped (128 more).
+__device__ __forceinline__ float byte_f32(uint32_t w, int j, float bias) {
+  return __fsub_rn(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | (uint32_t)j)), bias);
+}
+
+// rint(top sqrt(u)) with the sign of `sign` for u in [0, 1] (a little above by
+// rounding), as the definition has it: the square root and the product rounded
+// to nearest.  The approximate root is within 2^-22, so the product is within
+// 2^-13 (top <= 255) and rounds to the same integer unless it lies that close
+// to a half; only then is the exact root taken.  1.5 2^23 added rounds to
+// nearest even and leaves the two's complement integer in the low bits.
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t code_of(float u, float top, float sign) {
+  float a;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(a) : "f"(u));
+  float y = __fmul_rn(a, top);
+  float t = __fadd_rn(y, 12582912.0f);
+  if (!(fabsf(__fsub_rn(y, __fsub_rn(t, 12582912.0f))) < 0.4998f)) {
+    y = __fmul_rn(__fsqrt_rn(u), top);
+    t = __fadd_rn(y, 12582912.0f);
+  }
+  const uint32_t k = __float_as_uint(t) & 255u;
+  return SIGNED && sign < 0.0f ? 0u - k : k;
+}
+
+// Four low bytes to a word.
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+template <int BITS>
+struct Block {  // a lane's share of a block, as loaded
+  float g[8], p[8];
+  float m[BITS == 32 ? 8 : 1], v[BITS == 32 ? 8 : 1];
+  uint32_t mw[2], vw[2];
+  float ms, vs;
+};
+
 template <int BITS, bool VEC>
-__device__ __forceinline__ void adamw_block(const Desc& d, int64_t blk, int lane, const AdamWArgs& a,
-                                            float scale, float step_size, float inv_rbc2) {
+__device__ __forceinline__ void load_block(const Desc& d, int64_t blk, int lane, Block<BITS>& b) {
   const int64_t at = blk * kBlock;
   const int left = d.n - at < kBlock ? (int)(d.n - at) : kBlock;
-  float g[8], p[8], m[8], v[8];
-  uint32_t mw[2], vw[2];
-  float ms = 0.0f, vs = 0.0f;
-  load_any<VEC>(d.g, d.gbf16, at, lane, left, g);
-  load_any<VEC>(d.p, d.pbf16, at, lane, left, p);
-  if (BITS == 32) {
-    load_f32<VEC>((const float*)d.m + at, lane, left, m);
-    load_f32<VEC>((const float*)d.v + at, lane, left, v);
+  load_any<VEC>(d.g, d.gbf16, at, lane, left, b.g);
+  load_any<VEC>(d.p, d.pbf16, at, lane, left, b.p);
+  if constexpr (BITS == 32) {
+    load_f32<VEC>((const float*)d.m + at, lane, left, b.m);
+    load_f32<VEC>((const float*)d.v + at, lane, left, b.v);
   } else {
-    load_codes<VEC>((const uint8_t*)d.m + at, lane, left, mw);
-    load_codes<VEC>((const uint8_t*)d.v + at, lane, left, vw);
-    ms = d.ms[blk];
-    vs = d.vs[blk];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float km = __fmul_rn((float)(int)(int8_t)(mw[j >> 2] >> (8 * (j & 3))), 1.0f / 127.0f);
-      const float kv = __fmul_rn((float)((vw[j >> 2] >> (8 * (j & 3))) & 255u), 1.0f / 255.0f);
-      m[j] = __fmul_rn(__fmul_rn(km, fabsf(km)), ms);
-      const float r = __fmul_rn(__fmul_rn(kv, kv), vs);
-      v[j] = __fmul_rn(r, r);
-    }
+    load_codes<VEC>((const uint8_t*)d.m + at, lane, left, b.mw);
+    load_codes<VEC>((const uint8_t*)d.v + at, lane, left, b.vw);
+    b.ms = d.ms[blk];
+    b.vs = d.vs[blk];
   }
+}
+
+template <int BITS, bool VEC>
+__device__ __forceinline__ void step_block(const Desc& d, int64_t blk, int lane, Block<BITS>& b,
+                                           const AdamWArgs& a, float scale, float step_size,
+                                           float inv_rbc2) {
+  const int64_t at = blk * kBlock;
+  const int left = d.n - at < kBlock ? (int)(d.n - at) : kBlock;
+  float m[8], r[8];
   float mmax = 0.0f, rmax = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float gj = __fmul_rn(g[j], scale);
-    m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(gj, a.omb1));
-    v[j] = __fadd_rn(__fmul_rn(v[j], a.b2), __fmul_rn(__fmul_rn(gj, gj), a.omb2));
-    const float r = __fsqrt_rn(v[j]);
-    const float step = __fdiv_rn(__fmul_rn(m[j], step_size), __fadd_rn(__fmul_rn(r, inv_rbc2), a.eps));
-    p[j] = __fsub_rn(__fmul_rn(p[j], a.decay), step);
-    if (BITS == 8) {
-      v[j] = r;  // what the codes hold
+    float v;
+    if constexpr (BITS == 32) {
+      m[j] = b.m[j];
+      v = b.v[j];
+    } else {
+      const float km = __fmul_rn(byte_f32(b.mw[j >> 2] ^ 0x80808080u, j & 3, 8388736.0f), 1.0f / 127.0f);
+      const float kv = __fmul_rn(byte_f32(b.vw[j >> 2], j & 3, 8388608.0f), 1.0f / 255.0f);
+      m[j] = __fmul_rn(__fmul_rn(km, fabsf(km)), b.ms);
+      const float root = __fmul_rn(__fmul_rn(kv, kv), b.vs);
+      v = __fmul_rn(root, root);
+    }
+    const float g = __fmul_rn(b.g[j], scale);
+    m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(g, a.omb1));
+    v = __fadd_rn(__fmul_rn(v, a.b2), __fmul_rn(__fmul_rn(g, g), a.omb2));
+    r[j] = __fsqrt_rn(v);
+    const float step =
+        __fdiv_rn(__fmul_rn(m[j], step_size), __fadd_rn(__fmul_rn(r[j], inv_rbc2), a.eps));
+    b.p[j] = __fsub_rn(__fmul_rn(b.p[j], a.decay), step);
+    if constexpr (BITS == 32) {
+      b.v[j] = v;
+    } else {
       mmax = __uint_as_float(max(__float_as_uint(mmax), __float_as_uint(fabsf(m[j]))));
-      rmax = __uint_as_float(max(__float_as_uint(rmax), __float_as_uint(r)));
+      rmax = __uint_as_float(max(__float_as_uint(rmax), __float_as_uint(r[j])));
     }
   }
-  store_any<VEC>(d.p, d.pbf16, at, lane, left, p);
-  if (BITS == 32) {
+  store_any<VEC>(d.p, d.pbf16, at, lane, left, b.p);
+  if constexpr (BITS == 32) {
     store_f32<VEC>((float*)d.m + at, lane, left, m);
-    store_f32<VEC>((float*)d.v + at, lane, left, v);
-    return;
-  }
-  mmax = warp_max_bits(mmax);
-  rmax = warp_max_bits(rmax);
-  const float im = inverse_of(mmax), iv = inverse_of(rmax);
-  mw[0] = mw[1] = vw[0] = vw[1] = 0;
+    store_f32<VEC>((float*)d.v + at, lane, left, b.v);
+  } else {
+    mmax = warp_max_bits(mmax);
+    rmax = warp_max_bits(rmax);
+    const float im = inverse_of(mmax), iv = inverse_of(rmax);
+    uint32_t km[8], kv[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int k = __float2int_rn(__fmul_rn(__fsqrt_rn(__fmul_rn(fabsf(m[j]), im)), 127.0f));
-    int u = __float2int_rn(__fmul_rn(__fsqrt_rn(__fmul_rn(v[j], iv)), 255.0f));
-    if (u == 0 && v[j] > 0.0f && iv > 0.0f) u = 1;
-    mw[j >> 2] |= ((uint32_t)(m[j] < 0.0f ? -k : k) & 255u) << (8 * (j & 3));
-    vw[j >> 2] |= ((uint32_t)u & 255u) << (8 * (j & 3));
-  }
-  store_codes<VEC>((uint8_t*)d.m + at, lane, left, mw);
-  store_codes<VEC>((uint8_t*)d.v + at, lane, left, vw);
-  if (lane == 0) {
-    d.ms[blk] = mmax;
-    d.vs[blk] = rmax;
+    for (int j = 0; j < 8; ++j) {
+      km[j] = code_of<true>(__fmul_rn(fabsf(m[j]), im), 127.0f, m[j]);
+      kv[j] = code_of<false>(__fmul_rn(r[j], iv), 255.0f, 0.0f);
+      if (r[j] > 0.0f && iv > 0.0f) kv[j] = max(kv[j], 1u);
+    }
+    const uint32_t mw[2] = {pack4(km[0], km[1], km[2], km[3]), pack4(km[4], km[5], km[6], km[7])};
+    const uint32_t vw[2] = {pack4(kv[0], kv[1], kv[2], kv[3]), pack4(kv[4], kv[5], kv[6], kv[7])};
+    store_codes<VEC>((uint8_t*)d.m + at, lane, left, mw);
+    store_codes<VEC>((uint8_t*)d.v + at, lane, left, vw);
+    if (lane == 0) {
+      d.ms[blk] = mmax;
+      d.vs[blk] = rmax;
+    }
   }
 }
 
 template <int BITS, int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     adamw_kernel(const __grid_constant__ Batch<CAP> b, const AdamWArgs a) {
   __shared__ float terms[2];
   const int lane = threadIdx.x & 31;
@@ -279,11 +342,21 @@ __global__ void __launch_bounds__(kThreads)
     step_size = terms[0];
     inv_rbc2 = terms[1];
   }
-  const uint32_t warps = gridDim.x * (kThreads / 32);
-  for (uint32_t blk = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); blk < b.blocks; blk += warps) {
-    const Desc& d = b.d[find(b, blk)];
-    if (d.vec) adamw_block<BITS, true>(d, blk - d.first, lane, a, scale, step_size, inv_rbc2);
-    else adamw_block<BITS, false>(d, blk - d.first, lane, a, scale, step_size, inv_rbc2);
+  const Run run = my_run(b.blocks);
+  uint32_t blk = run.lo + (threadIdx.x >> 5);
+  if (blk >= run.hi) return;
+  int i = find(b, blk);
+  for (; blk < run.hi; blk += kThreads / 32) {
+    while (i + 1 < b.count && b.d[i + 1].first <= blk) ++i;
+    const Desc& d = b.d[i];
+    Block<BITS> x;
+    if (d.vec) {
+      load_block<BITS, true>(d, blk - d.first, lane, x);
+      step_block<BITS, true>(d, blk - d.first, lane, x, a, scale, step_size, inv_rbc2);
+    } else {
+      load_block<BITS, false>(d, blk - d.first, lane, x);
+      step_block<BITS, false>(d, blk - d.first, lane, x, a, scale, step_size, inv_rbc2);
+    }
   }
 }
 
@@ -295,17 +368,32 @@ __global__ void __launch_bounds__(kThreads)
     sumsq_kernel(const __grid_constant__ Batch<CAP> b, double* __restrict__ part) {
   __shared__ double sums[kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t warps = gridDim.x * (kThreads / 32);
+  if (threadIdx.x == 0) griddep_launch_dependents();  // the norm kernel waits for this grid
+  const Run run = my_run(b.blocks);
+  uint32_t blk = run.lo + warp;
+  int i = blk < run.hi ? find(b, blk) : 0;
   double acc = 0.0;
-  for (uint32_t blk = blockIdx.x * (kThreads / 32) + warp; blk < b.blocks; blk += warps) {
-    const Desc& d = b.d[find(b, blk)];
-    const int64_t at = (int64_t)(blk - d.first) * kBlock;
-    const int left = d.n - at < kBlock ? (int)(d.n - at) : kBlock;
-    float g[8];
-    if (d.vec) load_any<true>(d.g, d.gbf16, at, lane, left, g);
-    else load_any<false>(d.g, d.gbf16, at, lane, left, g);
+  // four blocks on their way at a time
+  while (blk < run.hi) {
+    float g[4][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc = fma((double)g[j], (double)g[j], acc);
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[k][j] = 0.0f;
+      if (blk < run.hi) {
+        while (i + 1 < b.count && b.d[i + 1].first <= blk) ++i;
+        const Desc& d = b.d[i];
+        const int64_t at = (int64_t)(blk - d.first) * kBlock;
+        const int left = d.n - at < kBlock ? (int)(d.n - at) : kBlock;
+        if (d.vec) load_any<true>(d.g, d.gbf16, at, lane, left, g[k]);
+        else load_any<false>(d.g, d.gbf16, at, lane, left, g[k]);
+      }
+      blk += kThreads / 32;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc = fma((double)g[k][j], (double)g[k][j], acc);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
@@ -322,6 +410,7 @@ __global__ void __launch_bounds__(kThreads)
     norm_kernel(const double* __restrict__ part, int32_t n, float max_norm, qlora_step_control* c) {
   __shared__ double sums[kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  griddep_wait();
   double acc = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) acc += part[i];
 #pragma unroll
@@ -344,16 +433,20 @@ __global__ void __launch_bounds__(kThreads)
 bool on(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 148;
+  static std::atomic<int> count[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  int n = count[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+    count[dev].store(n, std::memory_order_relaxed);
+  }
   return n;
 }
 
-constexpr int kCtasPerSm = 8;
+constexpr int kCtasPerSm = 4;  // one wave at up to 64 registers a thread
 
-// Calls f(batch) for the tensors from `i` on that fit one launch; returns
+// Fills the batch with the tensors from `i` on that fit one launch; returns
 // where the next one begins.
 template <int CAP>
 int32_t fill(Batch<CAP>& b, const qlora_tensor* t, int32_t count, int32_t i, int bits, bool grads_only) {
@@ -441,12 +534,23 @@ cudaError_t launch_grad_norm(const qlora_tensor* t, int32_t count, float max_nor
                              qlora_step_control* control, void* ws, cudaStream_t st) {
   double* part = (double*)ws;
   int32_t n = 0;
-  const cudaError_t e = count <= kFew ? sumsq_all<kFew>(t, count, part, &n, st)
-                                      : sumsq_all<kMany>(t, count, part, &n, st);
+  cudaError_t e = count <= kFew    ? sumsq_all<kFew>(t, count, part, &n, st)
+                  : count <= kSome ? sumsq_all<kSome>(t, count, part, &n, st)
+                                   : sumsq_all<kMany>(t, count, part, &n, st);
   if (e != cudaSuccess) return e;
-  norm_kernel<<<1, kThreads, 0, st>>>(part, n, max_norm, control);
+  // its launch overlaps the last sums; it waits for their grid itself
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = n > 0 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, norm_kernel, (const double*)part, n, max_norm, control);
   count_launch();
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_adamw(const qlora_tensor* t, int32_t count, int32_t bits, int64_t step, float lr,
@@ -464,7 +568,9 @@ cudaError_t launch_adamw(const qlora_tensor* t, int32_t count, int32_t bits, int
   a.b2d = beta2;
   a.control = control;
   if (!control) bias_terms(a.lr, a.b1d, a.b2d, step, &a.step_size, &a.inv_rbc2);
-  return count <= kFew ? adamw_all<kFew>(t, count, bits, a, st) : adamw_all<kMany>(t, count, bits, a, st);
+  return count <= kFew    ? adamw_all<kFew>(t, count, bits, a, st)
+         : count <= kSome ? adamw_all<kSome>(t, count, bits, a, st)
+                          : adamw_all<kMany>(t, count, bits, a, st);
 }
 
 }  // namespace qlora
