@@ -48,15 +48,13 @@ def _check(status: int, where: str):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 _HERE = contextlib.nullcontext()
@@ -70,7 +68,8 @@ def _on(dev):
 def _need(where: str, name: str, t: Optional[torch.Tensor], dev, shape=None, dtype=None):
     """Reject (before any launch) a tensor the kernels would misread: not on
     the weight's CUDA device, not dense, or of the wrong shape or dtype."""
-    if t is None:
+    if t is None or (t.is_cuda and t.device == dev and (dtype is None or t.dtype is dtype)
+                     and (shape is None or t.shape == shape) and t.is_contiguous()):
         return
     if not t.is_cuda or t.device != dev:
         raise ValueError(f"{where}: {name} must be a CUDA tensor on {dev}")
@@ -104,10 +103,9 @@ class QuantizedWeight:
     bias: Optional[torch.Tensor] = None
 
     def c_struct(self) -> qlora_weight:
-        return qlora_weight(self.fmt, self.O, self.I, self.block, self.group, self.bits,
-                            *(t.data_ptr() if t is not None and t.numel() > 0 else None
-                              for t in (self.codes, self.scale_codes, self.group_absmax, self.mean,
-                                        self.scale, self.bias)))
+        return qlora_weight(self.fmt, self.O, self.I, self.block, self.group, self.bits, _ptr(self.codes),
+                            _ptr(self.scale_codes), _ptr(self.group_absmax), _ptr(self.mean),
+                            _ptr(self.scale), _ptr(self.bias))
 
     _BUFFERS = ("codes", "scale_codes", "group_absmax", "mean", "scale", "bias")
 
@@ -505,8 +503,9 @@ def qlora_linear_fwd(w: QuantizedWeight, X: torch.Tensor, A: torch.Tensor, B: to
         Y = torch.empty((R, w.O), dtype=X.dtype, device=X.device)
     if U_out is None and want_u:
         U_out = torch.empty((R, r), dtype=torch.float32, device=X.device)
+    cw = ctypes.byref(w.c_struct())
     if ws is None:
-        ws = workspace(qlora_linear_workspace_bytes(w, R, r, OP_FWD, compute), X.device)
+        ws = workspace(lib.qlora_linear_workspace_bytes(cw, R, r, OP_FWD, compute), X.device)
     dev, f = w.codes.device, "qlora_linear_fwd"
     _need(f, "X", X, dev, (R, w.I))
     _need(f, "A", A, dev, (r, w.I), torch.float32)
@@ -514,9 +513,8 @@ def qlora_linear_fwd(w: QuantizedWeight, X: torch.Tensor, A: torch.Tensor, B: to
     _need(f, "Y", Y, dev, (R, w.O), X.dtype)
     _need(f, "U_out", U_out, dev, (R, r), torch.float32)
     _need(f, "ws", ws, dev)
-    cw = w.c_struct()
     with _on(dev):
-        st = lib.qlora_linear_fwd(ctypes.byref(cw), _ptr(X), R, _ptr(A), _ptr(B), r, float(alpha), compute,
+        st = lib.qlora_linear_fwd(cw, _ptr(X), R, _ptr(A), _ptr(B), r, float(alpha), compute,
                                   _ptr(Y), _ptr(U_out), _ptr(ws), ws.numel(), _stream(stream))
     _check(st, "qlora_linear_fwd")
     return Y, U_out
@@ -539,8 +537,9 @@ def qlora_linear_bwd(w: QuantizedWeight, X: Optional[torch.Tensor], dY: torch.Te
         dA = torch.empty((r, w.I), dtype=torch.float32, device=dev)
     if want_db and dB is None:
         dB = torch.empty((w.O, r), dtype=torch.float32, device=dev)
+    cw = ctypes.byref(w.c_struct())
     if ws is None:
-        ws = workspace(qlora_linear_workspace_bytes(w, R, r, OP_BWD, compute), dev)
+        ws = workspace(lib.qlora_linear_workspace_bytes(cw, R, r, OP_BWD, compute), dev)
     wd, f = w.codes.device, "qlora_linear_bwd"
     _need(f, "dY", dY, wd, (R, w.O))
     _need(f, "X", X, wd, (R, w.I), dY.dtype)
@@ -551,9 +550,8 @@ def qlora_linear_bwd(w: QuantizedWeight, X: Optional[torch.Tensor], dY: torch.Te
     _need(f, "dA", dA if want_da else None, wd, (r, w.I), torch.float32)
     _need(f, "dB", dB if want_db else None, wd, (w.O, r), torch.float32)
     _need(f, "ws", ws, wd)
-    cw = w.c_struct()
     with _on(wd):
-        st = lib.qlora_linear_bwd(ctypes.byref(cw), _ptr(X), _ptr(dY), R, _ptr(A), _ptr(B), r, float(alpha),
+        st = lib.qlora_linear_bwd(cw, _ptr(X), _ptr(dY), R, _ptr(A), _ptr(B), r, float(alpha),
                                   _ptr(U), compute, _ptr(dX if want_dx else None), _ptr(dA if want_da else None),
                                   _ptr(dB if want_db else None), _ptr(ws), ws.numel(), _stream(stream))
     _check(st, "qlora_linear_bwd")

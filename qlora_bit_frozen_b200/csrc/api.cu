@@ -247,9 +247,9 @@ Int8Layout int8_layout(const qlora_weight* w, int64_t R, int32_t r, bool bwd) {
   }
   off += red;
   L.split = off;
-  size_t sp = adapter_split_ws(w->I, r);
+  size_t sp = adapter_split_ws(w->I, r, 3);
   if (bwd) {
-    const size_t more[2] = {adapter_split_ws(w->O, r), adapter_split_ws(R, r)};
+    const size_t more[2] = {adapter_split_ws(w->O, r, 3), adapter_split_ws(R, r, 3)};
     for (size_t m : more)
       if (m > sp) sp = m;
   }
@@ -257,7 +257,7 @@ Int8Layout int8_layout(const qlora_weight* w, int64_t R, int32_t r, bool bwd) {
   L.red2 = off;
   if (bwd) off += coldot_ws(R, w->O, r);
   L.split2 = off;
-  if (bwd) off += adapter_split_ws(R, r);
+  if (bwd) off += adapter_split_ws(R, r, 3);
   L.rows = off;
   off += int8_ws(bwd, R, w->O, w->I, r);
   L.total = off;
@@ -286,14 +286,22 @@ Int8Call int8_call(const qlora_weight* w, bool dx, bool bf16, int64_t R, const v
 cudaError_t int8_fwd(const qlora_weight* w, const void* X, int64_t R, const float* A, const float* B,
                      int32_t r, float sc, bool bf16, void* Y, float* U_out, void* ws, cudaStream_t s) {
   const Int8Layout L = int8_layout(w, R, r, false);
-  unsigned* tickets = (unsigned*)((char*)ws + kWsHeader);
   float* U = U_out ? U_out : (float*)((char*)ws + L.u);
   const Int8Call c = int8_call(w, false, bf16, R, X, U, B, r, sc, Y);
-  cudaError_t e = launch_int8_rows(c, (char*)ws + L.rows, s);
+  const Int8Clear header = {ws, kWsZeroed};
+  void* rows = (char*)ws + L.rows;
+  if (R <= kInt8Few) {
+    Int8Few f = {};
+    f.F = A;
+    f.T = U;
+    return launch_int8_few(c, f, rows, header, (uint32_t*)ws, s);
+  }
+  cudaError_t e = launch_int8_rows(c, rows, header, s);
   if (e == cudaSuccess)
     e = launch_rowdot(X, bf16, R, w->I, A, false, r, U, s, nullptr, nullptr, 0, 0, 1.0f, nullptr, nullptr,
-                      (float*)((char*)ws + L.red), tickets, (uint16_t*)((char*)ws + L.split));
-  if (e == cudaSuccess) e = launch_int8_product(c, (char*)ws + L.rows, (uint32_t*)ws, s);
+                      (float*)((char*)ws + L.red), (unsigned*)((char*)ws + kWsHeader),
+                      (uint16_t*)((char*)ws + L.split), 3);
+  if (e == cudaSuccess) e = launch_int8_product(c, rows, (uint32_t*)ws, s);
   return e;
 }
 
@@ -307,11 +315,11 @@ cudaError_t adapter_grads(bool bf16, const void* X, int64_t I, const float* V, f
   cudaError_t e = cudaSuccess;
   if (dA && dB && bf16)
     e = launch_coldot_pair(X, I, V, false, dA, red, split, dY, O, U, true, dB, red2, split2, R, r, sc, s,
-                           tickets, &paired);
+                           tickets, &paired, 3);
   if (e == cudaSuccess && dA && !paired)
-    e = launch_coldot(X, bf16, R, I, V, r, sc, false, dA, red, s, tickets, split);
+    e = launch_coldot(X, bf16, R, I, V, r, sc, false, dA, red, s, tickets, split, 3);
   if (e == cudaSuccess && dB && !paired)
-    e = launch_coldot(dY, bf16, R, O, U, r, sc, true, dB, red, s, tickets, split);
+    e = launch_coldot(dY, bf16, R, O, U, r, sc, true, dB, red, s, tickets, split, 3);
   return e;
 }
 
@@ -321,27 +329,40 @@ cudaError_t int8_bwd(const qlora_weight* w, const void* X, const void* dY, int64
   const Int8Layout L = int8_layout(w, R, r, true);
   unsigned* tickets = (unsigned*)((char*)ws + kWsHeader);
   float* V = (float*)((char*)ws + L.v);
+  float* Uw = (float*)((char*)ws + L.u);
   float* red = (float*)((char*)ws + L.red);
   uint16_t* split = (uint16_t*)((char*)ws + L.split);
-  cudaError_t e = cudaSuccess;
-  if (R > 0 && (dX || dA))
+  void* rows = (char*)ws + L.rows;
+  const Int8Clear header = {ws, kWsZeroed};
+  const Int8Call c = int8_call(w, true, bf16, R, dY, V, A, r, sc, dX);
+  if (dX && R > 0 && R <= kInt8Few) {
+    Int8Few f = {};
+    f.F = B;
+    f.T = V;
+    f.X = X;
+    f.A = A;
+    f.U_new = dB && !U_in ? Uw : nullptr;
+    f.U = U_in ? U_in : Uw;
+    f.dA = dA;
+    f.dB = dB;
+    return launch_int8_few(c, f, rows, header, (uint32_t*)ws, s);
+  }
+  cudaError_t e;
+  if (dX && R > 0) e = launch_int8_rows(c, rows, header, s);
+  else e = cudaMemsetAsync(ws, 0, kWsZeroed, s);
+  if (e == cudaSuccess && R > 0 && (dX || dA))
     e = launch_rowdot(dY, bf16, R, w->O, B, true, r, V, s, nullptr, nullptr, 0, 0, 1.0f, nullptr,
-                      (float*)((char*)ws + L.bt), red, tickets, split);
+                      (float*)((char*)ws + L.bt), red, tickets, split, 3);
   const float* U = U_in;
   if (e == cudaSuccess && R > 0 && dB && !U) {
-    float* Uw = (float*)((char*)ws + L.u);
     e = launch_rowdot(X, bf16, R, w->I, A, false, r, Uw, s, nullptr, nullptr, 0, 0, 1.0f, nullptr, nullptr,
-                      red, tickets, split);
+                      red, tickets, split, 3);
     U = Uw;
   }
   if (e == cudaSuccess)
     e = adapter_grads(bf16, X, w->I, V, dA, dY, w->O, U, dB, R, r, sc, red, (char*)ws + L.red2, split,
                       (uint16_t*)((char*)ws + L.split2), tickets, s);
-  if (e == cudaSuccess && R > 0 && dX) {
-    const Int8Call c = int8_call(w, true, bf16, R, dY, V, A, r, sc, dX);
-    e = launch_int8_rows(c, (char*)ws + L.rows, s);
-    if (e == cudaSuccess) e = launch_int8_product(c, (char*)ws + L.rows, (uint32_t*)ws, s);
-  }
+  if (e == cudaSuccess && R > 0 && dX) e = launch_int8_product(c, rows, (uint32_t*)ws, s);
   return e;
 }
 
@@ -638,14 +659,14 @@ qlora_status qlora_linear_fwd(const qlora_weight* w, const void* X, int64_t R, c
   st = device_ready();
   if (st != QLORA_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
+  const float sc = alpha / (float)r;
+  if (int8 && R > 0)
+    return cuda_status(
+        int8_fwd(w, X, R, A, B, r, sc, compute == QLORA_COMPUTE_BF16, Y, U_out, ws, s));
   cudaError_t e = cudaMemsetAsync(ws, 0, kWsZeroed, s);
   if (e != cudaSuccess) return QLORA_ERR_CUDA;
   if (R == 0) return QLORA_OK;
   unsigned* tickets = (unsigned*)((char*)ws + kWsHeader);
-  const float sc = alpha / (float)r;
-  if (int8)
-    return cuda_status(
-        int8_fwd(w, X, R, A, B, r, sc, compute == QLORA_COMPUTE_BF16, Y, U_out, ws, s));
   float* red = (float*)((char*)ws + L.red);
   float* U = U_out ? U_out : (float*)((char*)ws + L.u);
   const WView v = view_of(w);
@@ -693,13 +714,13 @@ qlora_status qlora_linear_bwd(const qlora_weight* w, const void* X, const void* 
   st = device_ready();
   if (st != QLORA_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = cudaMemsetAsync(ws, 0, kWsZeroed, s);
-  if (e != cudaSuccess) return QLORA_ERR_CUDA;
-  unsigned* tickets = (unsigned*)((char*)ws + kWsHeader);
   const bool bf16 = compute == QLORA_COMPUTE_BF16;
   const float sc = alpha / (float)r;
   if (int8)
     return cuda_status(int8_bwd(w, X, dY, R, A, B, r, sc, U_in, bf16, dX, dA, dB, ws, s));
+  cudaError_t e = cudaMemsetAsync(ws, 0, kWsZeroed, s);
+  if (e != cudaSuccess) return QLORA_ERR_CUDA;
+  unsigned* tickets = (unsigned*)((char*)ws + kWsHeader);
   const WView v = view_of(w);
   float* V = (float*)((char*)ws + L.v);
   void* red = (char*)ws + L.red;

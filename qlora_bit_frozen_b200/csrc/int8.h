@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "qlora.h"
@@ -37,15 +38,42 @@ struct Int8Call {
   void* out;             // [R x N]
 };
 size_t int8_ws(bool dx, int64_t R, int64_t O, int64_t I, int32_t r);
-// Quantizes the activation rows into the workspace (before or after T is
-// computed), then multiplies.
-cudaError_t launch_int8_rows(const Int8Call& c, void* ws, cudaStream_t st);
+
+// Memory that the first kernel of a call clears for the ones after it.
+struct Int8Clear {
+  void* p;        // 16-byte aligned
+  size_t bytes;   // a multiple of 16
+};
+// Quantizes the activation rows into the workspace ws (int8_ws bytes), clears
+// `header` and what the product adds up in.
+cudaError_t launch_int8_rows(const Int8Call& c, void* ws, Int8Clear header, cudaStream_t st);
+// The product, over rows quantized before it, once T is computed.
+cudaError_t launch_int8_product(const Int8Call& c, void* ws, uint32_t* hdr, cudaStream_t st);
+
+// Up to this many tokens, two launches do the whole call: one quantizes the
+// rows and takes T (and, in the backward, U) by fp32 dot products, the other
+// multiplies and, in the backward, adds up dA and dB beside it.
+constexpr int64_t kInt8Few = 16;
+struct Int8Few {
+  const float* F;    // factor of T: A [r x I] (forward) or B [O x r] (backward)
+  float* T;          // [R x r]
+  // backward only (each nullable)
+  const void* X;     // [R x I]
+  const float* A;    // where U is to be computed: its factor
+  float* U_new;      // and its place
+  const float* U;    // [R x r] for dB
+  float* dA;         // [r x I]
+  float* dB;         // [O x r]
+};
+cudaError_t launch_int8_few(const Int8Call& c, const Int8Few& f, void* ws, Int8Clear header, uint32_t* hdr,
+                            cudaStream_t st);
+
 // int8_tc.cu: the product over codes xq [R x int8_pitch(K)] with row scales
-// xs; ws: int8_tc_ws bytes, of which the first int8_tc_zeroed are zero.
+// xs; ws: int8_tc_ws bytes, of which the first int8_tc_zeroed are zero; few:
+// the backward's side sums, nullable.
 size_t int8_tc_ws(bool dx, int64_t R, int64_t O, int64_t I, int32_t r);
 size_t int8_tc_zeroed(bool dx, int64_t R, int64_t O, int64_t I);
-cudaError_t launch_int8_tc(const Int8Call& c, const int8_t* xq, const float* xs, void* ws, uint32_t* hdr,
-                           cudaStream_t st);
-cudaError_t launch_int8_product(const Int8Call& c, void* ws, uint32_t* hdr, cudaStream_t st);
+cudaError_t launch_int8_tc(const Int8Call& c, const int8_t* xq, const float* xs, const Int8Few* few, void* ws,
+                           uint32_t* hdr, cudaStream_t st);
 
 }  // namespace qlora

@@ -187,7 +187,7 @@ static_assert(kPairSmem <= 227 * 1024, "one CTA per SM");
 constexpr int kPairThreads = 128 + 32 * kEpiWarps;
 
 struct PairArgs {
-  Epi e;
+  Epi e = {};
   int32_t KB, tiles_m, tiles_n;
 };
 
@@ -503,20 +503,60 @@ struct StreamCfg {
   static constexpr int kStage = kHalf + kTok;
   static constexpr int kStages = BN <= 16 ? 11 : BN <= 32 ? 10 : BN <= 64 ? (RT > 16 ? 7 : 8) : RT > 16 ? 5 : 6;
   static constexpr int kCols = BN < 32 ? 32 : BN;  // TMEM columns of one accumulator
-  static constexpr int kSide = BN * (RT + 1) * 4;  // the tokens' rows of T and scales
+  // the tokens' rows of T, their scales, and (up to 16 tokens) rows of U
+  static constexpr int kSide = BN * (RT + 1) * 4 + (BN == 16 ? BN * RT * 4 : 0);
   static constexpr int kSmem = 1024 + kStages * kStage + kSide + 512;
   static_assert(kSmem <= 227 * 1024 && kSmem > 114 * 1024, "one CTA per SM");
 };
 constexpr int kStreamThreads = 192;  // producer, MMA issuer, four epilogue warps
 
 struct StreamArgs {
-  Epi e;
+  Epi e = {};
   int32_t KB, tok_tiles;
   int64_t tiles;
   int32_t shared;       // deal out K steps (tiles may be shared by CTAs), else whole tiles
   int32_t* part;        // [tiles][BN][128] sums of tiles that several CTAs share (zeroed)
   uint32_t* tickets;    // [tiles] K steps added so far (zeroed)
+  // input gradient of up to 16 tokens: the adapter gradients beside it
+  const void* X;        // [R x I]
+  const void* dY;       // [R x O]
+  const float* U;       // [R x r]
+  float* dA;            // [r x I], nullable
+  float* dB;            // [O x r], nullable
+  int64_t I, O;
 };
+
+// The backward's side sums over up to 16 tokens, by the epilogue warps while
+// the products run: dA[j, i] = sum_t sV[t, j] X[t, i], dB[o, j] = sum_t
+// sU[t, j] dY[t, o]; a thread takes a column of X or dY.  sV, sU: [16 x RT] in
+// shared memory, s folded in.
+template <int RT>
+__device__ __forceinline__ void side_sums(const StreamArgs& p, const float* sV, const float* sU, int et) {
+  const int64_t nA = p.dA ? p.I : 0, nB = p.dB ? p.O : 0;
+  const int R = (int)p.e.R, r = p.e.r;
+  for (int64_t e = (int64_t)blockIdx.x * 128 + et; e < nA + nB; e += (int64_t)gridDim.x * 128) {
+    const bool a = e < nA;
+    const int64_t col = a ? e : e - nA, n = a ? p.I : p.O;
+    const void* P = a ? p.X : p.dY;
+    const float* f = a ? sV : sU;
+    float x[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      x[t] = 0.0f;
+      if (t < R)
+        x[t] = p.e.bf16 ? __bfloat162float(((const __nv_bfloat16*)P)[t * n + col]) : ((const float*)P)[t * n + col];
+    }
+    float* out = a ? p.dA + col : p.dB + col * r;
+    const int64_t step = a ? p.I : 1;
+    for (int j = 0; j < r; ++j) {
+      float d = 0.0f;
+#pragma unroll
+      for (int t = 0; t < 16; ++t)
+        if (t < R) d = fmaf(f[t * RT + j], x[t], d);
+      out[j * step] = d;
+    }
+  }
+}
 
 // Units (K steps, tile after tile) [lo, hi) of this CTA.
 __device__ __forceinline__ void stream_range(const StreamArgs& p, int64_t& lo, int64_t& hi) {
@@ -535,7 +575,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   float* side = (float*)(smem + C::kStages * C::kStage);  // [BN][RT] T, then [BN] scales
-  uint64_t* bars = (uint64_t*)(side + BN * (RT + 1));
+  uint64_t* bars = (uint64_t*)((uint8_t*)side + C::kSide);
   uint64_t* full = bars;
   uint64_t* empty = bars + C::kStages;
   uint64_t* acc_full = bars + 2 * C::kStages;
@@ -657,6 +697,27 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     int b = 0;
     uint32_t pa = 0;
     int64_t staged = -1;  // token tile whose T and scales are in shared memory
+    auto stage_side = [&](int64_t t0, int toks) {
+      for (int e = et; e < toks * RT; e += 128) {
+        const int t = e / RT, j = e % RT;
+        side[e] = j < p.e.r ? p.e.s * __ldg(p.e.T + (t0 + t) * p.e.r + j) : 0.0f;
+      }
+      for (int e = et; e < toks; e += 128) side[BN * RT + e] = __ldg(p.e.xs + t0 + e);
+    };
+    if constexpr (BN == 16 && DX) {
+      if (p.dA || p.dB) {  // a single token tile
+        float* su = side + BN * (RT + 1);
+        stage_side(0, (int)p.e.R);
+        if (p.dB)
+          for (int e = et; e < (int)p.e.R * RT; e += 128) {
+            const int t = e / RT, j = e % RT;
+            su[e] = j < p.e.r ? p.e.s * __ldg(p.U + t * p.e.r + j) : 0.0f;
+          }
+        staged = 0;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        side_sums<RT>(p, side, su, et);
+      }
+    }
     for (int64_t u = lo; u < hi;) {
       const int64_t tile = u / p.KB, end = min(hi, (tile + 1) * p.KB);
       const int steps = (int)(end - u);
@@ -673,11 +734,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       const float sw = !DX && in ? __ldg(p.e.ws + n) : 1.0f;
       if (tt != staged) {
         asm volatile("bar.sync 1, 128;" ::: "memory");  // the last tile's are read
-        for (int e = et; e < toks * RT; e += 128) {
-          const int t = e / RT, j = e % RT;
-          side[e] = j < p.e.r ? p.e.s * __ldg(p.e.T + (t0 + t) * p.e.r + j) : 0.0f;
-        }
-        for (int e = et; e < toks; e += 128) side[BN * RT + e] = __ldg(p.e.xs + t0 + e);
+        stage_side(t0, toks);
         staged = tt;
       }
       // one answer for all four warps, which meet at barriers below
@@ -897,8 +954,8 @@ cudaError_t go_stream(const Plan& pl, const CUtensorMap& x, const CUtensorMap& w
 }
 
 template <bool DX, typename OUT, int RT>
-cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& base, int64_t K, void* ws,
-               cudaStream_t st) {
+cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& base, const Int8Few* few,
+               int64_t K, void* ws, cudaStream_t st) {
   Epi e = base;
   CUtensorMap mx, mw, mo;
   const int64_t xp = int8_pitch(K), wp = int8_pitch(c.I);
@@ -932,7 +989,7 @@ cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& b
     return go_pair<DX, OUT, RT>(pl, mx, mw, mo, a, st);
   }
   constexpr int SRT = RT <= 16 ? 16 : 64;
-  StreamArgs a;
+  StreamArgs a = {};
   a.e = e;
   a.KB = (int32_t)up(K, kBK);
   a.tok_tiles = (int32_t)up(c.R, pl.bn);
@@ -940,6 +997,15 @@ cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& b
   a.shared = pl.shared ? 1 : 0;
   a.part = (int32_t*)ws;
   a.tickets = (uint32_t*)((char*)ws + stream_part_bytes(pl));
+  if (few && DX) {
+    a.X = few->X;
+    a.dY = c.P;
+    a.U = few->U;
+    a.dA = few->dA;
+    a.dB = few->dB;
+    a.I = c.I;
+    a.O = c.O;
+  }
   switch (pl.bn) {
     case 16: return go_stream<DX, 16, SRT>(pl, mx, mw, a, st);
     case 32: return go_stream<DX, 32, SRT>(pl, mx, mw, a, st);
@@ -949,13 +1015,13 @@ cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& b
 }
 
 template <bool DX, typename OUT>
-cudaError_t go_rank(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& e, int64_t K, void* ws,
-                    cudaStream_t st) {
+cudaError_t go_rank(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& e, const Int8Few* few,
+                    int64_t K, void* ws, cudaStream_t st) {
   switch (rank_pad(c.r)) {
-    case 8: return go<DX, OUT, 8>(pl, c, xq, e, K, ws, st);
-    case 16: return go<DX, OUT, 16>(pl, c, xq, e, K, ws, st);
-    case 32: return go<DX, OUT, 32>(pl, c, xq, e, K, ws, st);
-    default: return go<DX, OUT, 64>(pl, c, xq, e, K, ws, st);
+    case 8: return go<DX, OUT, 8>(pl, c, xq, e, few, K, ws, st);
+    case 16: return go<DX, OUT, 16>(pl, c, xq, e, few, K, ws, st);
+    case 32: return go<DX, OUT, 32>(pl, c, xq, e, few, K, ws, st);
+    default: return go<DX, OUT, 64>(pl, c, xq, e, few, K, ws, st);
   }
 }
 
@@ -973,11 +1039,11 @@ size_t int8_tc_zeroed(bool dx, int64_t R, int64_t O, int64_t I) {
   return p.pair ? 0 : stream_part_bytes(p) + stream_ticket_bytes(p);
 }
 
-cudaError_t launch_int8_tc(const Int8Call& c, const int8_t* xq, const float* xs, void* ws, uint32_t* hdr,
-                           cudaStream_t st) {
+cudaError_t launch_int8_tc(const Int8Call& c, const int8_t* xq, const float* xs, const Int8Few* few, void* ws,
+                           uint32_t* hdr, cudaStream_t st) {
   const int64_t K = c.dx ? c.O : c.I;
   const Plan pl = plan_for(c.R, c.dx ? c.I : c.O, K);
-  Epi e;
+  Epi e = {};
   e.R = c.R;
   e.N = c.dx ? c.I : c.O;
   e.xs = xs;
@@ -992,10 +1058,10 @@ cudaError_t launch_int8_tc(const Int8Call& c, const int8_t* xq, const float* xs,
   e.err = hdr;
   e.wait_ns = kWaitLimitNs;
   if (c.dx)
-    return c.bf16 ? go_rank<true, __nv_bfloat16>(pl, c, xq, e, K, ws, st)
-                  : go_rank<true, float>(pl, c, xq, e, K, ws, st);
-  return c.bf16 ? go_rank<false, __nv_bfloat16>(pl, c, xq, e, K, ws, st)
-                : go_rank<false, float>(pl, c, xq, e, K, ws, st);
+    return c.bf16 ? go_rank<true, __nv_bfloat16>(pl, c, xq, e, few, K, ws, st)
+                  : go_rank<true, float>(pl, c, xq, e, few, K, ws, st);
+  return c.bf16 ? go_rank<false, __nv_bfloat16>(pl, c, xq, e, few, K, ws, st)
+                : go_rank<false, float>(pl, c, xq, e, few, K, ws, st);
 }
 
 }  // namespace qlora
