@@ -101,6 +101,22 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
       : "memory");
 }
 
+// The producer and MMA warps run their loops with all lanes (the loop state
+// then lives in uniform registers) and let one elected lane issue: with a
+// single lane running the loop the MMA warp took 550 cycles a step, whatever
+// the tile.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// Bounded wait of a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, uint32_t* err,
+                                          uint32_t where) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns, err, where));
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -127,6 +143,18 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* tmap, ui
       "[%1, {%3, %4}], [%2];" ::"r"(dst),
       "l"(tmap), "r"(bar), "r"(x), "r"(y)
       : "memory");
+}
+// The same box into L2 only.
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap), "r"(x), "r"(y)
+               : "memory");
+}
+// 32 lanes x 8 columns of TMEM.
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr));
 }
 __device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tmap),
@@ -258,71 +286,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int64_t t = cluster; t < tiles && ok; t += clusters) {
-        int tm, tn;
-        pair_tile(t, p.tiles_m, p.tiles_n, tm, tn);
-        const int m0 = tm * 256 + 128 * (int)rank, n0 = tn * 256 + 128 * (int)rank;
-        for (int kb = 0; kb < p.KB; ++kb) {
-          if (((kb & 7) == 0 && *abort_flag) ||
-              !mbar_wait(smem_u32(&empty[s]), ph ^ 1u, p.e.wait_ns, p.e.err, 0x501)) {
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int64_t t = cluster; t < tiles && ok; t += clusters) {
+      int tm, tn;
+      pair_tile(t, p.tiles_m, p.tiles_n, tm, tn);
+      const int m0 = tm * 256 + 128 * (int)rank, n0 = tn * 256 + 128 * (int)rank;
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+      for (int kb = 0; kb < p.KB; ++kb) {
+        if (!warp_wait(smem_u32(&empty[s]), ph ^ 1u, p.e.wait_ns, p.e.err, 0x501)) {
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           const uint32_t fb = smem_u32(&full[s]), dst = smem_u32(smem + s * kStage);
           if (rank == 0) mbar_arrive_expect_tx(fb, 2 * kStage);
           const uint32_t lead = at_rank(fb, 0);
           tma_load_pair(dst, &tm_x, lead, kb * kBK, m0);
           tma_load_pair(dst + kHalf, &tm_w, lead, DX ? n0 : kb * kBK, DX ? kb * kBK : n0);
-          if (++s == kPairStages) { s = 0; ph ^= 1u; }
         }
-      }
-      // every copy has landed and every commit to this CTA's barriers has
-      // arrived before the pair may exit
-      for (int i = 0; i < kPairStages; ++i) {
-        mbar_wait(smem_u32(&empty[s]), ph ^ 1u, p.e.wait_ns, ok ? p.e.err : nullptr, 0x502);
+        __syncwarp();
         if (++s == kPairStages) { s = 0; ph ^= 1u; }
       }
     }
-    __syncwarp();
+    // every copy has landed and every commit to this CTA's barriers has
+    // arrived before the pair may exit
+    for (int i = 0; i < kPairStages; ++i) {
+      warp_wait(smem_u32(&empty[s]), ph ^ 1u, p.e.wait_ns, ok ? p.e.err : nullptr, 0x502);
+      if (++s == kPairStages) { s = 0; ph ^= 1u; }
+    }
   } else if (warp == 1) {
     // -------------------------------------------------------- MMA issuer
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       int s = 0, b = 0;
       uint32_t ph = 0, pa = 0;
       bool ok = true;
       for (int64_t t = cluster; t < tiles && ok; t += clusters) {
-        if (!mbar_wait(smem_u32(&acc_empty[b]), pa ^ 1u, p.e.wait_ns, p.e.err, 0x503)) {
+        if (!warp_wait(smem_u32(&acc_empty[b]), pa ^ 1u, p.e.wait_ns, p.e.err, 0x503)) {
           *abort_flag = 1;
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + 256u * (uint32_t)b;
         for (int kb = 0; kb < p.KB; ++kb) {
-          if (!mbar_wait(smem_u32(&full[s]), ph, p.e.wait_ns, p.e.err, 0x504)) {
+          if (!warp_wait(smem_u32(&full[s]), ph, p.e.wait_ns, p.e.err, 0x504)) {
             *abort_flag = 1;
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t base = smem_u32(smem + s * kStage);
-          const uint64_t ad = sdesc(base, 16, 1024);
-          const uint64_t bd = DX ? sdesc(base + kHalf, kHalf, 1024) : sdesc(base + kHalf, 16, 1024);
+          if (elect_one()) {
+            const uint32_t base = smem_u32(smem + s * kStage);
+            const uint64_t ad = sdesc(base, 16, 1024);
+            const uint64_t bd = DX ? sdesc(base + kHalf, kHalf, 1024) : sdesc(base + kHalf, 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 32; ++kk)
-            umma_i8<2>(d, ad + 2 * kk, bd + (DX ? 256 : 2) * kk, kIdesc, (kb | kk) ? 1u : 0u);
-          umma_commit_pair(smem_u32(&empty[s]));
+            for (int kk = 0; kk < kBK / 32; ++kk)
+              umma_i8<2>(d, ad + 2 * kk, bd + (DX ? 256 : 2) * kk, kIdesc, (kb | kk) ? 1u : 0u);
+            umma_commit_pair(smem_u32(&empty[s]));
+            if (kb + 1 == p.KB) umma_commit_pair(smem_u32(&acc_full[b]));
+          }
+          __syncwarp();
           if (++s == kPairStages) { s = 0; ph ^= 1u; }
         }
-        if (ok) umma_commit_pair(smem_u32(&acc_full[b]));
         if (++b == 2) { b = 0; pa ^= 1u; }
       }
     }
-    __syncwarp();
   } else if (warp >= 4) {
     // ---------------------------------------------------------- epilogue
     // Lane = token.  Warp `half` of a quarter takes 64-column runs half, half
@@ -513,7 +543,7 @@ constexpr int kStreamThreads = 192;  // producer, MMA issuer, four epilogue warp
 struct StreamArgs {
   Epi e = {};
   int32_t KB, tok_tiles;
-  int64_t tiles;
+  int64_t tiles;  // one token tile after the other, then the next weight tile
   int32_t shared;       // deal out K steps (tiles may be shared by CTAs), else whole tiles
   int32_t* part;        // [tiles][BN][128] sums of tiles that several CTAs share (zeroed)
   uint32_t* tickets;    // [tiles] K steps added so far (zeroed)
@@ -528,42 +558,90 @@ struct StreamArgs {
 
 // The backward's side sums over up to 16 tokens, by the epilogue warps while
 // the products run: dA[j, i] = sum_t sV[t, j] X[t, i], dB[o, j] = sum_t
-// sU[t, j] dY[t, o]; a thread takes a column of X or dY.  sV, sU: [16 x RT] in
-// shared memory, s folded in.
-template <int RT>
-__device__ __forceinline__ void side_sums(const StreamArgs& p, const float* sV, const float* sU, int et) {
-  const int64_t nA = p.dA ? p.I : 0, nB = p.dB ? p.O : 0;
-  const int R = (int)p.e.R, r = p.e.r;
-  for (int64_t e = (int64_t)blockIdx.x * 128 + et; e < nA + nB; e += (int64_t)gridDim.x * 128) {
+// sU[t, j] dY[t, o]; a thread takes a column of X or dY at a time.  The column
+// does not depend on the launch before this one, sV and sU do ([16 x RT] in
+// shared memory, s folded in): the first column is loaded ahead of the wait.
+struct SideSums {
+  int64_t e, total, nA;
+  float x[16];
+  __device__ __forceinline__ SideSums(const StreamArgs& p, int et) {
+    nA = p.dA ? p.I : 0;
+    total = nA + (p.dB ? p.O : 0);
+    e = (int64_t)blockIdx.x * 128 + et;
+    load(p);
+  }
+  __device__ __forceinline__ void load(const StreamArgs& p) {
+    if (e >= total) return;
     const bool a = e < nA;
     const int64_t col = a ? e : e - nA, n = a ? p.I : p.O;
     const void* P = a ? p.X : p.dY;
-    const float* f = a ? sV : sU;
-    float x[16];
 #pragma unroll
     for (int t = 0; t < 16; ++t) {
       x[t] = 0.0f;
-      if (t < R)
+      if (t < (int)p.e.R)
         x[t] = p.e.bf16 ? __bfloat162float(((const __nv_bfloat16*)P)[t * n + col]) : ((const float*)P)[t * n + col];
     }
-    float* out = a ? p.dA + col : p.dB + col * r;
-    const int64_t step = a ? p.I : 1;
-    for (int j = 0; j < r; ++j) {
-      float d = 0.0f;
+  }
+  template <int RT>
+  __device__ __forceinline__ void run(const StreamArgs& p, const float* sV, const float* sU) {
+    const int R = (int)p.e.R, r = p.e.r;
+    while (e < total) {
+      const bool a = e < nA;
+      const int64_t col = a ? e : e - nA, step = a ? p.I : 1;
+      const float* f = a ? sV : sU;
+      float* out = a ? p.dA + col : p.dB + col * r;
+#pragma unroll 1
+      for (int j = 0; j < r; j += 4) {
+        float d[4] = {};
 #pragma unroll
-      for (int t = 0; t < 16; ++t)
-        if (t < R) d = fmaf(f[t * RT + j], x[t], d);
-      out[j * step] = d;
+        for (int t = 0; t < 16; ++t) {
+          if (t < R) {
+            const float4 v = *reinterpret_cast<const float4*>(f + t * RT + j);
+            d[0] = fmaf(v.x, x[t], d[0]);
+            d[1] = fmaf(v.y, x[t], d[1]);
+            d[2] = fmaf(v.z, x[t], d[2]);
+            d[3] = fmaf(v.w, x[t], d[3]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j + i < r) out[(j + i) * step] = d[i];
+      }
+      e += (int64_t)gridDim.x * 128;
+      load(p);
     }
   }
-}
+};
 
-// Units (K steps, tile after tile) [lo, hi) of this CTA.
-__device__ __forceinline__ void stream_range(const StreamArgs& p, int64_t& lo, int64_t& hi) {
-  const int64_t n = p.shared ? p.tiles * p.KB : p.tiles, one = p.shared ? 1 : p.KB;
-  lo = n * blockIdx.x / gridDim.x * one;
-  hi = n * (blockIdx.x + 1) / gridDim.x * one;
-}
+// The K steps of this CTA, tile after tile: `steps` of them, from step kb of
+// tile (weight tile mt, token tile tt) on.  Every role walks them with running
+// counters: a 64-bit division is a hundred instructions of its one thread.
+struct Walk {
+  int64_t tile, steps;
+  int32_t kb, mt, tt;
+  __device__ __forceinline__ explicit Walk(const StreamArgs& p) {
+    const int64_t n = p.shared ? p.tiles * p.KB : p.tiles;
+    const int64_t lo = n * blockIdx.x / gridDim.x, hi = n * (blockIdx.x + 1) / gridDim.x;
+    tile = p.shared ? lo / p.KB : lo;
+    kb = p.shared ? (int32_t)(lo - tile * p.KB) : 0;
+    steps = p.shared ? hi - lo : (hi - lo) * p.KB;
+    mt = (int32_t)(tile / p.tok_tiles);
+    tt = (int32_t)(tile - (int64_t)mt * p.tok_tiles);
+  }
+  // steps left of the current tile
+  __device__ __forceinline__ int run(const StreamArgs& p) const {
+    return (int)(steps < p.KB - kb ? steps : p.KB - kb);
+  }
+  __device__ __forceinline__ void advance(const StreamArgs& p, int n) {  // within the tile
+    steps -= n;
+    kb += n;
+    if (kb == p.KB) {
+      kb = 0;
+      ++tile;
+      if (++tt == p.tok_tiles) { tt = 0; ++mt; }
+    }
+  }
+};
 
 
 template <bool DX, int BN, int RT>
@@ -585,9 +663,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   volatile uint32_t* last_flag = tmem_slot + 2;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t lo, hi;
-  stream_range(p, lo, hi);
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
@@ -612,91 +687,101 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      // The weight does not depend on the launch before this one, the codes
-      // of the activations do: the first stages' weight tiles are on their
-      // way while that launch still runs.
-      const int64_t ahead = min(hi, lo + C::kStages);
-      auto load = [&](int64_t u, int slot, bool w, bool x) {
-        const int64_t tile = u / p.KB;
-        const int kb = (int)(u - tile * p.KB);
-        const int m0 = (int)(tile / p.tok_tiles) * 128, t0 = (int)(tile % p.tok_tiles) * BN;
-        const uint32_t fb = smem_u32(&full[slot]), dst = smem_u32(smem + slot * C::kStage);
-        if (w) {
-          mbar_arrive_expect_tx(fb, C::kStage);
-          tma_load_2d(dst, &tm_w, fb, DX ? m0 : kb * kBK, DX ? kb * kBK : m0);
-        }
-        if (x) tma_load_2d(dst + kHalf, &tm_x, fb, kb * kBK, t0);
-      };
-      for (int64_t u = lo; u < ahead; ++u) load(u, (int)(u - lo), true, false);
-      griddep_wait();
-      for (int64_t u = lo; u < hi; ++u) {
-        if (u < ahead) {
-          load(u, s, false, true);
-        } else {
-          if (*abort_flag || !mbar_wait(smem_u32(&empty[s]), ph ^ 1u, p.e.wait_ns, p.e.err, 0x601)) {
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-          load(u, s, true, true);
-        }
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    // The weight does not depend on the launch before this one, the codes of
+    // the activations do: the first stages' weight tiles are on their way
+    // while that launch still runs, and the next ones on their way into L2 (up
+    // to 57 MB of its 126 on 148 SMs).
+    Walk w(p);
+    const int ahead = (int)min((int64_t)C::kStages, w.steps);
+    auto load_w = [&](const Walk& at, int slot) {
+      const uint32_t fb = smem_u32(&full[slot]);
+      mbar_arrive_expect_tx(fb, C::kStage);
+      tma_load_2d(smem_u32(smem + slot * C::kStage), &tm_w, fb, DX ? at.mt * 128 : at.kb * kBK,
+                  DX ? at.kb * kBK : at.mt * 128);
+    };
+    auto load_x = [&](const Walk& at, int slot) {
+      tma_load_2d(smem_u32(smem + slot * C::kStage + kHalf), &tm_x, smem_u32(&full[slot]), at.kb * kBK,
+                  at.tt * BN);
+    };
+    Walk early = w;
+    for (int i = 0; i < ahead; ++i, early.advance(p, 1)) {
+      if (elect_one()) load_w(early, i);
+      __syncwarp();
+    }
+    for (int i = 0; i < 24 && early.steps > 0; ++i, early.advance(p, 1)) {
+      if (elect_one())
+        tma_prefetch_2d(&tm_w, DX ? early.mt * 128 : early.kb * kBK, DX ? early.kb * kBK : early.mt * 128);
+      __syncwarp();
+    }
+    griddep_wait();
+    for (int i = 0; w.steps > 0; ++i, w.advance(p, 1)) {
+      if (i >= ahead && (__any_sync(0xffffffffu, *abort_flag != 0) ||
+                         !warp_wait(smem_u32(&empty[s]), ph ^ 1u, p.e.wait_ns, p.e.err, 0x601))) {
+        *abort_flag = 1;
+        ok = false;
+        break;
+      }
+      if (elect_one()) {
+        if (i >= ahead) load_w(w, s);
+        load_x(w, s);
+      }
+      __syncwarp();
+      if (++s == C::kStages) { s = 0; ph ^= 1u; }
+    }
+    // copies in flight land before the CTA exits (the MMA has waited for
+    // them all unless something gave up)
+    if (!ok) {
+      for (int i = 0; i < C::kStages; ++i) {
+        warp_wait(smem_u32(&full[s]), ph ^ 1u, p.e.wait_ns, nullptr, 0);
         if (++s == C::kStages) { s = 0; ph ^= 1u; }
       }
-      // copies in flight land before the CTA exits (the MMA has waited for
-      // them all unless something gave up)
-      if (!ok) {
-        for (int i = 0; i < C::kStages; ++i) {
-          mbar_wait(smem_u32(&full[s]), ph ^ 1u, p.e.wait_ns, nullptr, 0);
-          if (++s == C::kStages) { s = 0; ph ^= 1u; }
-        }
-      }
     }
-    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      int s = 0, b = 0;
-      uint32_t ph = 0, pa = 0;
-      bool ok = true;
-      for (int64_t u = lo; u < hi && ok;) {
-        const int64_t end = min(hi, (u / p.KB + 1) * p.KB);  // this tile's run
-        if (!mbar_wait(smem_u32(&acc_empty[b]), pa ^ 1u, p.e.wait_ns, p.e.err, 0x602)) {
+    int s = 0, b = 0;
+    uint32_t ph = 0, pa = 0;
+    bool ok = true;
+    for (Walk w(p); w.steps > 0 && ok;) {
+      const int run = w.run(p);
+      if (!warp_wait(smem_u32(&acc_empty[b]), pa ^ 1u, p.e.wait_ns, p.e.err, 0x602)) {
+        *abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem + (uint32_t)(C::kCols * b);
+      for (int i = 0; i < run; ++i) {
+        if (!warp_wait(smem_u32(&full[s]), ph, p.e.wait_ns, p.e.err, 0x603)) {
           *abort_flag = 1;
+          ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(C::kCols * b);
-        for (bool first = true; u < end; ++u, first = false) {
-          if (!mbar_wait(smem_u32(&full[s]), ph, p.e.wait_ns, p.e.err, 0x603)) {
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        if (elect_one()) {
           const uint32_t base = smem_u32(smem + s * C::kStage);
           const uint64_t ad = DX ? sdesc(base, kHalf, 1024) : sdesc(base, 16, 1024);
           const uint64_t bd = sdesc(base + kHalf, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < kBK / 32; ++kk)
-            umma_i8<1>(d, ad + (DX ? 256 : 2) * kk, bd + 2 * kk, kIdesc, (!first || kk) ? 1u : 0u);
+            umma_i8<1>(d, ad + (DX ? 256 : 2) * kk, bd + 2 * kk, kIdesc, (i | kk) ? 1u : 0u);
           umma_commit(smem_u32(&empty[s]));
-          if (++s == C::kStages) { s = 0; ph ^= 1u; }
+          if (i + 1 == run) umma_commit(smem_u32(&acc_full[b]));
         }
-        if (ok) umma_commit(smem_u32(&acc_full[b]));
-        if (++b == 2) { b = 0; pa ^= 1u; }
+        __syncwarp();
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
       }
+      if (++b == 2) { b = 0; pa ^= 1u; }
+      w.advance(p, run);
     }
-    __syncwarp();
   } else {
     // epilogue: lane = output n, TMEM column = token
     const int quad = warp & 3, et = (int)threadIdx.x - 64;
+    SideSums sums(p, et);
     griddep_wait();
     int b = 0;
     uint32_t pa = 0;
-    int64_t staged = -1;  // token tile whose T and scales are in shared memory
+    int staged = -1;  // token tile whose T and scales are in shared memory
     auto stage_side = [&](int64_t t0, int toks) {
       for (int e = et; e < toks * RT; e += 128) {
         const int t = e / RT, j = e % RT;
@@ -715,22 +800,29 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           }
         staged = 0;
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        side_sums<RT>(p, side, su, et);
+        sums.template run<RT>(p, side, su);
       }
     }
-    for (int64_t u = lo; u < hi;) {
-      const int64_t tile = u / p.KB, end = min(hi, (tile + 1) * p.KB);
-      const int steps = (int)(end - u);
-      u = end;
-      const int64_t n = (tile / p.tok_tiles) * 128 + 32 * quad + lane;
-      const int64_t tt = tile % p.tok_tiles, t0 = tt * BN;
+    Walk w(p);
+    while (w.steps > 0) {
+      const int64_t tile = w.tile;
+      const int steps = w.run(p), tt = w.tt;
+      const int64_t n = (int64_t)w.mt * 128 + 32 * quad + lane, t0 = (int64_t)tt * BN;
+      w.advance(p, steps);
       const int toks = (int)min((int64_t)BN, p.e.R - t0);
       // this tile's side inputs, while its products run
-      float l[RT];
+      uint64_t l[RT / 2];
       const bool in = n < p.e.N;
 #pragma unroll
-      for (int j = 0; j < RT; ++j)
-        l[j] = in && j < p.e.r ? __ldg(p.e.L + (DX ? (int64_t)j * p.e.N + n : n * p.e.r + j)) : 0.0f;
+      for (int j = 0; j < RT / 2; ++j) {
+        float v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int q = 2 * j + i;
+          v[i] = in && q < p.e.r ? __ldg(p.e.L + (DX ? (int64_t)q * p.e.N + n : n * p.e.r + q)) : 0.0f;
+        }
+        l[j] = pack2(v[0], v[1]);
+      }
       const float sw = !DX && in ? __ldg(p.e.ws + n) : 1.0f;
       if (tt != staged) {
         asm volatile("bar.sync 1, 128;" ::: "memory");  // the last tile's are read
@@ -749,12 +841,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       bool finish = whole;
       if (!whole) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < toks; c0 += 32) {
-          uint32_t acc[32];
-          tmem_ld_32x32b_x32(acc0 + (uint32_t)c0, acc);
+        for (int c0 = 0; c0 < toks; c0 += 8) {
+          uint32_t acc[8];
+          tmem_ld_32x32b_x8(acc0 + (uint32_t)c0, acc);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
+          for (int j = 0; j < 8; ++j)
             if (c0 + j < toks) atomicAdd(part + (c0 + j) * 128, (int)acc[j]);
         }
         __threadfence();
@@ -767,37 +859,41 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         asm volatile("bar.sync 1, 128;" ::: "memory");  // all have read the flag
       }
       if (finish) {
+        // eight tokens at a time (columns past the last token hold sums of
+        // zero-filled rows and are not stored)
 #pragma unroll 1
-        for (int c0 = 0; c0 < toks; c0 += 32) {
-          uint32_t acc[32];
+        for (int c0 = 0; c0 < toks; c0 += 8) {
+          uint32_t acc[8];
           if (whole) {
-            tmem_ld_32x32b_x32(acc0 + (uint32_t)c0, acc);
+            tmem_ld_32x32b_x8(acc0 + (uint32_t)c0, acc);
             tmem_ld_wait();
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[j] = c0 + j < toks ? (uint32_t)__ldcg(part + (c0 + j) * 128) : 0u;
+            for (int j = 0; j < 8; ++j) acc[j] = (uint32_t)__ldcg(part + (c0 + j) * 128);
           }
+          float v[8];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (c0 + j < toks) {
-              const float* T = side + (c0 + j) * RT;
-              float d = 0.0f;
+          for (int j = 0; j < 8; ++j) {
+            const float* T = side + (c0 + j) * RT;
+            uint64_t d = 0;
 #pragma unroll
-              for (int q = 0; q < RT; q += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(T + q);
-                d = fmaf(l[q], v.x, d);
-                d = fmaf(l[q + 1], v.y, d);
-                d = fmaf(l[q + 2], v.z, d);
-                d = fmaf(l[q + 3], v.w, d);
-              }
-              const float v =
-                  __fadd_rn(__fmul_rn(__fmul_rn((float)(int)acc[j], side[BN * RT + c0 + j]), sw), d);
-              const int64_t o = (t0 + c0 + j) * p.e.N + n;
-              if (in) {
-                if (p.e.bf16) ((__nv_bfloat16*)p.e.out)[o] = __float2bfloat16_rn(v);
-                else ((float*)p.e.out)[o] = v;
-              }
+            for (int q = 0; q < RT / 4; ++q) {
+              const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(T + 4 * q);
+              d = fma2(l[2 * q], t.x, d);
+              d = fma2(l[2 * q + 1], t.y, d);
             }
+            v[j] = __fadd_rn(__fmul_rn(__fmul_rn((float)(int)acc[j], side[BN * RT + c0 + j]), sw), sum2(d));
+          }
+          if (!in) continue;
+          const int64_t o = (t0 + c0) * p.e.N + n;
+          if (p.e.bf16) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (c0 + j < toks) ((__nv_bfloat16*)p.e.out)[o + j * p.e.N] = __float2bfloat16_rn(v[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (c0 + j < toks) ((float*)p.e.out)[o + j * p.e.N] = v[j];
           }
         }
       }
