@@ -500,9 +500,9 @@ def qlora_linear_fwd(w: QuantizedWeight, X: torch.Tensor, A: torch.Tensor, B: to
     r = A.shape[0]
     compute = _compute_of(X)
     if Y is None:
-        Y = torch.empty((R, w.O), dtype=X.dtype, device=X.device)
+        Y = X.new_empty((R, w.O))
     if U_out is None and want_u:
-        U_out = torch.empty((R, r), dtype=torch.float32, device=X.device)
+        U_out = A.new_empty((R, r))
     cw = ctypes.byref(w.c_struct())
     if ws is None:
         ws = workspace(lib.qlora_linear_workspace_bytes(cw, R, r, OP_FWD, compute), X.device)

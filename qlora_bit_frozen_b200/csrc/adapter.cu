@@ -1124,7 +1124,7 @@ cudaError_t rowdot_mma_r(const __nv_bfloat16* P, int64_t R, int64_t K, const flo
 cudaError_t split_factor(const float* src, int64_t extent, int r, bool nr, uint16_t* dst,
                          int64_t* ld, cudaStream_t st, int parts = 2) {
   const int NP = 8 * rank_tiles(r);
-  *ld = (extent + 7) / 8 * 8;
+  *ld = adapter_split_ld(extent);
   const int64_t pairs = (int64_t)NP * *ld / 2;
   if (parts == 3)
     split_factor_kernel<3><<<cdiv(pairs, 256), 256, 0, st>>>(src, extent, r, nr ? 1 : 0, NP, *ld, dst);
@@ -1240,6 +1240,11 @@ bool coldot_mma_ok(const void* P, bool bf16, int64_t R, int64_t N, const float* 
 
 }  // namespace
 
+bool coldot_takes(const void* P, int64_t R, int64_t N) {
+  return R > 0 && N % 8 == 0 && (uintptr_t)P % 16 == 0;
+}
+int adapter_rank_rows(int32_t r) { return 8 * rank_tiles(r); }
+
 size_t adapter_split_ws(int64_t extent, int32_t r, int parts) {
   if (rank_tiles(r) < 2 && parts == 2) return 0;
   return align_up((size_t)parts * 8 * rank_tiles(r) * (size_t)((extent + 7) / 8 * 8) * 2, 256);
@@ -1317,7 +1322,7 @@ cudaError_t launch_coldot_pair(const void* PA, int64_t NA, const float* auxA, bo
                                float* outA, void* wsA, uint16_t* splitA, const void* PB,
                                int64_t NB, const float* auxB, bool out_nrB, float* outB, void* wsB,
                                uint16_t* splitB, int64_t R, int32_t r, float s, cudaStream_t st,
-                               unsigned* tickets, bool* done, int parts) {
+                               unsigned* tickets, bool* done, int parts, bool split_done) {
   *done = false;
   if (R <= 0 || NA <= 0 || NB <= 0 || !tickets) return cudaSuccess;
   if (!coldot_mma_ok(PA, true, R, NA, auxA) || !coldot_mma_ok(PB, true, R, NB, auxB))
@@ -1329,9 +1334,10 @@ cudaError_t launch_coldot_pair(const void* PA, int64_t NA, const float* auxA, bo
   *done = true;
   if ((rank_tiles(r) >= 2 || parts == 3) && splitA && splitB && ((uintptr_t)splitA % 16) == 0 &&
       ((uintptr_t)splitB % 16) == 0) {
-    int64_t lda = 0, ldb = 0;
-    cudaError_t e = split_factor(auxA, R, r, true, splitA, &lda, st, parts);
-    if (e == cudaSuccess) e = split_factor(auxB, R, r, true, splitB, &ldb, st, parts);
+    int64_t lda = adapter_split_ld(R), ldb = lda;
+    cudaError_t e = cudaSuccess;
+    if (!split_done) e = split_factor(auxA, R, r, true, splitA, &lda, st, parts);
+    if (!split_done && e == cudaSuccess) e = split_factor(auxB, R, r, true, splitB, &ldb, st, parts);
     if (e != cudaSuccess) return e;
     const ColJob ja = col_job(A, R, NA, (const float*)splitA, lda, r, pa, s, out_nrA, outA,
                               (float*)wsA, tickets);

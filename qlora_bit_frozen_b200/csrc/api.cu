@@ -290,18 +290,20 @@ cudaError_t int8_fwd(const qlora_weight* w, const void* X, int64_t R, const floa
   const Int8Call c = int8_call(w, false, bf16, R, X, U, B, r, sc, Y);
   const Int8Clear header = {ws, kWsZeroed};
   void* rows = (char*)ws + L.rows;
-  if (R <= kInt8Few) {
+  cudaError_t e;
+  if (int8_few_applies(R, w->I, r)) {
     Int8Few f = {};
     f.F = A;
     f.T = U;
-    return launch_int8_few(c, f, rows, header, (uint32_t*)ws, s);
+    e = launch_int8_few(c, f, rows, header, s);
+    return e != cudaSuccess ? e : launch_int8_product(c, rows, (uint32_t*)ws, nullptr, s);
   }
-  cudaError_t e = launch_int8_rows(c, rows, header, s);
+  e = launch_int8_rows(c, rows, header, s);
   if (e == cudaSuccess)
     e = launch_rowdot(X, bf16, R, w->I, A, false, r, U, s, nullptr, nullptr, 0, 0, 1.0f, nullptr, nullptr,
                       (float*)((char*)ws + L.red), (unsigned*)((char*)ws + kWsHeader),
                       (uint16_t*)((char*)ws + L.split), 3);
-  if (e == cudaSuccess) e = launch_int8_product(c, rows, (uint32_t*)ws, s);
+  if (e == cudaSuccess) e = launch_int8_product(c, rows, (uint32_t*)ws, nullptr, s);
   return e;
 }
 
@@ -310,12 +312,12 @@ cudaError_t int8_fwd(const qlora_weight* w, const void* X, int64_t R, const floa
 cudaError_t adapter_grads(bool bf16, const void* X, int64_t I, const float* V, float* dA, const void* dY,
                           int64_t O, const float* U, float* dB, int64_t R, int32_t r, float sc, void* red,
                           void* red2, uint16_t* split, uint16_t* split2, unsigned* tickets,
-                          cudaStream_t s) {
+                          cudaStream_t s, bool split_done = false) {
   bool paired = false;
   cudaError_t e = cudaSuccess;
   if (dA && dB && bf16)
     e = launch_coldot_pair(X, I, V, false, dA, red, split, dY, O, U, true, dB, red2, split2, R, r, sc, s,
-                           tickets, &paired, 3);
+                           tickets, &paired, 3, split_done);
   if (e == cudaSuccess && dA && !paired)
     e = launch_coldot(X, bf16, R, I, V, r, sc, false, dA, red, s, tickets, split, 3);
   if (e == cudaSuccess && dB && !paired)
@@ -335,17 +337,36 @@ cudaError_t int8_bwd(const qlora_weight* w, const void* X, const void* dY, int64
   void* rows = (char*)ws + L.rows;
   const Int8Clear header = {ws, kWsZeroed};
   const Int8Call c = int8_call(w, true, bf16, R, dY, V, A, r, sc, dX);
-  if (dX && R > 0 && R <= kInt8Few) {
+  // (the same kernels whichever gradients are wanted: each has the same bits)
+  if (R > 0 && int8_few_applies(R, w->O, r) && int8_few_applies(R, w->I, r)) {
+    // the rows, V and U in one launch; dA and dB beside the products, or, for
+    // more tokens, from the parts of V and U that the first launch left
     Int8Few f = {};
     f.F = B;
-    f.T = V;
+    f.T = dX || dA ? V : nullptr;
     f.X = X;
     f.A = A;
     f.U_new = dB && !U_in ? Uw : nullptr;
     f.U = U_in ? U_in : Uw;
-    f.dA = dA;
-    f.dB = dB;
-    return launch_int8_few(c, f, rows, header, (uint32_t*)ws, s);
+    const bool beside = R <= kInt8Few;
+    if (beside) {
+      f.dA = dA;
+      f.dB = dB;
+    }
+    const bool parts = !beside && dA && dB && bf16 && coldot_takes(X, R, w->I) && coldot_takes(dY, R, w->O);
+    if (parts) {
+      f.T_parts = split;
+      f.U_parts = (uint16_t*)((char*)ws + L.split2);
+      f.NP = adapter_rank_rows(r);
+      f.ld = adapter_split_ld(R);
+    }
+    cudaError_t e = launch_int8_few(c, f, rows, header, s);
+    if (e == cudaSuccess && !beside)
+      e = adapter_grads(bf16, X, w->I, V, dA, dY, w->O, f.U, dB, R, r, sc, red, (char*)ws + L.red2, split,
+                        (uint16_t*)((char*)ws + L.split2), tickets, s, parts);
+    if (e == cudaSuccess && (dX || (beside && (dA || dB))))
+      e = launch_int8_product(c, rows, (uint32_t*)ws, &f, s);
+    return e;
   }
   cudaError_t e;
   if (dX && R > 0) e = launch_int8_rows(c, rows, header, s);
@@ -362,7 +383,7 @@ cudaError_t int8_bwd(const qlora_weight* w, const void* X, const void* dY, int64
   if (e == cudaSuccess)
     e = adapter_grads(bf16, X, w->I, V, dA, dY, w->O, U, dB, R, r, sc, red, (char*)ws + L.red2, split,
                       (uint16_t*)((char*)ws + L.split2), tickets, s);
-  if (e == cudaSuccess && R > 0 && dX) e = launch_int8_product(c, rows, (uint32_t*)ws, s);
+  if (e == cudaSuccess && R > 0 && dX) e = launch_int8_product(c, rows, (uint32_t*)ws, nullptr, s);
   return e;
 }
 

@@ -257,157 +257,196 @@ __global__ void __launch_bounds__(kThreads)
 
 // -------------------------------------------------------------- few tokens
 
-// One dot-product job: out[t, j] = sum_k P[t, k] L(k, j), fp32; optionally
-// the rows of P quantized on the way.
+// One dot-product job: out[t, j] = sum_k P[t, k] L(k, j), fp32, for the rows t
+// of P, which may be quantized on the way; and / or the values out (or, with P
+// null, in) split into three bf16 parts, [3][NP][ld] with the tokens along a
+// row, as the column products read them.
 struct FewJob {
   const void* P;
   const float* L;   // [r x K], or [K x r] (kr)
   float* out;       // [R x r]
+  const float* in;  // [R x r], split only
+  uint16_t* parts;  // nullable
   int64_t K;
-  int32_t kr, quantize;
+  int32_t kr, quantize, ctas;
 };
 struct FewArgs {
-  FewJob job[2];    // the second one may be empty (P null)
-  int32_t R, r, groups;
+  FewJob job[2];
+  int32_t R, r, groups, NP;
+  int64_t ld;
   RowsArgs rows;    // of the job that quantizes
 };
 
-// Four consecutive factor entries, zeros from `left` on.
-__device__ __forceinline__ float4 load4(const float* p, int64_t left, bool wide) {
-  if (wide && left >= 4) return __ldg(reinterpret_cast<const float4*>(p));
-  float4 v;
-  v.x = left > 0 ? __ldg(p) : 0.0f;
-  v.y = left > 1 ? __ldg(p + 1) : 0.0f;
-  v.z = left > 2 ? __ldg(p + 2) : 0.0f;
-  v.w = left > 3 ? __ldg(p + 3) : 0.0f;
-  return v;
+__device__ __forceinline__ void put_parts(const FewArgs& a, uint16_t* parts, int64_t t, int j, float v) {
+  // the remainders are exact in fp32
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const __nv_bfloat16 b = __float2bfloat16_rn(v);
+    parts[((int64_t)q * a.NP + j) * a.ld + t] = __bfloat16_as_ushort(b);
+    v -= __bfloat162float(b);
+  }
+  if (t + 1 == a.R)  // zeros up to the row's end: they meet zero rows of P
+    for (int q = 0; q < 3; ++q)
+      for (int64_t e = a.R; e < a.ld; ++e) parts[((int64_t)q * a.NP + j) * a.ld + e] = 0;
 }
 
-// One CTA takes a token and eight columns of its factor; the one with the
-// first eight also quantizes the token.  The rest of the grid clears.  What
-// bounds it is latency: one pass over a row and eight factor rows (or eight
-// columns), a block reduction, and a second pass for the codes.
-template <typename T>
-__global__ void __launch_bounds__(512) few_kernel(const FewArgs a) {
-  constexpr int V = 4;  // consecutive elements a thread takes
-  __shared__ float sums[16][8];
-  __shared__ uint32_t buf[32];
-  if (threadIdx.x == 0) griddep_launch_dependents();
-  const int per = a.R * a.groups, jobs = a.job[1].P ? 2 : 1;
-  const int cta = (int)blockIdx.x;
-  if (cta >= per * jobs) {
-    clear_part(a.rows.clear, cta - per * jobs, (int64_t)gridDim.x - per * jobs);
-    return;
+// V elements of a row from k on (16-byte loads of aligned rows, else one by one).
+template <typename T, bool WIDE>
+__device__ __forceinline__ void few_row(const T* x, int64_t k, int64_t K, float (&v)[8]) {
+  if (WIDE && sizeof(T) == 2) {
+    if (k < K) Vec<__nv_bfloat16>::open(__ldg(reinterpret_cast<const uint4*>(x + k)), v);
+  } else if (WIDE) {
+    if (k < K) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(x + k));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(x + k) + 1);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k + i < K) v[i] = to_f32(x[k + i]);
   }
-  const FewJob& job = a.job[cta / per];
-  const int t = (cta % per) / a.groups, j0 = 8 * ((cta % per) % a.groups);
+}
+
+// A token and eight columns of its factor per CTA; the CTA of the first eight
+// also quantizes the token.  In a wide call K and r are multiples of 8 and 4
+// and everything is 16-byte aligned.  A factor [r x K] is read eight elements
+// a thread, a factor [K x r] one row a thread (eight rows in flight), so that
+// either way neighbouring threads read neighbouring bytes.
+template <typename T, bool KR, bool WIDE>
+__device__ __forceinline__ void few_token(const FewArgs& a, const FewJob& job, int t, int j0, float (*sums)[8],
+                                          uint32_t* buf) {
   const int64_t K = job.K;
   const T* x = (const T*)job.P + t * K;
   const bool quantize = job.quantize && j0 == 0;
-  const bool xw = K % V == 0 && ((uintptr_t)job.P & (V * sizeof(T) - 1)) == 0;
-  const bool lw = ((uintptr_t)job.L & 15) == 0 && (job.kr ? a.r % 4 == 0 : K % 4 == 0);
   const float* f = a.rows.f;
-  const bool fw = f && ((uintptr_t)f & 15) == 0;
-  const int cols = min(8, a.r - j0);
-
-  auto load_x = [&](int64_t k, float (&v)[V]) {
-    if (xw && sizeof(T) == 2) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(x + k));
-      v[0] = __uint_as_float(w.x << 16);
-      v[1] = __uint_as_float(w.x & 0xffff0000u);
-      v[2] = __uint_as_float(w.y << 16);
-      v[3] = __uint_as_float(w.y & 0xffff0000u);
-    } else if (xw) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(x + k));
-      v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = k + i < K ? to_f32(x[k + i]) : 0.0f;
-    }
-  };
-  auto scaled = [&](int64_t k, const float (&v)[V], float (&y)[V]) {
-    if (!f) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) y[i] = v[i];
-      return;
-    }
-    const float4 w = load4(f + k, K - k, fw);
-    y[0] = __fmul_rn(v[0], w.x);
-    y[1] = __fmul_rn(v[1], w.y);
-    y[2] = __fmul_rn(v[2], w.z);
-    y[3] = __fmul_rn(v[3], w.w);
-  };
-
+  const int cols = min(8, a.r - j0), threads = (int)blockDim.x;
   float acc[8] = {};
   uint32_t top = 0;
-  for (int64_t k = (int64_t)threadIdx.x * V; k < K; k += 512 * V) {
-    float v[V];
-    load_x(k, v);
-    if (job.kr) {
-      float4 l[V][2];
+  for (int64_t base = 0; base < K; base += threads * 8) {
+    float v[8] = {};
+    if (KR) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float* p = job.L + (k + i) * a.r + j0;
-        const int64_t left = k + i < K ? cols : 0;
-        l[i][0] = load4(p, left, lw);
-        l[i][1] = load4(p + 4, left - 4, lw);
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float m[8] = {l[i][0].x, l[i][0].y, l[i][0].z, l[i][0].w,
-                            l[i][1].x, l[i][1].y, l[i][1].z, l[i][1].w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = fmaf(v[i], m[j], acc[j]);
+      for (int i = 0; i < 8; ++i) {
+        const int64_t k = base + threads * i + threadIdx.x;
+        if (k < K) v[i] = to_f32(x[k]);
       }
     } else {
-      float4 l[8];
+      few_row<T, WIDE>(x, base + (int64_t)threadIdx.x * 8, K, v);
+    }
+    float l[8][8];
+    if (KR) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t k = base + threads * i + threadIdx.x;
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (k < K) {
+            const float* p = job.L + k * a.r + j0 + j;
+            if (WIDE) {
+              if (j < cols) w = __ldg(reinterpret_cast<const float4*>(p));
+            } else {
+              if (j < cols) w.x = __ldg(p);
+              if (j + 1 < cols) w.y = __ldg(p + 1);
+              if (j + 2 < cols) w.z = __ldg(p + 2);
+              if (j + 3 < cols) w.w = __ldg(p + 3);
+            }
+          }
+          l[i][j] = w.x; l[i][j + 1] = w.y; l[i][j + 2] = w.z; l[i][j + 3] = w.w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = fmaf(v[i], l[i][j], acc[j]);
+    } else {
+      const int64_t k = base + (int64_t)threadIdx.x * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l[j][i] = 0.0f;
+        if (j < cols) few_row<float, WIDE>(job.L + (int64_t)(j0 + j) * K, k, K, l[j]);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        l[j] = load4(job.L + (int64_t)(j0 + j) * K + k, j < cols ? K - k : 0, lw);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        acc[j] = fmaf(v[3], l[j].w, fmaf(v[2], l[j].z, fmaf(v[1], l[j].y, fmaf(v[0], l[j].x, acc[j]))));
+        for (int i = 0; i < 8; ++i) acc[j] = fmaf(v[i], l[j][i], acc[j]);
     }
     if (quantize) {
-      float y[V];
-      scaled(k, v, y);
 #pragma unroll
-      for (int i = 0; i < V; ++i) top = max(top, __float_as_uint(fabsf(y[i])));
+      for (int i = 0; i < 8; ++i) {
+        const int64_t k = KR ? base + threads * i + threadIdx.x : base + (int64_t)threadIdx.x * 8 + i;
+        float y = v[i];
+        if (f && k < K) y = __fmul_rn(y, __ldg(f + k));
+        top = max(top, __float_as_uint(fabsf(y)));
+      }
     }
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
-  const int warp = threadIdx.x >> 5;
   if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sums[warp][j] = acc[j];
+    for (int j = 0; j < 8; ++j) sums[threadIdx.x >> 5][j] = acc[j];
   }
   top = block_max_bits(top, buf);
   if ((int)threadIdx.x < cols) {
     float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) s += sums[w][threadIdx.x];
+    for (int w = 0; w < threads / 32; ++w) s += sums[w][threadIdx.x];
     job.out[(int64_t)t * a.r + j0 + threadIdx.x] = s;
+    if (job.parts) put_parts(a, job.parts, t, j0 + threadIdx.x, s);
   }
   if (!quantize) return;
   const float s = row_scale(top);
   const float inv = reciprocal(s);
   if (threadIdx.x == 0) a.rows.scale[t] = s;
-  uint32_t* q = reinterpret_cast<uint32_t*>(a.rows.codes + t * a.rows.pitch);
-  for (int64_t k = (int64_t)threadIdx.x * V; k < a.rows.pitch; k += 512 * V) {
-    uint32_t c = 0;
-    if (k < K) {
-      float v[V], y[V];
-      load_x(k, v);
-      scaled(k, v, y);
+  uint2* q = reinterpret_cast<uint2*>(a.rows.codes + t * a.rows.pitch);
+  for (int64_t k = (int64_t)threadIdx.x * 8; k < a.rows.pitch; k += threads * 8) {
+    float v[8] = {};
+    uint32_t c[2] = {0, 0};
+    few_row<T, WIDE>(x, k, K, v);
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (k + i < K) c |= code_of(y[i], s, inv) << (8 * i);
+    for (int i = 0; i < 8; ++i) {
+      if (k + i < K) {
+        const float y = f ? __fmul_rn(v[i], __ldg(f + k + i)) : v[i];
+        c[i >> 2] |= code_of(y, s, inv) << (8 * (i & 3));
+      }
     }
-    q[k / 4] = c;
+    q[k / 8] = make_uint2(c[0], c[1]);
   }
+}
+
+// Latency is what bounds it: one pass over a row beside eight factor rows (or
+// columns), a block reduction, and a second pass for the codes.  The last CTAs
+// of the grid clear.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(512) few_kernel(const FewArgs a) {
+  __shared__ float sums[16][8];
+  __shared__ uint32_t buf[32];
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  int cta = (int)blockIdx.x;
+  for (int k = 0; k < 2; ++k) {
+    const FewJob& job = a.job[k];
+    if (cta >= job.ctas) {
+      cta -= job.ctas;
+      continue;
+    }
+    if (!job.P) {
+      const int64_t n = (int64_t)a.R * a.r;
+      for (int64_t e = (int64_t)cta * blockDim.x + threadIdx.x; e < n; e += (int64_t)job.ctas * blockDim.x)
+        put_parts(a, job.parts, e / a.r, (int)(e % a.r), __ldg(job.in + e));
+      return;
+    }
+    const int t = cta / a.groups, j0 = 8 * (cta % a.groups);
+    if (job.kr) few_token<T, true, WIDE>(a, job, t, j0, sums, buf);
+    else few_token<T, false, WIDE>(a, job, t, j0, sums, buf);
+    return;
+  }
+  const int used = a.job[0].ctas + a.job[1].ctas;
+  clear_part(a.rows.clear, cta, (int64_t)gridDim.x - used);
 }
 
 struct Layout {
@@ -475,29 +514,49 @@ cudaError_t launch_int8_rows(const Int8Call& c, void* ws, Int8Clear header, cuda
   return c.bf16 ? launch_rows<__nv_bfloat16>(a, st) : launch_rows<float>(a, st);
 }
 
-cudaError_t launch_int8_product(const Int8Call& c, void* ws, uint32_t* hdr, cudaStream_t st) {
+cudaError_t launch_int8_product(const Int8Call& c, void* ws, uint32_t* hdr, const Int8Few* few,
+                                cudaStream_t st) {
   const Layout l = layout(c.R, c.dx ? c.O : c.I);
-  return launch_int8_tc(c, (const int8_t*)ws + l.codes, (const float*)((char*)ws + l.scale), nullptr,
+  return launch_int8_tc(c, (const int8_t*)ws + l.codes, (const float*)((char*)ws + l.scale), few,
                         (char*)ws + l.total, hdr, st);
 }
 
-cudaError_t launch_int8_few(const Int8Call& c, const Int8Few& f, void* ws, Int8Clear header, uint32_t* hdr,
+bool int8_few_applies(int64_t R, int64_t K, int32_t r) {
+  // every CTA reads eight factor rows from L2: up to 48 MB, about what the
+  // separate launches cost in latency
+  return R <= kInt8Few || R * ((r + 7) / 8) * K <= (int64_t)48 * 1024 * 1024 / 32;
+}
+
+cudaError_t launch_int8_few(const Int8Call& c, const Int8Few& f, void* ws, Int8Clear header,
                             cudaStream_t st) {
   FewArgs a = {};
   a.rows = rows_args(c, ws, header);
   a.R = (int32_t)c.R;
   a.r = c.r;
   a.groups = (c.r + 7) / 8;
-  a.job[0] = {c.P, f.F, f.T, a.rows.K, c.dx ? 1 : 0, 1};
-  if (f.U_new) a.job[1] = {f.X, f.A, f.U_new, c.I, 0, 0};
-  const unsigned ctas = (unsigned)(a.R * a.groups * (f.U_new ? 2 : 1)) + clear_ctas(a.rows.clear);
-  if (c.bf16) few_kernel<__nv_bfloat16><<<ctas, 512, 0, st>>>(a);
-  else few_kernel<float><<<ctas, 512, 0, st>>>(a);
+  a.NP = f.NP;
+  a.ld = f.ld;
+  if (f.T)
+    a.job[0] = {c.P, f.F, f.T, nullptr, f.T_parts, a.rows.K, c.dx ? 1 : 0, c.out ? 1 : 0, a.R * a.groups};
+  if (f.U_new) a.job[1] = {f.X, f.A, f.U_new, nullptr, f.U_parts, c.I, 0, 0, a.R * a.groups};
+  else if (f.U_parts)
+    a.job[1] = {nullptr, nullptr, nullptr, f.U, f.U_parts, 0, 0, 0, (int32_t)((c.R * c.r + 4095) / 4096)};
+  const int64_t K = f.U_new && c.I > a.rows.K ? c.I : a.rows.K;
+  bool wide = c.r % 4 == 0;
+  for (const FewJob& job : a.job)
+    if (job.P && (job.K % 8 != 0 || (uintptr_t)job.P % 16 != 0 || (uintptr_t)job.L % 16 != 0)) wide = false;
+  int threads = (int)((K + 255) / 256) * 32;
+  threads = threads < 128 ? 128 : threads > 512 ? 512 : threads;
+  const unsigned ctas = (unsigned)(a.job[0].ctas + a.job[1].ctas) + clear_ctas(a.rows.clear);
+  if (c.bf16) {
+    if (wide) few_kernel<__nv_bfloat16, true><<<ctas, threads, 0, st>>>(a);
+    else few_kernel<__nv_bfloat16, false><<<ctas, threads, 0, st>>>(a);
+  } else {
+    if (wide) few_kernel<float, true><<<ctas, threads, 0, st>>>(a);
+    else few_kernel<float, false><<<ctas, threads, 0, st>>>(a);
+  }
   count_launch();
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const Layout l = layout(c.R, a.rows.K);
-  return launch_int8_tc(c, a.rows.codes, a.rows.scale, &f, (char*)ws + l.total, hdr, st);
+  return cudaGetLastError();
 }
 
 }  // namespace qlora

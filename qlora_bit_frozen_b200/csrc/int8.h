@@ -35,7 +35,7 @@ struct Int8Call {
   const float* L;        // B [O x r] or A [r x I]
   int32_t r;
   float s;
-  void* out;             // [R x N]
+  void* out;             // [R x N], nullable in the input gradient: nothing is multiplied
 };
 size_t int8_ws(bool dx, int64_t R, int64_t O, int64_t I, int32_t r);
 
@@ -47,26 +47,30 @@ struct Int8Clear {
 // Quantizes the activation rows into the workspace ws (int8_ws bytes), clears
 // `header` and what the product adds up in.
 cudaError_t launch_int8_rows(const Int8Call& c, void* ws, Int8Clear header, cudaStream_t st);
-// The product, over rows quantized before it, once T is computed.
-cudaError_t launch_int8_product(const Int8Call& c, void* ws, uint32_t* hdr, cudaStream_t st);
-
-// Up to this many tokens, two launches do the whole call: one quantizes the
-// rows and takes T (and, in the backward, U) by fp32 dot products, the other
-// multiplies and, in the backward, adds up dA and dB beside it.
+// Few tokens: one launch does the same and takes T (and, in the backward, U)
+// by fp32 dot products.
 constexpr int64_t kInt8Few = 16;
+bool int8_few_applies(int64_t R, int64_t K, int32_t r);
 struct Int8Few {
-  const float* F;    // factor of T: A [r x I] (forward) or B [O x r] (backward)
-  float* T;          // [R x r]
-  // backward only (each nullable)
-  const void* X;     // [R x I]
-  const float* A;    // where U is to be computed: its factor
-  float* U_new;      // and its place
-  const float* U;    // [R x r] for dB
-  float* dA;         // [r x I]
-  float* dB;         // [O x r]
+  const float* F;      // factor of T: A [r x I] (forward) or B [O x r] (backward)
+  float* T;            // [R x r] (null: not wanted)
+  uint16_t* T_parts;   // nullable: T in three bf16 parts, [3][NP][ld]
+  // backward only
+  const void* X;       // [R x I]
+  const float* A;      // where U is to be computed: its factor
+  float* U_new;        // and its place (else null)
+  const float* U;      // [R x r] for dB
+  uint16_t* U_parts;   // nullable, as T_parts
+  float* dA;           // [r x I]: what the product kernel adds up beside its
+  float* dB;           // [O x r]  products, up to kInt8Few tokens (nullable)
+  int32_t NP;
+  int64_t ld;
 };
-cudaError_t launch_int8_few(const Int8Call& c, const Int8Few& f, void* ws, Int8Clear header, uint32_t* hdr,
-                            cudaStream_t st);
+cudaError_t launch_int8_few(const Int8Call& c, const Int8Few& f, void* ws, Int8Clear header, cudaStream_t st);
+// The product, over rows quantized before it, once T is computed; few:
+// nullable, dA and dB.
+cudaError_t launch_int8_product(const Int8Call& c, void* ws, uint32_t* hdr, const Int8Few* few,
+                                cudaStream_t st);
 
 // int8_tc.cu: the product over codes xq [R x int8_pitch(K)] with row scales
 // xs; ws: int8_tc_ws bytes, of which the first int8_tc_zeroed are zero; few:

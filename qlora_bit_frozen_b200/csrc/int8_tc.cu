@@ -538,7 +538,8 @@ struct StreamCfg {
   static constexpr int kSmem = 1024 + kStages * kStage + kSide + 512;
   static_assert(kSmem <= 227 * 1024 && kSmem > 114 * 1024, "one CTA per SM");
 };
-constexpr int kStreamThreads = 192;  // producer, MMA issuer, four epilogue warps
+constexpr int kStreamEpi = 256;  // epilogue threads: two warps to a TMEM lane quarter
+constexpr int kStreamThreads = 64 + kStreamEpi;  // after the producer and the MMA issuer
 
 struct StreamArgs {
   Epi e = {};
@@ -567,7 +568,7 @@ struct SideSums {
   __device__ __forceinline__ SideSums(const StreamArgs& p, int et) {
     nA = p.dA ? p.I : 0;
     total = nA + (p.dB ? p.O : 0);
-    e = (int64_t)blockIdx.x * 128 + et;
+    e = (int64_t)blockIdx.x * kStreamEpi + et;
     load(p);
   }
   __device__ __forceinline__ void load(const StreamArgs& p) {
@@ -595,7 +596,7 @@ struct SideSums {
         float d[4] = {};
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
-          if (t < R) {
+          if (t < R) {  // rows past R of sV, sU are not filled
             const float4 v = *reinterpret_cast<const float4*>(f + t * RT + j);
             d[0] = fmaf(v.x, x[t], d[0]);
             d[1] = fmaf(v.y, x[t], d[1]);
@@ -607,7 +608,7 @@ struct SideSums {
         for (int i = 0; i < 4; ++i)
           if (j + i < r) out[(j + i) * step] = d[i];
       }
-      e += (int64_t)gridDim.x * 128;
+      e += (int64_t)gridDim.x * kStreamEpi;
       load(p);
     }
   }
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&acc_full[b]), 1);
-      mbar_init(smem_u32(&acc_empty[b]), 4);
+      mbar_init(smem_u32(&acc_empty[b]), kStreamEpi / 32);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -776,30 +777,31 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     }
   } else {
     // epilogue: lane = output n, TMEM column = token
-    const int quad = warp & 3, et = (int)threadIdx.x - 64;
+    // (two warps to a quarter take runs of eight tokens in turn)
+    const int quad = warp & 3, et = (int)threadIdx.x - 64, c_first = 8 * ((warp - 2) >> 2);
     SideSums sums(p, et);
     griddep_wait();
     int b = 0;
     uint32_t pa = 0;
     int staged = -1;  // token tile whose T and scales are in shared memory
     auto stage_side = [&](int64_t t0, int toks) {
-      for (int e = et; e < toks * RT; e += 128) {
+      for (int e = et; e < toks * RT; e += kStreamEpi) {
         const int t = e / RT, j = e % RT;
         side[e] = j < p.e.r ? p.e.s * __ldg(p.e.T + (t0 + t) * p.e.r + j) : 0.0f;
       }
-      for (int e = et; e < toks; e += 128) side[BN * RT + e] = __ldg(p.e.xs + t0 + e);
+      for (int e = et; e < toks; e += kStreamEpi) side[BN * RT + e] = __ldg(p.e.xs + t0 + e);
     };
     if constexpr (BN == 16 && DX) {
       if (p.dA || p.dB) {  // a single token tile
         float* su = side + BN * (RT + 1);
         stage_side(0, (int)p.e.R);
         if (p.dB)
-          for (int e = et; e < (int)p.e.R * RT; e += 128) {
+          for (int e = et; e < (int)p.e.R * RT; e += kStreamEpi) {
             const int t = e / RT, j = e % RT;
             su[e] = j < p.e.r ? p.e.s * __ldg(p.U + t * p.e.r + j) : 0.0f;
           }
         staged = 0;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(kStreamEpi) : "memory");
         sums.template run<RT>(p, side, su);
       }
     }
@@ -825,12 +827,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       }
       const float sw = !DX && in ? __ldg(p.e.ws + n) : 1.0f;
       if (tt != staged) {
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // the last tile's are read
+        asm volatile("bar.sync 1, %0;" ::"n"(kStreamEpi) : "memory");  // the last tile's are read
         stage_side(t0, toks);
         staged = tt;
       }
-      // one answer for all four warps, which meet at barriers below
-      if (!all_epilogue<128>(mbar_wait(smem_u32(&acc_full[b]), pa, p.e.wait_ns, p.e.err, 0x604))) {
+      // one answer for all warps, which meet at barriers below
+      if (!all_epilogue<kStreamEpi>(mbar_wait(smem_u32(&acc_full[b]), pa, p.e.wait_ns, p.e.err, 0x604))) {
         *abort_flag = 1;
         break;
       }
@@ -841,7 +843,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       bool finish = whole;
       if (!whole) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < toks; c0 += 8) {
+        for (int c0 = c_first; c0 < toks; c0 += 16) {
           uint32_t acc[8];
           tmem_ld_32x32b_x8(acc0 + (uint32_t)c0, acc);
           tmem_ld_wait();
@@ -850,19 +852,19 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             if (c0 + j < toks) atomicAdd(part + (c0 + j) * 128, (int)acc[j]);
         }
         __threadfence();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(kStreamEpi) : "memory");
         if (warp == 2 && lane == 0)
           *last_flag = atomicAdd(p.tickets + tile, (uint32_t)steps) + (uint32_t)steps == (uint32_t)p.KB;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(kStreamEpi) : "memory");
         finish = *last_flag != 0;
         __threadfence();
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // all have read the flag
+        asm volatile("bar.sync 1, %0;" ::"n"(kStreamEpi) : "memory");  // all have read the flag
       }
       if (finish) {
         // eight tokens at a time (columns past the last token hold sums of
         // zero-filled rows and are not stored)
 #pragma unroll 1
-        for (int c0 = 0; c0 < toks; c0 += 8) {
+        for (int c0 = c_first; c0 < toks; c0 += 16) {
           uint32_t acc[8];
           if (whole) {
             tmem_ld_32x32b_x8(acc0 + (uint32_t)c0, acc);
@@ -1084,13 +1086,19 @@ cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& b
     a.tiles_n = (int32_t)up(e.N, 256);
     return go_pair<DX, OUT, RT>(pl, mx, mw, mo, a, st);
   }
-  constexpr int SRT = RT <= 16 ? 16 : 64;
+  constexpr int SRT = RT <= 16 ? RT : 64;
   StreamArgs a = {};
   a.e = e;
   a.KB = (int32_t)up(K, kBK);
   a.tok_tiles = (int32_t)up(c.R, pl.bn);
   a.tiles = pl.tiles;
   a.shared = pl.shared ? 1 : 0;
+  Plan run = pl;
+  if (!c.out) {  // only the side sums
+    a.tiles = 0;
+    const int64_t want = up(c.I + c.O, kStreamEpi);
+    run.ctas = (int)(want < sm_count() ? want : sm_count());
+  }
   a.part = (int32_t*)ws;
   a.tickets = (uint32_t*)((char*)ws + stream_part_bytes(pl));
   if (few && DX) {
@@ -1103,10 +1111,10 @@ cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& b
     a.O = c.O;
   }
   switch (pl.bn) {
-    case 16: return go_stream<DX, 16, SRT>(pl, mx, mw, a, st);
-    case 32: return go_stream<DX, 32, SRT>(pl, mx, mw, a, st);
-    case 64: return go_stream<DX, 64, SRT>(pl, mx, mw, a, st);
-    default: return go_stream<DX, 128, SRT>(pl, mx, mw, a, st);
+    case 16: return go_stream<DX, 16, SRT>(run, mx, mw, a, st);
+    case 32: return go_stream<DX, 32, SRT>(run, mx, mw, a, st);
+    case 64: return go_stream<DX, 64, SRT>(run, mx, mw, a, st);
+    default: return go_stream<DX, 128, SRT>(run, mx, mw, a, st);
   }
 }
 

@@ -120,7 +120,13 @@ cudaError_t launch_coldot_pair(const void* PA, int64_t NA, const float* auxA, bo
                                float* outA, void* wsA, uint16_t* splitA, const void* PB,
                                int64_t NB, const float* auxB, bool out_nrB, float* outB, void* wsB,
                                uint16_t* splitB, int64_t R, int32_t r, float s, cudaStream_t st,
-                               unsigned* tickets, bool* done, int parts = 2);
+                               unsigned* tickets, bool* done, int parts = 2,
+                               bool split_done = false);
+// split_done: splitA and splitB hold the three parts already (rows of
+// adapter_split_ld(R) along R).
+bool coldot_takes(const void* P, int64_t R, int64_t N);
+int adapter_rank_rows(int32_t r);
+inline int64_t adapter_split_ld(int64_t extent) { return (extent + 7) / 8 * 8; }
 // out = scale * sum of the split partials.  pdl: launched with a
 // programmatic dependency on the kernel before it (which must have
 // triggered its dependents); the kernel waits for that grid first.

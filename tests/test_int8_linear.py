@@ -162,8 +162,10 @@ def test_forward_and_backward(R, O, I, r, dtype):
         close(dB, c * dY64.T @ u, c * (rel * dY64.abs().T @ u.abs() + dY64.abs().T @ du) * 1.001)
 
 
-def test_parts_of_the_gradient_alone():
-    W, X, dY, A, B = make(40, 96, 80, 8, BF)
+@pytest.mark.parametrize("R", [1, 40, 2000])
+@pytest.mark.parametrize("r", [8, 20])
+def test_parts_of_the_gradient_alone(R, r):
+    W, X, dY, A, B = make(R, 1096, 80, r, BF)
     w, _, _ = weight(W)
     full = q.qlora_linear_bwd(w, X, dY, A, B, 16.0)
     for k in range(3):
