@@ -18,6 +18,8 @@
 namespace qlora {
 namespace {
 
+using namespace int8;
+
 constexpr int kThreads = 256;
 
 // Largest of non-negative values by their bits, so that a NaN wins over all.
@@ -36,23 +38,67 @@ __device__ __forceinline__ float row_scale(uint32_t top) {
   return top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(top), 127.0f);
 }
 
-// Code of x as the low byte of the result: rint(fl(x / s)).  The product with
-// the reciprocal is within 2^-15 of the quotient (at most 127 in magnitude,
-// two roundings), so it rounds to the same integer unless it lies that close
-// to a half; only then (and for scales whose reciprocal is not a normal
-// number: inv is NaN) is the division done.  Adding 1.5 2^23 rounds to the
-// nearest integer, ties to even, and leaves it in the low bits.
-__device__ __forceinline__ uint32_t code_of(float x, float s, float inv) {
-  const float y = __fmul_rn(x, inv);
-  float t = __fadd_rn(y, 12582912.0f);
-  if (!(fabsf(__fsub_rn(y, __fsub_rn(t, 12582912.0f))) < 0.49995f)) {
-    const float q = s > 0.0f ? fminf(fmaxf(__fdiv_rn(x, s), -127.0f), 127.0f) : 0.0f;
-    t = __fadd_rn(q, 12582912.0f);
-  }
-  return __float_as_uint(t) & 255u;
+// Code of x: rint(fl(x / s)), by division.
+__device__ __forceinline__ uint32_t code_exact(float x, float s) {
+  const float q = s > 0.0f ? fminf(fmaxf(__fdiv_rn(x, s), -127.0f), 127.0f) : 0.0f;
+  return __float_as_uint(__fadd_rn(q, 12582912.0f));
 }
+
+// Reciprocal of the scale; NaN where it is not a normal number.
 __device__ __forceinline__ float reciprocal(float s) {
   return s >= 1e-37f ? __fdiv_rn(1.0f, s) : __uint_as_float(0x7fc00000u);
+}
+
+// Two fp32 operations in one instruction, each rounded to nearest.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ float lo_of(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float hi_of(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// max(|a|, |b|, |c|); a NaN wins.
+__device__ __forceinline__ float top3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Codes of N values (in pairs), packed.  With M = 1.5 2^23 the sum x inv + M,
+// rounded once, is M plus the integer nearest to x inv (ties to even), and its
+// low byte is that integer.  x inv is within 127 2^-24 of the quotient and the
+// quotient's own rounding within half of that, so the definition's integer is
+// another one only where x inv lies within 1.2e-5 of a half; there (3e-5), and
+// for scales without a reciprocal, the division is done.  One test serves all
+// N: a branch for each of them took 36 issue slots an element, this takes 4.
+template <int N>
+__device__ __forceinline__ void codes_of(const uint64_t (&x)[N / 2], float s, float inv, uint32_t (&c)[N / 4]) {
+  const uint64_t inv2 = pair(inv, inv), M = pair(12582912.0f, 12582912.0f), minus = pair(-1.0f, -1.0f);
+  uint32_t t[N];
+  float worst = 0.0f;
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) {
+    const uint64_t r = fma2(x[j], inv2, M);
+    const uint64_t d = fma2(x[j], inv2, fma2(r, minus, M));  // x inv - nearest
+    worst = top3(worst, lo_of(d), hi_of(d));
+    t[2 * j] = (uint32_t)r;
+    t[2 * j + 1] = (uint32_t)(r >> 32);
+  }
+  if (!(worst < 0.49997f)) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) t[j] = code_exact(j & 1 ? hi_of(x[j / 2]) : lo_of(x[j / 2]), s);
+  }
+#pragma unroll
+  for (int j = 0; j < N; j += 4)
+    c[j / 4] = __byte_perm(__byte_perm(t[j], t[j + 1], 0x0040), __byte_perm(t[j + 2], t[j + 3], 0x0040), 0x5410);
 }
 
 // Two runs of 16-byte words to clear for the kernels after, by CTA cta of ctas.
@@ -77,57 +123,79 @@ struct RowsArgs {
   Clear clear;
 };
 
-// 16 bytes of activations as floats (8 bf16 or 4 fp32).
+// 16 bytes of activations as pairs of floats (8 bf16 or 4 fp32).
 template <typename T>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
-  __device__ static void open(uint4 v, float (&x)[8]) {
+  __device__ static void open(uint4 v, uint64_t (&x)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = (uint64_t)(w[i] << 16) | ((uint64_t)(w[i] & 0xffff0000u) << 32);
   }
 };
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  __device__ static void open(uint4 v, float (&x)[4]) {
-    x[0] = __uint_as_float(v.x);
-    x[1] = __uint_as_float(v.y);
-    x[2] = __uint_as_float(v.z);
-    x[3] = __uint_as_float(v.w);
+  __device__ static void open(uint4 v, uint64_t (&x)[2]) {
+    x[0] = (uint64_t)v.x | ((uint64_t)v.y << 32);
+    x[1] = (uint64_t)v.z | ((uint64_t)v.w << 32);
   }
 };
 
+// Largest magnitude of a vector and of `top`; a NaN wins.
+template <typename T>
+__device__ __forceinline__ float top_of(uint4 v, float top) {
+  if (Vec<T>::N == 8) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+    const uint32_t b = *reinterpret_cast<const uint32_t*>(&m);
+    return top3(top, __uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+  }
+  return top3(top3(top, __uint_as_float(v.x), __uint_as_float(v.y)), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+
 // Rows that take 16-byte accesses (K a multiple of 16, P aligned): a thread
 // keeps its NV vectors of the row in registers between the maximum and the
-// codes, so the row is read once; its column factors stay in registers over
-// all the rows the CTA takes, and the next row is on its way while this one
-// is reduced.
+// codes, so the row is read once, and the next row is on its way while this one
+// is reduced.  The column factors of those vectors stay in registers over all
+// the rows that the CTA takes (from shared memory they cost more than a third
+// of the row's time).
+template <int NV, bool FACTOR>
+constexpr int rows_threads() {  // most threads: 64, 85 or 102 registers each
+  return !FACTOR || NV == 1 ? 1024 : NV == 2 ? 768 : 640;
+}
 template <typename T, int NV, bool FACTOR>
-__global__ void __launch_bounds__(512) rows_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(rows_threads<NV, FACTOR>()) rows_kernel(const RowsArgs a) {
   constexpr int N = Vec<T>::N;
   __shared__ uint32_t buf[2][32];
-  const int64_t nvec = a.K / N;
-  float f[FACTOR ? NV * N : 1];
+  const int nvec = (int)(a.K / N);
+  uint64_t f[FACTOR ? NV * N / 2 : 1];
   if (FACTOR) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t v = threadIdx.x + (int64_t)i * blockDim.x;
+      const int v = threadIdx.x + i * blockDim.x;
 #pragma unroll
-      for (int j = 0; j < N; ++j) f[i * N + j] = v < nvec ? __ldg(a.f + v * N + j) : 0.0f;
+      for (int j = 0; j < N / 2; ++j) {
+        const float* p = a.f + (int64_t)v * N + 2 * j;
+        f[i * (N / 2) + j] = v < nvec ? pair(__ldg(p), __ldg(p + 1)) : 0;
+      }
     }
   }
+  auto scaled = [&](uint4 w, int i, uint64_t (&x)[N / 2]) {  // vector i of the thread times its factors
+    Vec<T>::open(w, x);
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) x[j] = mul2(x[j], f[i * (N / 2) + j]);
+  };
   uint4 next[NV];
   auto load = [&](int64_t row) {
     const uint4* x = reinterpret_cast<const uint4*>((const T*)a.P + row * a.K);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t v = threadIdx.x + (int64_t)i * blockDim.x;
+      const int v = threadIdx.x + i * blockDim.x;
       next[i] = v < nvec ? __ldg(x + v) : make_uint4(0, 0, 0, 0);
     }
   };
@@ -136,39 +204,39 @@ __global__ void __launch_bounds__(512) rows_kernel(const RowsArgs a) {
   clear_part(a.clear, blockIdx.x, gridDim.x);
   for (int k = 0; row < a.R; k ^= 1) {
     uint4 cur[NV];
-    uint32_t top = 0;
+    float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       cur[i] = next[i];
-      float x[N];
-      Vec<T>::open(cur[i], x);
+      if (FACTOR) {
+        uint64_t x[N / 2];
+        scaled(cur[i], i, x);
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        top = max(top, __float_as_uint(fabsf(FACTOR ? __fmul_rn(x[j], f[i * N + j]) : x[j])));
+        for (int j = 0; j < N / 2; ++j) top = top3(top, lo_of(x[j]), hi_of(x[j]));
+      } else {
+        top = top_of<T>(cur[i], top);
+      }
     }
     const int64_t now = row;
     row += gridDim.x;
     if (row < a.R) load(row);
-    top = block_max_bits(top, buf[k]);
-    const float s = row_scale(top);
+    const uint32_t bits = block_max_bits(__float_as_uint(top), buf[k]);
+    const float s = row_scale(bits);
     const float inv = reciprocal(s);
     if (threadIdx.x == 0) {
       a.scale[now] = s;
-      if (a.hdr && top >= 0x7f800000u) atomicOr(a.hdr + 2, 1u);
+      if (a.hdr && bits >= 0x7f800000u) atomicOr(a.hdr + 2, 1u);
     }
     uint32_t* q = reinterpret_cast<uint32_t*>(a.codes + now * a.pitch);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t v = threadIdx.x + (int64_t)i * blockDim.x;
-      float x[N];
-      uint32_t c[N / 4];
-      Vec<T>::open(cur[i], x);
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const uint32_t b = code_of(FACTOR ? __fmul_rn(x[j], f[i * N + j]) : x[j], s, inv);
-        c[j / 4] = j % 4 == 0 ? b : c[j / 4] | (b << (8 * (j % 4)));
-      }
+      const int v = threadIdx.x + i * blockDim.x;
       if (v < nvec) {
+        uint32_t c[N / 4];
+        uint64_t x[N / 2];
+        if (FACTOR) scaled(cur[i], i, x);
+        else Vec<T>::open(cur[i], x);
+        codes_of<N>(x, s, inv, c);
         if (N == 8) reinterpret_cast<uint2*>(q)[v] = make_uint2(c[0], c[N / 4 - 1]);
         else q[v] = c[0];
       }
@@ -191,7 +259,6 @@ __global__ void __launch_bounds__(kThreads) rows_any_kernel(const RowsArgs a) {
   }
   top = block_max_bits(top, buf);
   const float s = row_scale(top);
-  const float inv = reciprocal(s);
   if (threadIdx.x == 0) {
     a.scale[row] = s;
     if (a.hdr && top >= 0x7f800000u) atomicOr(a.hdr + 2, 1u);
@@ -199,7 +266,7 @@ __global__ void __launch_bounds__(kThreads) rows_any_kernel(const RowsArgs a) {
   int8_t* q = a.codes + row * a.pitch;
   for (int64_t k = threadIdx.x; k < a.pitch; k += kThreads) {
     uint32_t c = 0;
-    if (k < a.K) c = code_of(a.f ? __fmul_rn(to_f32(x[k]), a.f[k]) : to_f32(x[k]), s, inv);
+    if (k < a.K) c = code_exact(a.f ? __fmul_rn(to_f32(x[k]), a.f[k]) : to_f32(x[k]), s);
     q[k] = (int8_t)c;
   }
 }
@@ -216,28 +283,26 @@ unsigned clear_ctas(const Clear& c) {
   return (unsigned)(n < 592 ? n : 592);
 }
 
-// Vector rows: up to 512 threads and 8 vectors a thread (fp32 weights of
-// 16384 columns, bf16 activations of 32768).  The CTAs are as many as the SMs
-// hold at once, each over rows in turn; few rows get extra CTAs for clearing.
+// Vector rows: up to four vectors a thread (32768 bf16 or 16384 fp32 columns,
+// 20480 or 10240 with factors).  The CTAs are as many as the SMs hold at once,
+// each over rows in turn; few rows get extra CTAs for clearing.
 template <typename T>
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
-  constexpr int N = Vec<T>::N;
-  const int64_t nvec = a.K / N;
+  const int64_t nvec = a.K / Vec<T>::N;
   const unsigned clear = clear_ctas(a.clear);
-  if (a.K % 16 == 0 && a.K > 0 && (uintptr_t)a.P % 16 == 0 && (uintptr_t)a.codes % 8 == 0 &&
-      nvec <= 8 * 512) {
-    int nv = 1;
-    while (nv < 4 && nvec > (int64_t)nv * 256) nv *= 2;
-    if (nvec > (int64_t)nv * 512) nv = 8;
+  const bool wide = a.K % 16 == 0 && a.K > 0 && (uintptr_t)a.P % 16 == 0 && (uintptr_t)a.codes % 8 == 0;
+  if (wide && nvec <= 4 * (a.f ? rows_threads<4, true>() : 1024)) {
+    // more vectors a thread, more warps to the SM: two with factors as long as
+    // 768 threads reach, else four from 512 vectors on
+    const int nv = nvec <= 256 ? 1 : nvec <= (a.f ? 2 * 768 : 512) ? 2 : 4;
     const int threads = (int)((nvec + nv - 1) / nv + 31) / 32 * 32;
-    const int64_t most = (int64_t)148 * (1536 / threads);
+    const int64_t most = (int64_t)sm_count() * (2048 / threads);
     unsigned ctas = (unsigned)(a.R < most ? a.R : most);
     if (ctas < clear) ctas = clear;
     switch (nv) {
       case 1: rows_go<T, 1>(a, ctas, threads, st); break;
       case 2: rows_go<T, 2>(a, ctas, threads, st); break;
-      case 4: rows_go<T, 4>(a, ctas, threads, st); break;
-      default: rows_go<T, 8>(a, ctas, threads, st); break;
+      default: rows_go<T, 4>(a, ctas, threads, st); break;
     }
   } else {
     rows_any_kernel<T><<<(unsigned)(a.R > clear ? a.R : clear), kThreads, 0, st>>>(a);
@@ -294,7 +359,15 @@ __device__ __forceinline__ void put_parts(const FewArgs& a, uint16_t* parts, int
 template <typename T, bool WIDE>
 __device__ __forceinline__ void few_row(const T* x, int64_t k, int64_t K, float (&v)[8]) {
   if (WIDE && sizeof(T) == 2) {
-    if (k < K) Vec<__nv_bfloat16>::open(__ldg(reinterpret_cast<const uint4*>(x + k)), v);
+    if (k < K) {
+      uint64_t w[4];
+      Vec<__nv_bfloat16>::open(__ldg(reinterpret_cast<const uint4*>(x + k)), w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = lo_of(w[i]);
+        v[2 * i + 1] = hi_of(w[i]);
+      }
+    }
   } else if (WIDE) {
     if (k < K) {
       const float4 a = __ldg(reinterpret_cast<const float4*>(x + k));
@@ -406,15 +479,17 @@ __device__ __forceinline__ void few_token(const FewArgs& a, const FewJob& job, i
   uint2* q = reinterpret_cast<uint2*>(a.rows.codes + t * a.rows.pitch);
   for (int64_t k = (int64_t)threadIdx.x * 8; k < a.rows.pitch; k += threads * 8) {
     float v[8] = {};
-    uint32_t c[2] = {0, 0};
-    few_row<T, WIDE>(x, k, K, v);
+    uint32_t c[2];
+    few_row<T, WIDE>(x, k, K, v);  // zeros past the row, whose code is 0
+    if (f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (k + i < K) {
-        const float y = f ? __fmul_rn(v[i], __ldg(f + k + i)) : v[i];
-        c[i >> 2] |= code_of(y, s, inv) << (8 * (i & 3));
-      }
+      for (int i = 0; i < 8; ++i)
+        if (k + i < K) v[i] = __fmul_rn(v[i], __ldg(f + k + i));
     }
+    uint64_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = pair(v[2 * i], v[2 * i + 1]);
+    codes_of<8>(y, s, inv, c);
     q[k / 8] = make_uint2(c[0], c[1]);
   }
 }

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "qlora.h"
 
 namespace qlora {
@@ -79,5 +81,35 @@ size_t int8_tc_ws(bool dx, int64_t R, int64_t O, int64_t I, int32_t r);
 size_t int8_tc_zeroed(bool dx, int64_t R, int64_t O, int64_t I);
 cudaError_t launch_int8_tc(const Int8Call& c, const int8_t* xq, const float* xs, const Int8Few* few, void* ws,
                            uint32_t* hdr, cudaStream_t st);
+
+namespace int8 {
+
+constexpr int kMaxDevices = 64;
+
+inline int sm_count() {
+  static std::atomic<int> count[kMaxDevices];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return 148;
+  n = count[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+    count[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Once per kernel and device: the attribute belongs to the device's context.
+template <typename K>
+inline cudaError_t allow_smem(K kern, int bytes, std::atomic<bool>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kMaxDevices && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < kMaxDevices) done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
+}  // namespace int8
 
 }  // namespace qlora

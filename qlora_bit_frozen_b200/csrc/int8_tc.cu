@@ -31,14 +31,14 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <atomic>
-
 #include "common.cuh"
 #include "int8.h"
 #include "internal.h"
 
 namespace qlora {
 namespace {
+
+using namespace int8;
 
 constexpr int kBK = 128;              // K bytes per step
 constexpr int kHalf = 128 * kBK;      // bytes of a 128-row operand tile
@@ -942,32 +942,6 @@ bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t
   return enc(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-constexpr int kMaxDevices = 64;
-
-int sm_count() {
-  static std::atomic<int> count[kMaxDevices];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return 148;
-  n = count[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-    count[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
-// Once per kernel and device: the attribute belongs to the device's context.
-template <typename K>
-cudaError_t allow_smem(K kern, int bytes, std::atomic<bool>* done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < kMaxDevices && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < kMaxDevices) done[dev].store(true, std::memory_order_relaxed);
-  return e;
 }
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }

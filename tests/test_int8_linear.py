@@ -68,7 +68,8 @@ def products(X, A):
     return X @ A.T, (2.0 ** -16 + X.shape[1] * U) * (X.abs() @ A.abs().T)
 
 
-@pytest.mark.parametrize("O,I", [(1, 1), (1, 17), (5, 3), (64, 64), (33, 1000), (1024, 1024), (3, 20000), (700, 4100)])
+@pytest.mark.parametrize("O,I", [(1, 1), (1, 17), (5, 3), (64, 64), (33, 1000), (1024, 1024), (3, 20000), (700, 4100),
+                                 (1300, 4112), (900, 13312), (700, 20000), (1500, 8192)])
 def test_quantize_is_exact(O, I):
     W = normal(3, O, I, std=0.02)
     if O > 2:
@@ -131,7 +132,8 @@ def test_zero_adapter_forward_and_gradient_are_exact(R, O, I):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("r", [1, 8, 13, 16, 32, 64])
-@pytest.mark.parametrize("R,O,I", [(1, 300, 200), (19, 256, 512), (200, 520, 264), (1400, 1030, 300), (2300, 2048, 512)])
+@pytest.mark.parametrize("R,O,I", [(1, 300, 200), (19, 256, 512), (200, 520, 264), (1400, 1030, 300), (2300, 2048, 512),
+                                   (1201, 640, 9216)])
 def test_forward_and_backward(R, O, I, r, dtype):
     W, X, dY, A, B = make(R, O, I, r, dtype, seed=10 + r)
     w, nw, s = weight(W)
