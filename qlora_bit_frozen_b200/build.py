@@ -16,8 +16,9 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libqlora.so")
 
 SOURCES = ["api.cu", "quantize.cu", "simt.cu", "adapter.cu", "tc_gemm.cu", "smallr.cu", "noalloc.cu",
-           "merge.cu", "adam.cu", "int8.cu", "int8_tc.cu", "optim.cu"]
-HEADERS = ["common.cuh", "internal.h", "tc_gemm.h", "smallr.h", "int8.h"]
+           "merge.cu", "adam.cu", "int8.cu", "int8_tc.cu", "int8_side.cu",
+           "optim.cu"]
+HEADERS = ["common.cuh", "internal.h", "tc_gemm.h", "smallr.h", "int8.h", "int8_dev.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]

@@ -398,10 +398,6 @@ __global__ void __launch_bounds__(kThreads) coldot_kernel(const T* __restrict__ 
 // significant bits (relative error <= 2^-16), against 24 in the FMA form.
 // That removes the r FMAs per activation element from the issue slots; the
 // kernels are then bound by HBM on the activation, not by instructions.
-// With three parts (the remainder of the remainder too) the factor keeps all
-// its 24 bits; the tensor core's sums lose a little at every step (measured
-// 1.7e-8 of the result per chained product), so that form starts its sums anew
-// for every stage and adds them up in fp32.
 
 constexpr int kMmaStages = 4;
 constexpr int kMaxTickets = 1024;  // zeroed counters the caller provides
@@ -494,37 +490,10 @@ __device__ __forceinline__ void mma_pairs(float (&c)[4], const uint32_t (&a)[4],
   mma16816(c, a, *reinterpret_cast<const uint32_t*>(l), *reinterpret_cast<const uint32_t*>(l + 8));
 }
 
-__device__ __forceinline__ void ldsm_x2(uint32_t addr, uint32_t (&a)[2]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
-               : "=r"(a[0]), "=r"(a[1])
-               : "r"(addr));
-}
-
-// c[n] += A * (B_0 + B_1 + B_2) for NT n-tiles from a split tile in shared
-// memory at t (part q, column n, k contiguous: t + (q part + n) ls + k, bf16);
-// kb: first column of the 16-column chunk.
-template <int NT>
-__device__ __forceinline__ void mma_thirds(float (&c)[NT][4], const uint32_t (&a)[4], uint32_t t, int ls,
-                                           int part, int kb, int lane) {
-  const uint32_t first = t + (uint32_t)((((lane >> 4) * part + (lane & 7)) * ls + kb + 8 * ((lane >> 3) & 1)) * 2);
-  const uint32_t third = t + (uint32_t)(((2 * part + (lane & 7)) * ls + kb + 8 * ((lane >> 3) & 1)) * 2);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    uint32_t b[4], d[2];
-    ldsm_x4(first + (uint32_t)(8 * n * ls * 2), b);
-    ldsm_x2(third + (uint32_t)(8 * n * ls * 2), d);
-    mma16816(c[n], a, d[0], d[1]);
-    mma16816(c[n], a, b[2], b[3]);
-    mma16816(c[n], a, b[0], b[1]);
-  }
-}
-
 // Split an r-wide fp32 factor into bf16 hi / lo rows, n-major:
 // dst[j * ld + k] = hi, dst[(NP + j) * ld + k] = lo of F(k, j), where
 // F(k, j) = src[k * r + j] (nr = 1, [n x r]) or src[j * n + k] (nr = 0,
-// [r x n]); zero for j >= r or k >= n, up to the row length ld.  Three parts:
-// the remainder after lo in dst[(2 NP + j) * ld + k].
-template <int PARTS>
+// [r x n]); zero for j >= r or k >= n, up to the row length ld.
 __global__ void split_factor_kernel(const float* __restrict__ src, int64_t n, int r, int nr, int NP,
                                     int64_t ld, uint16_t* __restrict__ dst) {
   const int64_t e = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 2;  // (j, k) pair start
@@ -535,15 +504,9 @@ __global__ void split_factor_kernel(const float* __restrict__ src, int64_t n, in
     return nr ? src[kk * r + j] : src[j * n + kk];
   };
   uint32_t h, l;
-  const float x = f(k), y = f(k + 1);
-  split_bf16(x, y, h, l);
+  split_bf16(f(k), f(k + 1), h, l);
   *reinterpret_cast<uint32_t*>(dst + j * ld + k) = h;
   *reinterpret_cast<uint32_t*>(dst + ((int64_t)NP + j) * ld + k) = l;
-  if (PARTS == 3) {  // both differences are exact in fp32
-    const float x2 = (x - __uint_as_float(h << 16)) - __uint_as_float(l << 16);
-    const float y2 = (y - __uint_as_float(h & 0xFFFF0000u)) - __uint_as_float(l & 0xFFFF0000u);
-    *reinterpret_cast<uint32_t*>(dst + ((int64_t)2 * NP + j) * ld + k) = pack_bf16x2(x2, y2);
-  }
 }
 
 // rowdot on the tensor cores: out[m, j] = sum_k P[m, k] L(k, j).
@@ -563,7 +526,7 @@ constexpr int colmma_rt(int nt) { return nt >= 4 ? 32 : 64; }
 // Factor modes: FM 0 fp32 [r x K] rows (A), FM 1 fp32 [K x r] (B), FM 2 the
 // factor already split into bf16 hi / lo rows [2][NP][lstride] (n-major,
 // zero past r and K) by split_factor_kernel: B fragments are then plain
-// bf16 pairs, no per-warp split arithmetic; FM 3 the same in three parts.
+// bf16 pairs, no per-warp split arithmetic.
 template <int NT, int FM>
 struct RowMma {
   static constexpr bool LKR = FM == 1;
@@ -574,7 +537,7 @@ struct RowMma {
   static constexpr int PB = RB * PSTR;
   static constexpr int LSTRF = KT + 8;                 // floats per L row ([r x K] case)
   static constexpr int LSTRH = KT + 8;                 // bf16 per split row (FM 2)
-  static constexpr int LB = FM >= 2 ? FM * NP * LSTRH * 2 : LKR ? KT * NP * 4 : NP * LSTRF * 4;
+  static constexpr int LB = FM == 2 ? 2 * NP * LSTRH * 2 : LKR ? KT * NP * 4 : NP * LSTRF * 4;
   static constexpr int STAGE = PB + LB;
   static constexpr int TSTR = NP + 1;                  // result tile row stride (floats)
   static constexpr int RED = 4 * 32 * NT * 4 * 4;      // K-group combine buffer
@@ -617,9 +580,9 @@ __global__ void __launch_bounds__(kThreads) rowdot_mma_kernel(
       const uint32_t nb = (m < R && rem > 0) ? (uint32_t)min((int64_t)16, rem) : 0u;
       cp_async16(ps + (uint32_t)(row * C::PSTR + ch * 16), nb ? (const void*)(P + m * K + k) : (const void*)P, nb);
     }
-    if (FM >= 2) {  // split rows: FM x NP rows of KT bf16
+    if (FM == 2) {  // split rows: 2 x NP rows of KT bf16
       const uint16_t* Ls = reinterpret_cast<const uint16_t*>(L);
-      for (int c = threadIdx.x; c < FM * C::NP * (C::KT / 8); c += kThreads) {
+      for (int c = threadIdx.x; c < 2 * C::NP * (C::KT / 8); c += kThreads) {
         const int row = c / (C::KT / 8), ch = c % (C::KT / 8);
         const int64_t k = k0 + ch * 8;
         const int64_t rem = (lstride - k) * 2;
@@ -667,16 +630,14 @@ __global__ void __launch_bounds__(kThreads) rowdot_mma_kernel(
     const uint8_t* stage = sm + ((t - t_lo) % kMmaStages) * C::STAGE;
     const uint32_t ps = (uint32_t)__cvta_generic_to_shared(stage);
     const float* ls = (const float*)(stage + C::PB);
-    float fresh[FM == 3 ? NT : 1][4] = {};
 #pragma unroll
     for (int q = 0; q < C::KT / 32; ++q) {
       const int kc = 2 * q + kg;  // 16-column chunk
       uint32_t a[4];
       ldsm_x4(ps + (uint32_t)((16 * rg + (lane & 15)) * C::PSTR + (kc * 16 + (lane >> 4) * 8) * 2), a);
       const int kb = kc * 16 + 2 * tq;
-      if constexpr (FM == 3) mma_thirds<NT>(fresh, a, ps + C::PB, C::LSTRH, C::NP, kc * 16, lane);
 #pragma unroll
-      for (int n = 0; n < (FM == 3 ? 0 : NT); ++n) {
+      for (int n = 0; n < NT; ++n) {
         if (FM == 2)
           mma_pairs(c[n], a, reinterpret_cast<const uint16_t*>(ls), C::LSTRH, C::NP * C::LSTRH,
                     8 * n + g, kb);
@@ -686,12 +647,6 @@ __global__ void __launch_bounds__(kThreads) rowdot_mma_kernel(
         else
           mma_split(c[n], a, kb, 8 * n + g, [&](int k, int j) { return ls[j * C::LSTRF + k]; });
       }
-    }
-    if constexpr (FM == 3) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[n][e] += fresh[n][e];
     }
   }
   cp_async_wait<0>();
@@ -757,8 +712,8 @@ __global__ void __launch_bounds__(kThreads) rowdot_mma_kernel(
 // grid = column blocks x row splits, the last block of a column block to
 // finish (ticket) adds the split partials in split order, scales by s and
 // writes dA as [r x N] (out_nr = 0) or dB as [N x r] (out_nr = 1).
-// Aux modes: FM 0 fp32 [R x r]; FM 2, 3 split into bf16 rows (as for the
-// rowdot factor).
+// Aux modes: FM 0 fp32 [R x r]; FM 2 split into bf16 hi / lo rows (as for
+// the rowdot factor).
 template <int NT, int FM>
 struct ColMma {
   static constexpr int NC = 128, RT = colmma_rt(NT);
@@ -766,7 +721,7 @@ struct ColMma {
   static constexpr int PSTR = NC * 2 + 16;
   static constexpr int PB = RT * PSTR;
   static constexpr int ASTRH = RT + 8;                 // bf16 per split row (FM 2)
-  static constexpr int AB = FM >= 2 ? FM * NP * ASTRH * 2 : RT * NP * 4;  // aux tile
+  static constexpr int AB = FM == 2 ? 2 * NP * ASTRH * 2 : RT * NP * 4;  // aux tile
   static constexpr int STAGE = PB + AB;
   static constexpr int TSTR = NP + 1;
   static constexpr int TILE = NC * TSTR * 4;
@@ -828,9 +783,9 @@ __global__ void __launch_bounds__(kThreads) coldot_mma_kernel(const ColJob ja, c
       const uint32_t nb = (m < R && rem > 0) ? (uint32_t)min((int64_t)16, rem) : 0u;
       cp_async16(ps + (uint32_t)(row * C::PSTR + ch * 16), nb ? (const void*)(P + m * N + n) : (const void*)P, nb);
     }
-    if (FM >= 2) {  // split rows: FM x NP rows of RT bf16
+    if (FM == 2) {  // split rows: 2 x NP rows of RT bf16
       const uint16_t* As = reinterpret_cast<const uint16_t*>(aux);
-      for (int c = threadIdx.x; c < FM * C::NP * (C::RT / 8); c += kThreads) {
+      for (int c = threadIdx.x; c < 2 * C::NP * (C::RT / 8); c += kThreads) {
         const int row = c / (C::RT / 8), ch = c % (C::RT / 8);
         const int64_t m = mt + ch * 8;
         const int64_t rem = (astride - m) * 2;
@@ -870,15 +825,13 @@ __global__ void __launch_bounds__(kThreads) coldot_mma_kernel(const ColJob ja, c
     const uint8_t* stage = sm + ((t - t_lo) % kMmaStages) * C::STAGE;
     const uint32_t ps = (uint32_t)__cvta_generic_to_shared(stage);
     const float* as = (const float*)(stage + C::PB);
-    float fresh[FM == 3 ? NT : 1][4] = {};
 #pragma unroll
     for (int kc = 0; kc < C::RT / 16; ++kc) {
       uint32_t a[4];
       ldsm_x4_t(ps + (uint32_t)((kc * 16 + lrow) * C::PSTR + lcol * 2), a);
       const int kb = kc * 16 + 2 * tq;
-      if constexpr (FM == 3) mma_thirds<NT>(fresh, a, ps + C::PB, C::ASTRH, C::NP, kc * 16, lane);
 #pragma unroll
-      for (int n = 0; n < (FM == 3 ? 0 : NT); ++n) {
+      for (int n = 0; n < NT; ++n) {
         if (FM == 2)
           mma_pairs(c[n], a, reinterpret_cast<const uint16_t*>(as), C::ASTRH, C::NP * C::ASTRH,
                     8 * n + g, kb);
@@ -886,12 +839,6 @@ __global__ void __launch_bounds__(kThreads) coldot_mma_kernel(const ColJob ja, c
           mma_split(c[n], a, kb, 8 * n + g,
                     [&](int k, int j) { return j < r ? as[k * r + j] : 0.0f; });
       }
-    }
-    if constexpr (FM == 3) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[n][e] += fresh[n][e];
     }
   }
   cp_async_wait<0>();
@@ -1122,14 +1069,11 @@ cudaError_t rowdot_mma_r(const __nv_bfloat16* P, int64_t R, int64_t K, const flo
 // Split the r-wide factor of one product into bf16 hi / lo rows in `dst`
 // (row length ld = extent rounded up to 8).
 cudaError_t split_factor(const float* src, int64_t extent, int r, bool nr, uint16_t* dst,
-                         int64_t* ld, cudaStream_t st, int parts = 2) {
+                         int64_t* ld, cudaStream_t st) {
   const int NP = 8 * rank_tiles(r);
-  *ld = adapter_split_ld(extent);
+  *ld = (extent + 7) / 8 * 8;
   const int64_t pairs = (int64_t)NP * *ld / 2;
-  if (parts == 3)
-    split_factor_kernel<3><<<cdiv(pairs, 256), 256, 0, st>>>(src, extent, r, nr ? 1 : 0, NP, *ld, dst);
-  else
-    split_factor_kernel<2><<<cdiv(pairs, 256), 256, 0, st>>>(src, extent, r, nr ? 1 : 0, NP, *ld, dst);
+  split_factor_kernel<<<cdiv(pairs, 256), 256, 0, st>>>(src, extent, r, nr ? 1 : 0, NP, *ld, dst);
   count_launch();
   return cudaGetLastError();
 }
@@ -1184,7 +1128,7 @@ cudaError_t launch_rowdot(const void* P, bool bf16, int64_t R, int64_t K, const 
                           bool l_is_kr, int32_t r, float* out, cudaStream_t st, uint16_t* pad,
                           const float* side_src, int64_t side_extent, int side_mode,
                           float side_mul, uint16_t* side_dst, float* lt_ws, float* part_ws,
-                          unsigned* tickets, uint16_t* split_ws, int parts) {
+                          unsigned* tickets, uint16_t* split_ws) {
   PadJob job{side_src, side_dst, side_extent, r, side_mode, side_mul, 0};
   if (side_dst && side_extent > 0) job.blocks = (int)cdiv(64 * side_extent, kThreads * 8);
   if (R > 0 && rowdot_mma_ok(P, bf16, K, L)) {  // tensor cores, either factor layout
@@ -1196,13 +1140,10 @@ cudaError_t launch_rowdot(const void* P, bool bf16, int64_t R, int64_t K, const 
     // 8192 x 4096 and 16384 x 17408 activations).
     // Above rank 8, one small launch splits the factor into bf16 hi / lo
     // rows once, instead of every warp of every block splitting it again.
-    if (split_ws && (rank_tiles(r) >= 2 || parts == 3) && ((uintptr_t)split_ws % 16) == 0) {
+    if (split_ws && rank_tiles(r) >= 2 && ((uintptr_t)split_ws % 16) == 0) {
       int64_t ld = 0;
-      cudaError_t e = split_factor(L, K, r, l_is_kr, split_ws, &ld, st, parts);
+      cudaError_t e = split_factor(L, K, r, l_is_kr, split_ws, &ld, st);
       if (e != cudaSuccess) return e;
-      if (parts == 3)
-        return rowdot_mma_r<3>(Pb, R, K, (const float*)split_ws, ld, r, pl, out, pad, part_ws,
-                               tickets, job, st);
       return rowdot_mma_r<2>(Pb, R, K, (const float*)split_ws, ld, r, pl, out, pad, part_ws,
                              tickets, job, st);
     }
@@ -1240,14 +1181,9 @@ bool coldot_mma_ok(const void* P, bool bf16, int64_t R, int64_t N, const float* 
 
 }  // namespace
 
-bool coldot_takes(const void* P, int64_t R, int64_t N) {
-  return R > 0 && N % 8 == 0 && (uintptr_t)P % 16 == 0;
-}
-int adapter_rank_rows(int32_t r) { return 8 * rank_tiles(r); }
-
-size_t adapter_split_ws(int64_t extent, int32_t r, int parts) {
-  if (rank_tiles(r) < 2 && parts == 2) return 0;
-  return align_up((size_t)parts * 8 * rank_tiles(r) * (size_t)((extent + 7) / 8 * 8) * 2, 256);
+size_t adapter_split_ws(int64_t extent, int32_t r) {
+  if (rank_tiles(r) < 2) return 0;
+  return align_up((size_t)2 * 8 * rank_tiles(r) * (size_t)((extent + 7) / 8 * 8) * 2, 256);
 }
 
 size_t rowdot_ws(int64_t R, int64_t K, int32_t r) {
@@ -1270,26 +1206,18 @@ size_t coldot_ws(int64_t R, int64_t N, int32_t r) {
 
 cudaError_t launch_coldot(const void* P, bool bf16, int64_t R, int64_t N, const float* aux,
                           int32_t r, float s, bool out_nr, float* out, void* ws,
-                          cudaStream_t st, unsigned* tickets, uint16_t* split_ws, int parts) {
+                          cudaStream_t st, unsigned* tickets, uint16_t* split_ws) {
   if (N == 0) return cudaSuccess;
   if (R == 0) return cudaMemsetAsync(out, 0, (size_t)r * (size_t)N * 4, st);
   if (coldot_mma_ok(P, bf16, R, N, aux)) {  // tensor cores
     const MmaPlan pl = coldot_mma_plan(R, N, r, tickets != nullptr);
     const __nv_bfloat16* Pb = (const __nv_bfloat16*)P;
     float* part = (float*)ws;
-    if (split_ws && (rank_tiles(r) >= 2 || parts == 3) && ((uintptr_t)split_ws % 16) == 0) {
+    if (split_ws && rank_tiles(r) >= 2 && ((uintptr_t)split_ws % 16) == 0) {
       int64_t ld = 0;
-      cudaError_t e = split_factor(aux, R, r, true, split_ws, &ld, st, parts);
+      cudaError_t e = split_factor(aux, R, r, true, split_ws, &ld, st);
       if (e != cudaSuccess) return e;
       const float* sp = (const float*)split_ws;
-      if (parts == 3) {
-        switch (rank_tiles(r)) {
-          case 1: return coldot_mma_go<1, 3>(Pb, R, N, sp, ld, r, pl, s, out_nr, out, part, tickets, st);
-          case 2: return coldot_mma_go<2, 3>(Pb, R, N, sp, ld, r, pl, s, out_nr, out, part, tickets, st);
-          case 4: return coldot_mma_go<4, 3>(Pb, R, N, sp, ld, r, pl, s, out_nr, out, part, tickets, st);
-          default: return coldot_mma_go<8, 3>(Pb, R, N, sp, ld, r, pl, s, out_nr, out, part, tickets, st);
-        }
-      }
       switch (rank_tiles(r)) {
         case 2: return coldot_mma_go<2, 2>(Pb, R, N, sp, ld, r, pl, s, out_nr, out, part, tickets, st);
         case 4: return coldot_mma_go<4, 2>(Pb, R, N, sp, ld, r, pl, s, out_nr, out, part, tickets, st);
@@ -1322,7 +1250,7 @@ cudaError_t launch_coldot_pair(const void* PA, int64_t NA, const float* auxA, bo
                                float* outA, void* wsA, uint16_t* splitA, const void* PB,
                                int64_t NB, const float* auxB, bool out_nrB, float* outB, void* wsB,
                                uint16_t* splitB, int64_t R, int32_t r, float s, cudaStream_t st,
-                               unsigned* tickets, bool* done, int parts, bool split_done) {
+                               unsigned* tickets, bool* done) {
   *done = false;
   if (R <= 0 || NA <= 0 || NB <= 0 || !tickets) return cudaSuccess;
   if (!coldot_mma_ok(PA, true, R, NA, auxA) || !coldot_mma_ok(PB, true, R, NB, auxB))
@@ -1332,25 +1260,16 @@ cudaError_t launch_coldot_pair(const void* PA, int64_t NA, const float* auxA, bo
   const __nv_bfloat16* A = (const __nv_bfloat16*)PA;
   const __nv_bfloat16* B = (const __nv_bfloat16*)PB;
   *done = true;
-  if ((rank_tiles(r) >= 2 || parts == 3) && splitA && splitB && ((uintptr_t)splitA % 16) == 0 &&
+  if (rank_tiles(r) >= 2 && splitA && splitB && ((uintptr_t)splitA % 16) == 0 &&
       ((uintptr_t)splitB % 16) == 0) {
-    int64_t lda = adapter_split_ld(R), ldb = lda;
-    cudaError_t e = cudaSuccess;
-    if (!split_done) e = split_factor(auxA, R, r, true, splitA, &lda, st, parts);
-    if (!split_done && e == cudaSuccess) e = split_factor(auxB, R, r, true, splitB, &ldb, st, parts);
+    int64_t lda = 0, ldb = 0;
+    cudaError_t e = split_factor(auxA, R, r, true, splitA, &lda, st);
+    if (e == cudaSuccess) e = split_factor(auxB, R, r, true, splitB, &ldb, st);
     if (e != cudaSuccess) return e;
     const ColJob ja = col_job(A, R, NA, (const float*)splitA, lda, r, pa, s, out_nrA, outA,
                               (float*)wsA, tickets);
     const ColJob jb = col_job(B, R, NB, (const float*)splitB, ldb, r, pb, s, out_nrB, outB,
                               (float*)wsB, tickets + pa.blocks);
-    if (parts == 3) {
-      switch (rank_tiles(r)) {
-        case 1: return coldot_mma_pair_go<1, 3>(ja, jb, st);
-        case 2: return coldot_mma_pair_go<2, 3>(ja, jb, st);
-        case 4: return coldot_mma_pair_go<4, 3>(ja, jb, st);
-        default: return coldot_mma_pair_go<8, 3>(ja, jb, st);
-      }
-    }
     switch (rank_tiles(r)) {
       case 2: return coldot_mma_pair_go<2, 2>(ja, jb, st);
       case 4: return coldot_mma_pair_go<4, 2>(ja, jb, st);

@@ -223,43 +223,44 @@ BwdLayout bwd_layout(const qlora_weight* w, int64_t R, int32_t r, int32_t comput
   return L;
 }
 
-// INT8 weights: the scratch of the side products (u, v, bt, red, split,
-// red2, split2), then the quantized activation rows and the product's own.
+// INT8 weights: what the first kernel of a call clears (the status header, the
+// tickets), U and V, the parts of the factors and of U and V and the partial
+// sums of the tensor-core side products (or, for activations that those do not
+// take, the scratch of the fp32 ones), then the quantized rows and the
+// product's own.
 struct Int8Layout {
-  size_t u = 0, v = 0, bt = 0, red = 0, split = 0, red2 = 0, split2 = 0, rows = 0, total = 0;
+  size_t tickets = 0, cleared = 0, u = 0, v = 0, fA = 0, fB = 0, fU = 0, fV = 0, part = 0, bt = 0, red = 0,
+         rows = 0, total = 0;
 };
 
-Int8Layout int8_layout(const qlora_weight* w, int64_t R, int32_t r, bool bwd) {
+Int8Layout int8_layout(const qlora_weight* w, int64_t R, int32_t r, bool bwd, int32_t compute) {
   Int8Layout L;
   size_t off = kWsZeroed;
-  L.u = off;
-  off += align_up((size_t)R * r * 4, 256);
-  L.v = off;
-  if (bwd) off += align_up((size_t)R * r * 4, 256);
-  L.bt = off;
-  if (bwd) off += align_up((size_t)r * w->O * 4, 256);
-  L.red = off;
-  size_t red = rowdot_ws(R, w->I, r);
-  if (bwd) {
-    const size_t more[3] = {coldot_ws(R, w->I, r), coldot_ws(R, w->O, r), rowdot_ws(R, w->O, r)};
-    for (size_t m : more)
-      if (m > red) red = m;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align_up(bytes, 256);
+    return at;
+  };
+  const int64_t columns = bwd ? side_tiles(w->I) + side_tiles(w->O) : 0, rows = 2 * side_tiles(R);
+  L.tickets = take((size_t)(columns > rows ? columns : rows) * 4);
+  L.cleared = off;
+  L.u = take((size_t)R * r * 4);
+  if (bwd) L.v = take((size_t)R * r * 4);
+  if (compute == QLORA_COMPUTE_BF16) {
+    L.fA = take(side_parts_bytes(w->I, r));
+    if (bwd) {
+      L.fB = take(side_parts_bytes(w->O, r));
+      L.fU = take(side_parts_bytes(R, r));
+      L.fV = take(side_parts_bytes(R, r));
+    }
+    L.part = take(side_part_ws(r));
   }
-  off += red;
-  L.split = off;
-  size_t sp = adapter_split_ws(w->I, r, 3);
   if (bwd) {
-    const size_t more[2] = {adapter_split_ws(w->O, r, 3), adapter_split_ws(R, r, 3)};
-    for (size_t m : more)
-      if (m > sp) sp = m;
+    L.bt = take((size_t)r * w->O * 4);
+    const size_t a = coldot_ws(R, w->I, r), b = coldot_ws(R, w->O, r);
+    L.red = take(a > b ? a : b);
   }
-  off += sp;
-  L.red2 = off;
-  if (bwd) off += coldot_ws(R, w->O, r);
-  L.split2 = off;
-  if (bwd) off += adapter_split_ws(R, r, 3);
-  L.rows = off;
-  off += int8_ws(bwd, R, w->O, w->I, r);
+  L.rows = take(int8_ws(bwd, R, w->O, w->I, r));
   L.total = off;
   return L;
 }
@@ -284,106 +285,126 @@ Int8Call int8_call(const qlora_weight* w, bool dx, bool bf16, int64_t R, const v
 }
 
 cudaError_t int8_fwd(const qlora_weight* w, const void* X, int64_t R, const float* A, const float* B,
-                     int32_t r, float sc, bool bf16, void* Y, float* U_out, void* ws, cudaStream_t s) {
-  const Int8Layout L = int8_layout(w, R, r, false);
-  float* U = U_out ? U_out : (float*)((char*)ws + L.u);
+                     int32_t r, float sc, int32_t compute, void* Y, float* U_out, void* ws, cudaStream_t s) {
+  const bool bf16 = compute == QLORA_COMPUTE_BF16;
+  const Int8Layout L = int8_layout(w, R, r, false, compute);
+  auto at = [&](size_t off) { return (char*)ws + off; };
+  float* U = U_out ? U_out : (float*)at(L.u);
   const Int8Call c = int8_call(w, false, bf16, R, X, U, B, r, sc, Y);
-  const Int8Clear header = {ws, kWsZeroed};
-  void* rows = (char*)ws + L.rows;
+  const Int8Clear header = {ws, L.cleared};
   cudaError_t e;
   if (int8_few_applies(R, w->I, r)) {
     Int8Few f = {};
     f.F = A;
     f.T = U;
-    e = launch_int8_few(c, f, rows, header, s);
-    return e != cudaSuccess ? e : launch_int8_product(c, rows, (uint32_t*)ws, nullptr, s);
+    e = launch_int8_few(c, f, at(L.rows), header, s);
+  } else {
+    e = launch_int8_rows(c, at(L.rows), header, s);
+    if (e == cudaSuccess && bf16 && side_takes(X, R, w->I)) {
+      uint16_t* fA = (uint16_t*)at(L.fA);
+      const SideFactor f = {A, fA, w->I, false};
+      const SideProduct p = {X, w->I, fA, U, nullptr, false, 1.0f};
+      e = launch_side_split(&f, 1, r, s);
+      if (e == cudaSuccess)
+        e = launch_side(&p, 1, false, R, r, at(L.part), (uint32_t*)at(L.tickets), (uint32_t*)ws, s);
+    } else if (e == cudaSuccess) {
+      e = launch_rowdot(X, bf16, R, w->I, A, false, r, U, s);
+    }
   }
-  e = launch_int8_rows(c, rows, header, s);
-  if (e == cudaSuccess)
-    e = launch_rowdot(X, bf16, R, w->I, A, false, r, U, s, nullptr, nullptr, 0, 0, 1.0f, nullptr, nullptr,
-                      (float*)((char*)ws + L.red), (unsigned*)((char*)ws + kWsHeader),
-                      (uint16_t*)((char*)ws + L.split), 3);
-  if (e == cudaSuccess) e = launch_int8_product(c, rows, (uint32_t*)ws, nullptr, s);
-  return e;
-}
-
-// dA = s V^T X and dB = s dY^T U: one launch where the kernels take both,
-// else one each.
-cudaError_t adapter_grads(bool bf16, const void* X, int64_t I, const float* V, float* dA, const void* dY,
-                          int64_t O, const float* U, float* dB, int64_t R, int32_t r, float sc, void* red,
-                          void* red2, uint16_t* split, uint16_t* split2, unsigned* tickets,
-                          cudaStream_t s, bool split_done = false) {
-  bool paired = false;
-  cudaError_t e = cudaSuccess;
-  if (dA && dB && bf16)
-    e = launch_coldot_pair(X, I, V, false, dA, red, split, dY, O, U, true, dB, red2, split2, R, r, sc, s,
-                           tickets, &paired, 3, split_done);
-  if (e == cudaSuccess && dA && !paired)
-    e = launch_coldot(X, bf16, R, I, V, r, sc, false, dA, red, s, tickets, split, 3);
-  if (e == cudaSuccess && dB && !paired)
-    e = launch_coldot(dY, bf16, R, O, U, r, sc, true, dB, red, s, tickets, split, 3);
+  if (e == cudaSuccess) e = launch_int8_product(c, at(L.rows), (uint32_t*)ws, nullptr, s);
   return e;
 }
 
 cudaError_t int8_bwd(const qlora_weight* w, const void* X, const void* dY, int64_t R, const float* A,
-                     const float* B, int32_t r, float sc, const float* U_in, bool bf16, void* dX,
+                     const float* B, int32_t r, float sc, const float* U_in, int32_t compute, void* dX,
                      float* dA, float* dB, void* ws, cudaStream_t s) {
-  const Int8Layout L = int8_layout(w, R, r, true);
-  unsigned* tickets = (unsigned*)((char*)ws + kWsHeader);
-  float* V = (float*)((char*)ws + L.v);
-  float* Uw = (float*)((char*)ws + L.u);
-  float* red = (float*)((char*)ws + L.red);
-  uint16_t* split = (uint16_t*)((char*)ws + L.split);
-  void* rows = (char*)ws + L.rows;
-  const Int8Clear header = {ws, kWsZeroed};
+  const bool bf16 = compute == QLORA_COMPUTE_BF16;
+  const Int8Layout L = int8_layout(w, R, r, true, compute);
+  auto at = [&](size_t off) { return (char*)ws + off; };
+  float* V = (float*)at(L.v);
+  float* Uw = (float*)at(L.u);
+  const float* U = U_in ? U_in : Uw;
+  uint16_t *fA = (uint16_t*)at(L.fA), *fB = (uint16_t*)at(L.fB), *fU = (uint16_t*)at(L.fU),
+           *fV = (uint16_t*)at(L.fV);
+  uint32_t* tickets = (uint32_t*)at(L.tickets);
+  const Int8Clear header = {ws, L.cleared};
   const Int8Call c = int8_call(w, true, bf16, R, dY, V, A, r, sc, dX);
-  // (the same kernels whichever gradients are wanted: each has the same bits)
-  if (R > 0 && int8_few_applies(R, w->O, r) && int8_few_applies(R, w->I, r)) {
+  const bool want_v = dX || dA, new_u = dB && !U_in;
+  // which matrix the tensor-core side products take (else the fp32 ones do)
+  const bool sX = bf16 && side_takes(X, R, w->I), sY = bf16 && side_takes(dY, R, w->O);
+  // dA = s V^T X, dB = s dY^T U: from the parts of V and U, or from V and U
+  auto columns = [&]() {
+    SideProduct p[2];
+    int n = 0;
+    if (dA && sX) p[n++] = {X, w->I, fV, dA, nullptr, true, sc};
+    if (dB && sY) p[n++] = {dY, w->O, fU, dB, nullptr, false, sc};
+    cudaError_t e = cudaSuccess;
+    if (n) e = launch_side(p, n, true, R, r, at(L.part), tickets, (uint32_t*)ws, s);
+    if (e == cudaSuccess && dA && !sX) e = launch_coldot(X, bf16, R, w->I, V, r, sc, false, dA, at(L.red), s);
+    if (e == cudaSuccess && dB && !sY) e = launch_coldot(dY, bf16, R, w->O, U, r, sc, true, dB, at(L.red), s);
+    return e;
+  };
+  cudaError_t e;
+  if (R == 0) {
+    e = cudaMemsetAsync(ws, 0, L.cleared, s);
+    return e != cudaSuccess ? e : columns();  // zeros
+  }
+  if (int8_few_applies(R, w->O, r) && int8_few_applies(R, w->I, r)) {
     // the rows, V and U in one launch; dA and dB beside the products, or, for
-    // more tokens, from the parts of V and U that the first launch left
+    // more tokens, by themselves (the same kernels whichever gradients are
+    // wanted: each has the same bits)
+    const bool beside = R <= kInt8Few;
     Int8Few f = {};
     f.F = B;
-    f.T = dX || dA ? V : nullptr;
+    f.T = want_v ? V : nullptr;
     f.X = X;
     f.A = A;
-    f.U_new = dB && !U_in ? Uw : nullptr;
-    f.U = U_in ? U_in : Uw;
-    const bool beside = R <= kInt8Few;
+    f.U_new = new_u ? Uw : nullptr;
+    f.U = U;
     if (beside) {
       f.dA = dA;
       f.dB = dB;
+    } else {
+      f.T_parts = dA && sX ? fV : nullptr;
+      f.U_parts = dB && sY ? fU : nullptr;
+      f.NP = side_np(r);
+      f.ld = side_ld(R);
     }
-    const bool parts = !beside && dA && dB && bf16 && coldot_takes(X, R, w->I) && coldot_takes(dY, R, w->O);
-    if (parts) {
-      f.T_parts = split;
-      f.U_parts = (uint16_t*)((char*)ws + L.split2);
-      f.NP = adapter_rank_rows(r);
-      f.ld = adapter_split_ld(R);
-    }
-    cudaError_t e = launch_int8_few(c, f, rows, header, s);
-    if (e == cudaSuccess && !beside)
-      e = adapter_grads(bf16, X, w->I, V, dA, dY, w->O, f.U, dB, R, r, sc, red, (char*)ws + L.red2, split,
-                        (uint16_t*)((char*)ws + L.split2), tickets, s, parts);
+    e = launch_int8_few(c, f, at(L.rows), header, s);
+    if (e == cudaSuccess && !beside) e = columns();
     if (e == cudaSuccess && (dX || (beside && (dA || dB))))
-      e = launch_int8_product(c, rows, (uint32_t*)ws, &f, s);
+      e = launch_int8_product(c, at(L.rows), (uint32_t*)ws, &f, s);
     return e;
   }
-  cudaError_t e;
-  if (dX && R > 0) e = launch_int8_rows(c, rows, header, s);
-  else e = cudaMemsetAsync(ws, 0, kWsZeroed, s);
-  if (e == cudaSuccess && R > 0 && (dX || dA))
-    e = launch_rowdot(dY, bf16, R, w->O, B, true, r, V, s, nullptr, nullptr, 0, 0, 1.0f, nullptr,
-                      (float*)((char*)ws + L.bt), red, tickets, split, 3);
-  const float* U = U_in;
-  if (e == cudaSuccess && R > 0 && dB && !U) {
-    e = launch_rowdot(X, bf16, R, w->I, A, false, r, Uw, s, nullptr, nullptr, 0, 0, 1.0f, nullptr, nullptr,
-                      red, tickets, split, 3);
-    U = Uw;
+  e = dX ? launch_int8_rows(c, at(L.rows), header, s) : cudaMemsetAsync(ws, 0, L.cleared, s);
+  // the parts of the factors, then V and U (with their own parts where a
+  // tensor-core product makes them, else split after it)
+  SideFactor f[2], late[2];
+  SideProduct p[2];
+  int nf = 0, np = 0, nlate = 0;
+  const bool parts_v = dA && sX, parts_u = dB && sY;
+  if (want_v && sY) {
+    f[nf++] = {B, fB, w->O, true};
+    p[np++] = {dY, w->O, fB, V, parts_v ? fV : nullptr, false, 1.0f};
+  } else if (parts_v) {
+    late[nlate++] = {V, fV, R, true};
   }
-  if (e == cudaSuccess)
-    e = adapter_grads(bf16, X, w->I, V, dA, dY, w->O, U, dB, R, r, sc, red, (char*)ws + L.red2, split,
-                      (uint16_t*)((char*)ws + L.split2), tickets, s);
-  if (e == cudaSuccess && R > 0 && dX) e = launch_int8_product(c, rows, (uint32_t*)ws, nullptr, s);
+  if (new_u && sX) {
+    f[nf++] = {A, fA, w->I, false};
+    p[np++] = {X, w->I, fA, Uw, parts_u ? fU : nullptr, false, 1.0f};
+  } else if (parts_u) {
+    if (new_u) late[nlate++] = {U, fU, R, true};
+    else f[nf++] = {U, fU, R, true};
+  }
+  if (e == cudaSuccess) e = launch_side_split(f, nf, r, s);
+  if (e == cudaSuccess && np) e = launch_side(p, np, false, R, r, at(L.part), tickets, (uint32_t*)ws, s);
+  if (e == cudaSuccess && want_v && !sY)
+    e = launch_rowdot(dY, bf16, R, w->O, B, true, r, V, s, nullptr, nullptr, 0, 0, 1.0f, nullptr,
+                      (float*)at(L.bt));
+  if (e == cudaSuccess && new_u && !sX) e = launch_rowdot(X, bf16, R, w->I, A, false, r, Uw, s);
+  if (e == cudaSuccess) e = launch_side_split(late, nlate, r, s);
+  if (e == cudaSuccess) e = columns();
+  if (e == cudaSuccess && dX) e = launch_int8_product(c, at(L.rows), (uint32_t*)ws, nullptr, s);
   return e;
 }
 
@@ -645,7 +666,7 @@ size_t qlora_linear_workspace_bytes(const qlora_weight* w, int64_t R, int32_t r,
   if (w->fmt == QLORA_FMT_INT8) {
     if (w->O < 1 || w->I < 1 || w->O > kInt8MaxK || w->I > kInt8MaxK) return 0;
     if (op != QLORA_OP_FWD && op != QLORA_OP_BWD) return 0;
-    return int8_layout(w, R, r, op == QLORA_OP_BWD).total;
+    return int8_layout(w, R, r, op == QLORA_OP_BWD, compute).total;
   }
   if (op == QLORA_OP_FWD) return fwd_layout(w, R, r, compute).total;
   if (op == QLORA_OP_BWD) return bwd_layout(w, R, r, compute).total;
@@ -676,14 +697,14 @@ qlora_status qlora_linear_fwd(const qlora_weight* w, const void* X, int64_t R, c
   const bool int8 = w->fmt == QLORA_FMT_INT8;
   if (int8 && R > INT32_MAX) return QLORA_ERR_SHAPE;
   const FwdLayout L = int8 ? FwdLayout() : fwd_layout(w, R, r, compute);
-  if (ws_bytes < (int8 ? int8_layout(w, R, r, false).total : L.total)) return QLORA_ERR_WORKSPACE;
+  if (ws_bytes < (int8 ? int8_layout(w, R, r, false, compute).total : L.total)) return QLORA_ERR_WORKSPACE;
   st = device_ready();
   if (st != QLORA_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   const float sc = alpha / (float)r;
   if (int8 && R > 0)
     return cuda_status(
-        int8_fwd(w, X, R, A, B, r, sc, compute == QLORA_COMPUTE_BF16, Y, U_out, ws, s));
+        int8_fwd(w, X, R, A, B, r, sc, compute, Y, U_out, ws, s));
   cudaError_t e = cudaMemsetAsync(ws, 0, kWsZeroed, s);
   if (e != cudaSuccess) return QLORA_ERR_CUDA;
   if (R == 0) return QLORA_OK;
@@ -731,14 +752,14 @@ qlora_status qlora_linear_bwd(const qlora_weight* w, const void* X, const void* 
   const bool int8 = w->fmt == QLORA_FMT_INT8;
   if (int8 && R > INT32_MAX) return QLORA_ERR_SHAPE;
   const BwdLayout L = int8 ? BwdLayout() : bwd_layout(w, R, r, compute);
-  if (ws_bytes < (int8 ? int8_layout(w, R, r, true).total : L.total)) return QLORA_ERR_WORKSPACE;
+  if (ws_bytes < (int8 ? int8_layout(w, R, r, true, compute).total : L.total)) return QLORA_ERR_WORKSPACE;
   st = device_ready();
   if (st != QLORA_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   const bool bf16 = compute == QLORA_COMPUTE_BF16;
   const float sc = alpha / (float)r;
   if (int8)
-    return cuda_status(int8_bwd(w, X, dY, R, A, B, r, sc, U_in, bf16, dX, dA, dB, ws, s));
+    return cuda_status(int8_bwd(w, X, dY, R, A, B, r, sc, U_in, compute, dX, dA, dB, ws, s));
   cudaError_t e = cudaMemsetAsync(ws, 0, kWsZeroed, s);
   if (e != cudaSuccess) return QLORA_ERR_CUDA;
   unsigned* tickets = (unsigned*)((char*)ws + kWsHeader);

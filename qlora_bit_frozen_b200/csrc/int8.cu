@@ -13,6 +13,7 @@
 // one rounding to the type of the output.
 #include "common.cuh"
 #include "int8.h"
+#include "int8_dev.cuh"
 #include "internal.h"
 
 namespace qlora {
@@ -50,19 +51,11 @@ __device__ __forceinline__ float reciprocal(float s) {
 }
 
 // Two fp32 operations in one instruction, each rounded to nearest.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
-}
 __device__ __forceinline__ float lo_of(uint64_t a) { return __uint_as_float((uint32_t)a); }
 __device__ __forceinline__ float hi_of(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
 // max(|a|, |b|, |c|); a NaN wins.
@@ -81,7 +74,7 @@ __device__ __forceinline__ float top3(float a, float b, float c) {
 // N: a branch for each of them took 36 issue slots an element, this takes 4.
 template <int N>
 __device__ __forceinline__ void codes_of(const uint64_t (&x)[N / 2], float s, float inv, uint32_t (&c)[N / 4]) {
-  const uint64_t inv2 = pair(inv, inv), M = pair(12582912.0f, 12582912.0f), minus = pair(-1.0f, -1.0f);
+  const uint64_t inv2 = pack2(inv, inv), M = pack2(12582912.0f, 12582912.0f), minus = pack2(-1.0f, -1.0f);
   uint32_t t[N];
   float worst = 0.0f;
 #pragma unroll
@@ -181,7 +174,7 @@ __global__ void __launch_bounds__(rows_threads<NV, FACTOR>()) rows_kernel(const 
 #pragma unroll
       for (int j = 0; j < N / 2; ++j) {
         const float* p = a.f + (int64_t)v * N + 2 * j;
-        f[i * (N / 2) + j] = v < nvec ? pair(__ldg(p), __ldg(p + 1)) : 0;
+        f[i * (N / 2) + j] = v < nvec ? pack2(__ldg(p), __ldg(p + 1)) : 0;
       }
     }
   }
@@ -488,7 +481,7 @@ __device__ __forceinline__ void few_token(const FewArgs& a, const FewJob& job, i
     }
     uint64_t y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = pair(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) y[i] = pack2(v[2 * i], v[2 * i + 1]);
     codes_of<8>(y, s, inv, c);
     q[k / 8] = make_uint2(c[0], c[1]);
   }

@@ -5,8 +5,6 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "qlora.h"
 
 namespace qlora {
@@ -82,34 +80,34 @@ size_t int8_tc_zeroed(bool dx, int64_t R, int64_t O, int64_t I);
 cudaError_t launch_int8_tc(const Int8Call& c, const int8_t* xq, const float* xs, const Int8Few* few, void* ws,
                            uint32_t* hdr, cudaStream_t st);
 
-namespace int8 {
-
-constexpr int kMaxDevices = 64;
-
-inline int sm_count() {
-  static std::atomic<int> count[kMaxDevices];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return 148;
-  n = count[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-    count[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
-// Once per kernel and device: the attribute belongs to the device's context.
-template <typename K>
-inline cudaError_t allow_smem(K kern, int bytes, std::atomic<bool>* done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < kMaxDevices && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < kMaxDevices) done[dev].store(true, std::memory_order_relaxed);
-  return e;
-}
-
-}  // namespace int8
+// int8_side.cu: the adapter's thin products over bf16 matrices P [R x N].
+// Parts: an fp32 factor [n x r] or [r x n] as three bf16 parts, [3][side_np(r)]
+// rows of side_ld(n), zeros past n.
+int side_np(int32_t r);
+int64_t side_ld(int64_t n);
+size_t side_parts_bytes(int64_t n, int32_t r);
+size_t side_part_ws(int32_t r);     // scratch of one launch
+int64_t side_tiles(int64_t m);      // tickets it takes for m rows of output
+bool side_takes(const void* P, int64_t R, int64_t N);
+struct SideFactor {
+  const float* src;
+  uint16_t* parts;
+  int64_t n;
+  bool kr;  // [n x r]
+};
+cudaError_t launch_side_split(const SideFactor* f, int count, int32_t r, cudaStream_t st);
+struct SideProduct {
+  const void* P;
+  int64_t N;
+  const uint16_t* factor;  // parts over N (row products) or over R (column products)
+  float* out;              // s times the product: [R x r]; [N x r] or, transposed, [r x N]
+  uint16_t* parts;         // nullable: its own parts (row products)
+  bool transposed;
+  float s;
+};
+// One or two products in one launch: P L^T (rows) or P^T T (columns).  tickets:
+// side_tiles of each output, zero, left zero.
+cudaError_t launch_side(const SideProduct* f, int count, bool columns, int64_t R, int32_t r, void* part,
+                        uint32_t* tickets, uint32_t* hdr, cudaStream_t st);
 
 }  // namespace qlora

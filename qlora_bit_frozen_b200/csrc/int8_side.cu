@@ -1,0 +1,469 @@
+// int8_side.cu -- the adapter's thin products on the tensor cores with all 24
+// bits of the fp32 factors:
+//   row products     U = X A^T, V = dY B          (A operand: tokens x columns)
+//   column products  dA = s V^T X, dB = s dY^T U  (A operand: columns x tokens)
+// D[m, n] = sum_k A[m, k] B[n, k], M = 128 rows of the large matrix a tile and
+// N = 3 NP: the fp32 factor is split into three bf16 parts (each remainder is
+// exact), so that bf16 products lose nothing of it, and the parts' sums are
+// added at the end.  The large matrix is read once, by TMA, K-major for the row
+// products and MN-major (from the same row-major bytes) for the column ones.
+//
+// The tensor core's own sums lose a little at every step, so a sum runs over
+// 256 terms only (16 steps) in one of two accumulators in TMEM; the epilogue
+// warps drain it into fp32 registers while the other one fills.  Measured error
+// 2e-7 of the result where one running sum over 8192 tokens had 3e-6 to 9e-6.
+//
+// Each product's chunks, tile after tile, are dealt out in equal runs over the
+// SMs; a tile that several CTAs share is summed by the last of them, in CTA
+// order.  (The runs do not depend on what else is in the launch: a gradient has
+// the same bits whichever others are wanted.)  Bound by HBM on the large matrix.
+#include "common.cuh"
+#include "int8.h"
+#include "int8_dev.cuh"
+#include "internal.h"
+
+namespace qlora {
+namespace {
+
+using namespace int8;
+
+constexpr int kStep = 64;   // terms per ring stage: one 128-byte swizzle row
+constexpr int kChunk = 4;   // stages per accumulator
+constexpr int kTileA = 128 * kStep * 2;
+constexpr int kSideThreads = 192;  // producer, MMA issuer, four epilogue warps
+
+__host__ __device__ constexpr int side_n(int NP) { return NP == 8 ? 32 : 3 * NP; }  // MMA N
+__host__ __device__ constexpr int side_cols(int NP) {                              // TMEM columns of it
+  return NP == 8 ? 32 : NP == 16 ? 64 : NP == 32 ? 128 : 256;
+}
+
+template <int NP>
+struct SideCfg {
+  static constexpr int kTileB = side_n(NP) * kStep * 2;
+  static constexpr int kStage = kTileA + kTileB;
+  static constexpr int kStages = NP == 64 ? 5 : NP == 32 ? 7 : 8;
+  static constexpr int kSmem = 1024 + kStages * kStage + 256;
+  static_assert(kSmem <= 227 * 1024 && kSmem > 114 * 1024, "one CTA per SM");
+};
+
+struct SideOut {
+  float* out;       // [M x r], or [r x M] (transposed)
+  uint16_t* parts;  // nullable: the result's own three parts, [3][NP][ld]
+  int64_t M, ld;
+  int32_t chunks, steps;  // of a tile
+  int32_t transposed;
+  float s;
+};
+struct SideArgs {
+  SideOut job[2];
+  int64_t tiles[2];   // the second may be 0
+  int64_t units[2];   // chunks of all the job's tiles
+  int32_t r;
+  float* part;        // [CTAs][2 jobs][2][NP][128]
+  uint32_t* tickets;  // [tiles of both], zero, left zero
+  uint32_t* err;
+  uint64_t wait_ns;
+};
+
+__device__ __forceinline__ int64_t side_lo(const SideArgs& p, int job, int64_t cta) {
+  return p.units[job] * cta / gridDim.x;
+}
+
+// The chunks of this CTA: its run of job 0, then its run of job 1.
+struct SideWalk {
+  int64_t left, tile;
+  int32_t job, chunk;
+  __device__ __forceinline__ explicit SideWalk(const SideArgs& p) {
+    open(p, 0);
+    if (left == 0) open(p, 1);
+  }
+  __device__ __forceinline__ void open(const SideArgs& p, int k) {
+    job = k;
+    const int64_t lo = side_lo(p, k, blockIdx.x);
+    left = side_lo(p, k, (int64_t)blockIdx.x + 1) - lo;
+    tile = left ? lo / p.job[k].chunks : 0;
+    chunk = left ? (int32_t)(lo - tile * p.job[k].chunks) : 0;
+  }
+  __device__ __forceinline__ int steps(const SideArgs& p) const {
+    const int n = p.job[job].steps - chunk * kChunk;
+    return n < kChunk ? n : kChunk;
+  }
+  __device__ __forceinline__ void next(const SideArgs& p) {
+    if (--left == 0) {
+      if (job == 0) open(p, 1);
+      return;
+    }
+    if (++chunk == p.job[job].chunks) {
+      chunk = 0;
+      ++tile;
+    }
+  }
+};
+
+// CTA whose run of the job holds unit u.
+__device__ __forceinline__ int64_t side_owner(const SideArgs& p, int job, int64_t u) {
+  int64_t c = u * gridDim.x / p.units[job];
+  while (side_lo(p, job, c + 1) <= u) ++c;
+  while (side_lo(p, job, c) > u) --c;
+  return c;
+}
+
+__host__ __device__ constexpr uint32_t idesc_bf16(int N, bool a_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(128 >> 4) << 24);
+}
+
+template <int NP>
+__device__ __forceinline__ void side_write(const SideOut& o, int r, int64_t m, const float (&acc)[NP]) {
+  if (m >= o.M) {
+    // the parts' rows end with zeros: they meet zero rows of the large matrix
+    if (o.parts && m < o.ld)
+      for (int q = 0; q < 3 * r; ++q) o.parts[((int64_t)(q / r) * NP + q % r) * o.ld + m] = 0;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < NP; ++j) {
+    if (j < r) {
+      const float v = o.s * acc[j];
+      o.out[o.transposed ? (int64_t)j * o.M + m : m * r + j] = v;
+      if (o.parts) {
+        float rest = v;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          const __nv_bfloat16 b = __float2bfloat16_rn(rest);
+          o.parts[((int64_t)q * NP + j) * o.ld + m] = __bfloat16_as_ushort(b);
+          rest -= __bfloat162float(b);
+        }
+      }
+    }
+  }
+}
+
+template <bool A_MN, int NP>
+__global__ void __launch_bounds__(kSideThreads, 1)
+    side_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUtensorMap tb0,
+                const __grid_constant__ CUtensorMap ta1, const __grid_constant__ CUtensorMap tb1,
+                const SideArgs p) {
+  using C = SideCfg<NP>;
+  constexpr uint32_t kIdesc = idesc_bf16(side_n(NP), A_MN);
+  constexpr int kCols = side_cols(NP);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint64_t* bars = (uint64_t*)(smem + C::kStages * C::kStage);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + C::kStages;
+  uint64_t* acc_full = bars + 2 * C::kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  volatile uint32_t* tmem_slot = (volatile uint32_t*)(acc_empty + 2);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  volatile uint32_t* last_flag = tmem_slot + 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    griddep_launch_dependents();  // what is queued behind waits for this grid itself
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&acc_full[b]), 1);
+      mbar_init(smem_u32(&acc_empty[b]), 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&ta0);
+    prefetch_tensormap(&tb0);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32((const void*)tmem_slot), 2 * kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (SideWalk w(p); w.left > 0 && ok; w.next(p)) {
+      const CUtensorMap* ta = w.job ? &ta1 : &ta0;
+      const CUtensorMap* tb = w.job ? &tb1 : &tb0;
+      const int m0 = (int)w.tile * 128, steps = w.steps(p);
+      for (int i = 0; i < steps; ++i) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0) ||
+            !warp_wait(smem_u32(&empty[s]), ph ^ 1u, p.wait_ns, p.err, 0x801)) {
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t fb = smem_u32(&full[s]), dst = smem_u32(smem + s * C::kStage);
+          const int k = (w.chunk * kChunk + i) * kStep;
+          mbar_arrive_expect_tx(fb, C::kStage);
+          if (A_MN) {
+            tma_load_2d(dst, ta, fb, m0, k);
+            tma_load_2d(dst + kTileA / 2, ta, fb, m0 + 64, k);
+          } else {
+            tma_load_2d(dst, ta, fb, k, m0);
+          }
+          tma_load_2d(dst + kTileA, tb, fb, k, 0);
+        }
+        __syncwarp();
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
+      }
+    }
+    if (!ok)  // copies in flight land before the CTA exits
+      for (int i = 0; i < C::kStages; ++i) {
+        warp_wait(smem_u32(&full[s]), ph ^ 1u, p.wait_ns, nullptr, 0);
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
+      }
+  } else if (warp == 1) {
+    int s = 0, b = 0;
+    uint32_t ph = 0, pa = 0;
+    bool ok = true;
+    for (SideWalk w(p); w.left > 0 && ok; w.next(p)) {
+      const int steps = w.steps(p);
+      if (!warp_wait(smem_u32(&acc_empty[b]), pa ^ 1u, p.wait_ns, p.err, 0x802)) {
+        *abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem + (uint32_t)(kCols * b);
+      for (int i = 0; i < steps; ++i) {
+        if (!warp_wait(smem_u32(&full[s]), ph, p.wait_ns, p.err, 0x803)) {
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t base = smem_u32(smem + s * C::kStage);
+          const uint64_t ad = A_MN ? sdesc(base, kTileA / 2, 1024) : sdesc(base, 16, 1024);
+          const uint64_t bd = sdesc(base + kTileA, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kStep / 16; ++kk)
+            umma_bf16(d, ad + (A_MN ? 128 : 2) * kk, bd + 2 * kk, kIdesc, (i | kk) ? 1u : 0u);
+          umma_commit(smem_u32(&empty[s]));
+          if (i + 1 == steps) umma_commit(smem_u32(&acc_full[b]));
+        }
+        __syncwarp();
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
+      }
+      if (++b == 2) { b = 0; pa ^= 1u; }
+    }
+  } else {
+    const int quad = warp & 3;
+    int b = 0;
+    uint32_t pa = 0;
+    float acc[NP];
+    int run = 0;  // chunks in acc
+    int segment = 0;
+    for (SideWalk w(p); w.left > 0;) {
+      const int job = w.job, chunk = w.chunk;
+      const int64_t tile = w.tile;
+      if (run == 0) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) acc[j] = 0.0f;
+      }
+      // one answer for all four warps, which meet at barriers below
+      if (!all_of<128>(mbar_wait(smem_u32(&acc_full[b]), pa, p.wait_ns, p.err, 0x804))) {
+        *abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(kCols * b);
+#pragma unroll
+      for (int j0 = 0; j0 < NP; j0 += 8) {
+        uint32_t v[3][8];
+#pragma unroll
+        for (int q = 0; q < 3; ++q) tmem_ld_32x32b_x8(d + (uint32_t)(q * NP + j0), v[q]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          acc[j0 + j] += (__uint_as_float(v[2][j]) + __uint_as_float(v[1][j])) + __uint_as_float(v[0][j]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&acc_empty[b]));
+      if (++b == 2) { b = 0; pa ^= 1u; }
+      ++run;
+      w.next(p);
+      const SideOut& o = p.job[job];
+      const bool run_ends = w.left == 0 || w.job != job;
+      if (chunk + 1 < o.chunks && !run_ends) continue;
+      // the segment of this CTA in the tile is done
+      const int64_t m = tile * 128 + 32 * quad + lane;
+      if (run == o.chunks) {
+        side_write<NP>(o, p.r, m, acc);
+      } else {
+        const int64_t id = (job ? p.tiles[0] : 0) + tile, u0 = tile * o.chunks;
+        auto slot = [&](int64_t cta, int which) {
+          return p.part + ((cta * 2 + job) * 2 + which) * NP * 128 + 32 * quad + lane;
+        };
+        float* mine = slot(blockIdx.x, segment ? 1 : 0);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) mine[j * 128] = acc[j];
+        __threadfence();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (warp == 2 && lane == 0) {
+          const bool last = atomicAdd(p.tickets + id, (uint32_t)run) + (uint32_t)run == (uint32_t)o.chunks;
+          if (last) p.tickets[id] = 0;
+          *last_flag = last;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const bool last = *last_flag != 0;
+        __threadfence();
+        if (last) {
+          const int64_t c0 = side_owner(p, job, u0), c1 = side_owner(p, job, u0 + o.chunks - 1);
+#pragma unroll
+          for (int j = 0; j < NP; ++j) acc[j] = 0.0f;
+          for (int64_t c = c0; c <= c1; ++c) {
+            if (side_lo(p, job, c) == side_lo(p, job, c + 1)) continue;  // more CTAs than chunks
+            // the first segment of its run, unless that began in a tile before
+            const float* part = slot(c, side_lo(p, job, c) >= u0 ? 0 : 1);
+#pragma unroll
+            for (int j = 0; j < NP; ++j) acc[j] += __ldcg(part + j * 128);
+          }
+          side_write<NP>(o, p.r, m, acc);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // all have read the flag
+      }
+      run = 0;
+      segment = run_ends ? 0 : segment + 1;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * kCols);
+  }
+}
+
+// The three bf16 parts of up to two fp32 factors, [3][NP][ld], zeros past n
+// entries of a row: F(k, j) = src[k r + j] (kr) or src[j n + k].
+struct SplitJob {
+  const float* src;
+  uint16_t* dst;
+  int64_t n, ld;
+  int32_t kr, blocks;
+};
+struct SplitArgs {
+  SplitJob job[2];
+  int32_t r, NP;
+};
+__global__ void __launch_bounds__(256) split_kernel(const SplitArgs a) {
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int k1 = (int)blockIdx.x >= a.job[0].blocks ? 1 : 0;
+  const SplitJob& b = a.job[k1];
+  const int64_t e = ((int64_t)blockIdx.x - (k1 ? a.job[0].blocks : 0)) * 256 + threadIdx.x;
+  if (e >= (int64_t)a.r * b.ld) return;
+  // neighbouring threads on neighbouring source entries
+  const int64_t j = b.kr ? e % a.r : e / b.ld, k = b.kr ? e / a.r : e % b.ld;
+  float v = k < b.n ? __ldg(b.src + (b.kr ? k * a.r + j : j * b.n + k)) : 0.0f;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const __nv_bfloat16 h = __float2bfloat16_rn(v);
+    b.dst[((int64_t)q * a.NP + j) * b.ld + k] = __bfloat16_as_ushort(h);
+    v -= __bfloat162float(h);
+  }
+}
+
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <bool A_MN, int NP>
+cudaError_t side_go(const CUtensorMap* t, const SideArgs& a, unsigned ctas, cudaStream_t st) {
+  static std::atomic<bool> done[kMaxDevices];
+  const cudaError_t e = allow_smem(side_kernel<A_MN, NP>, SideCfg<NP>::kSmem, done);
+  if (e != cudaSuccess) return e;
+  side_kernel<A_MN, NP><<<ctas, kSideThreads, SideCfg<NP>::kSmem, st>>>(t[0], t[1], t[2], t[3], a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+template <bool A_MN>
+cudaError_t side_rank(const CUtensorMap* t, const SideArgs& a, int NP, unsigned ctas, cudaStream_t st) {
+  switch (NP) {
+    case 8: return side_go<A_MN, 8>(t, a, ctas, st);
+    case 16: return side_go<A_MN, 16>(t, a, ctas, st);
+    case 32: return side_go<A_MN, 32>(t, a, ctas, st);
+    default: return side_go<A_MN, 64>(t, a, ctas, st);
+  }
+}
+
+}  // namespace
+
+int side_np(int32_t r) { return r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : 64; }
+int64_t side_ld(int64_t n) { return up(n, 8) * 8; }
+size_t side_parts_bytes(int64_t n, int32_t r) {
+  return align_up((size_t)3 * side_np(r) * (size_t)side_ld(n) * 2, 256);
+}
+size_t side_part_ws(int32_t r) { return (size_t)sm_count() * 4 * side_np(r) * 128 * 4; }
+int64_t side_tiles(int64_t m) { return up(m, 128); }
+bool side_takes(const void* P, int64_t R, int64_t N) {
+  return R > 0 && R <= INT32_MAX - 256 && N % 8 == 0 && (uintptr_t)P % 16 == 0;
+}
+
+cudaError_t launch_side_split(const SideFactor* f, int count, int32_t r, cudaStream_t st) {
+  SplitArgs a = {};
+  a.r = r;
+  a.NP = side_np(r);
+  int blocks = 0;
+  for (int i = 0; i < count; ++i) {
+    SplitJob& b = a.job[i];
+    b.src = f[i].src;
+    b.dst = f[i].parts;
+    b.n = f[i].n;
+    b.ld = side_ld(f[i].n);
+    b.kr = f[i].kr ? 1 : 0;
+    b.blocks = (int)up((int64_t)r * b.ld, 256);
+    blocks += b.blocks;
+  }
+  if (blocks == 0) return cudaSuccess;
+  split_kernel<<<(unsigned)blocks, 256, 0, st>>>(a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_side(const SideProduct* f, int count, bool columns, int64_t R, int32_t r, void* part,
+                        uint32_t* tickets, uint32_t* hdr, cudaStream_t st) {
+  const int NP = side_np(r);
+  CUtensorMap t[4];
+  SideArgs a = {};
+  for (int i = 0; i < count; ++i) {
+    const int64_t N = f[i].N, K = columns ? R : N, M = columns ? N : R;
+    SideOut& o = a.job[i];
+    o.out = f[i].out;
+    o.parts = f[i].parts;
+    o.M = M;
+    o.ld = side_ld(M);
+    o.steps = (int32_t)up(K, kStep);
+    o.chunks = (int32_t)up(o.steps, kChunk);
+    o.transposed = f[i].transposed ? 1 : 0;
+    o.s = f[i].s;
+    a.tiles[i] = side_tiles(M);
+    a.units[i] = a.tiles[i] * o.chunks;
+    const int64_t ld = side_ld(K);
+    if (!make_map_2d(&t[2 * i], f[i].P, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)N, (uint64_t)R,
+                     (uint64_t)N * 2, 64, columns ? 64 : 128) ||
+        !make_map_2d(&t[2 * i + 1], f[i].factor, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)ld,
+                     (uint64_t)3 * NP, (uint64_t)ld * 2, 64, (uint32_t)side_n(NP)))
+      return cudaErrorInvalidValue;
+  }
+  if (count == 1) {
+    a.job[1].chunks = 1;
+    t[2] = t[0];
+    t[3] = t[1];
+  }
+  a.r = r;
+  a.part = (float*)part;
+  a.tickets = tickets;
+  a.err = hdr;
+  a.wait_ns = kWaitLimitNs;
+  const unsigned ctas = (unsigned)sm_count();
+  return columns ? side_rank<true>(t, a, NP, ctas, st) : side_rank<false>(t, a, NP, ctas, st);
+}
+
+}  // namespace qlora

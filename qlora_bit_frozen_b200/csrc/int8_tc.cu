@@ -28,11 +28,9 @@
 //
 // Every wait is bounded; on expiry the kernel records QLORA_ERR_TIMEOUT,
 // stops issuing, and still reaches its barriers and frees its TMEM.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "common.cuh"
 #include "int8.h"
+#include "int8_dev.cuh"
 #include "internal.h"
 
 namespace qlora {
@@ -58,15 +56,6 @@ struct Epi {
   uint32_t* err;
   uint64_t wait_ns;
 };
-
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= 1ull << 46;
-  d |= 2ull << 61;  // 128-byte swizzle
-  return d;
-}
 
 // kind::i8 instruction descriptor: s8 x s8 -> s32.
 __host__ __device__ constexpr uint32_t idesc_i8(int M, int N, bool a_mn, bool b_mn) {
@@ -101,22 +90,6 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
       : "memory");
 }
 
-// The producer and MMA warps run their loops with all lanes (the loop state
-// then lives in uniform registers) and let one elected lane issue: with a
-// single lane running the loop the MMA warp took 550 cycles a step, whatever
-// the tile.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-// Bounded wait of a whole warp, with one answer for all its lanes.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, uint32_t* err,
-                                          uint32_t where) {
-  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns, err, where));
-}
-
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -149,13 +122,6 @@ __device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int32_t x, int
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap), "r"(x), "r"(y)
                : "memory");
 }
-// 32 lanes x 8 columns of TMEM.
-__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr));
-}
 __device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tmap),
                "r"(src), "r"(x), "r"(y)
@@ -165,40 +131,6 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
                                              uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
-}
-
-// Untiled bulk copy (16-byte aligned, a multiple of 16 bytes).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
-// Whether `ok` holds for all THREADS epilogue threads (barrier 1).
-template <int THREADS>
-__device__ __forceinline__ bool all_epilogue(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred.aligned q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)ok), "n"(THREADS)
-      : "memory");
-  return r != 0;
-}
-
-// Two fp32 FMAs in one instruction.
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
-}
-__device__ __forceinline__ float sum2(uint64_t a) {
-  return __uint_as_float((uint32_t)a) + __uint_as_float((uint32_t)(a >> 32));
 }
 
 __host__ __device__ constexpr int rank_pad(int r) { return r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : 64; }
@@ -402,7 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       ok = mbar_wait(smem_u32(fac_full), pf, p.e.wait_ns, p.e.err, 0x505) && ok;
       ok = mbar_wait(smem_u32(&acc_full[b]), pa, p.e.wait_ns, p.e.err, 0x506) && ok;
       pf ^= 1u;
-      if (!all_epilogue<32 * kEpiWarps>(ok)) {
+      if (!all_of<32 * kEpiWarps>(ok)) {
         *abort_flag = 1;
         break;
       }
@@ -832,7 +764,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         staged = tt;
       }
       // one answer for all warps, which meet at barriers below
-      if (!all_epilogue<kStreamEpi>(mbar_wait(smem_u32(&acc_full[b]), pa, p.e.wait_ns, p.e.err, 0x604))) {
+      if (!all_of<kStreamEpi>(mbar_wait(smem_u32(&acc_full[b]), pa, p.e.wait_ns, p.e.err, 0x604))) {
         *abort_flag = 1;
         break;
       }
@@ -914,35 +846,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 }
 
 // ------------------------------------------------------------------- host
-
-using EncodeTiled = PFN_cuTensorMapEncodeTiled_v12000;
-
-EncodeTiled encode_fn() {
-  static const EncodeTiled fn = [] {
-    cudaDriverEntryPointQueryResult q;
-    void* f = nullptr;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return (EncodeTiled)f;
-  }();
-  return fn;
-}
-
-// Row-major [rows x cols] of esize-byte elements, rows `stride` bytes apart,
-// boxes of [br x bc], 128-byte swizzle.
-bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t cols, uint64_t rows,
-              uint64_t stride, uint32_t bc, uint32_t br) {
-  EncodeTiled enc = encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {stride};
-  cuuint32_t box[2] = {bc, br};
-  cuuint32_t es[2] = {1, 1};
-  return enc(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -1031,9 +934,9 @@ cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& b
   Epi e = base;
   CUtensorMap mx, mw, mo;
   const int64_t xp = int8_pitch(K), wp = int8_pitch(c.I);
-  if (!make_map(&mw, c.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)wp, (uint64_t)c.O, (uint64_t)wp, 128,
+  if (!make_map_2d(&mw, c.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)wp, (uint64_t)c.O, (uint64_t)wp, 128,
                 128) ||
-      !make_map(&mx, xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)xp, (uint64_t)c.R, (uint64_t)xp, 128,
+      !make_map_2d(&mx, xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)xp, (uint64_t)c.R, (uint64_t)xp, 128,
                 pl.pair ? 128 : (uint32_t)pl.bn))
     return cudaErrorInvalidValue;
   if (pl.pair) {
@@ -1049,7 +952,7 @@ cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& b
     e.wpad = wpad;
     e.tma_out = ((uintptr_t)c.out % 16 == 0 && (e.N * sizeof(OUT)) % 16 == 0) ? 1 : 0;
     if (e.tma_out &&
-        !make_map(&mo, c.out, sizeof(OUT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+        !make_map_2d(&mo, c.out, sizeof(OUT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                   (uint64_t)e.N, (uint64_t)c.R, (uint64_t)e.N * sizeof(OUT), 128 / sizeof(OUT), 32))
       return cudaErrorInvalidValue;
     if (!e.tma_out) mo = mx;  // not used

@@ -95,22 +95,20 @@ cudaError_t launch_rowdot(const void* P, bool bf16, int64_t R, int64_t K, const 
                           int64_t side_extent = 0, int side_mode = 0, float side_mul = 1.0f,
                           uint16_t* side_dst = nullptr, float* lt_ws = nullptr,
                           float* part_ws = nullptr, unsigned* tickets = nullptr,
-                          uint16_t* split_ws = nullptr, int parts = 2);
-// parts: the bf16 parts the fp32 factor is split into on the tensor-core
-// path, 2 (16 bits) or 3 (all 24; needs split_ws).
+                          uint16_t* split_ws = nullptr);
 // part_ws (rowdot_ws bytes) and tickets (kWsTickets bytes, zero on entry
 // and left zero) let the bf16 tensor-core path split K across blocks.
 size_t rowdot_ws(int64_t R, int64_t K, int32_t r);
 // split_ws (adapter_split_ws(extent, r) bytes, nullable): scratch for the
 // bf16 hi / lo copy of the r-wide operand (factor over K, or U / V over R)
 // that the tensor-core side products read above rank 8.
-size_t adapter_split_ws(int64_t extent, int32_t r, int parts = 2);
+size_t adapter_split_ws(int64_t extent, int32_t r);
 size_t coldot_ws(int64_t R, int64_t N, int32_t r);
 // tickets: as for launch_rowdot (nullptr: no row splits on the tensor-core path)
 cudaError_t launch_coldot(const void* P, bool bf16, int64_t R, int64_t N, const float* aux,
                           int32_t r, float s, bool out_nr, float* out, void* ws,
                           cudaStream_t st, unsigned* tickets = nullptr,
-                          uint16_t* split_ws = nullptr, int parts = 2);
+                          uint16_t* split_ws = nullptr);
 // Two coldot products over the same R rows in one launch (the backward's
 // dA = s V^T X and dB = s dY^T U), each with its own partial buffer
 // (coldot_ws) and split scratch; *done = false (nothing launched) when the
@@ -120,13 +118,7 @@ cudaError_t launch_coldot_pair(const void* PA, int64_t NA, const float* auxA, bo
                                float* outA, void* wsA, uint16_t* splitA, const void* PB,
                                int64_t NB, const float* auxB, bool out_nrB, float* outB, void* wsB,
                                uint16_t* splitB, int64_t R, int32_t r, float s, cudaStream_t st,
-                               unsigned* tickets, bool* done, int parts = 2,
-                               bool split_done = false);
-// split_done: splitA and splitB hold the three parts already (rows of
-// adapter_split_ld(R) along R).
-bool coldot_takes(const void* P, int64_t R, int64_t N);
-int adapter_rank_rows(int32_t r);
-inline int64_t adapter_split_ld(int64_t extent) { return (extent + 7) / 8 * 8; }
+                               unsigned* tickets, bool* done);
 // out = scale * sum of the split partials.  pdl: launched with a
 // programmatic dependency on the kernel before it (which must have
 // triggered its dependents); the kernel waits for that grid first.

@@ -133,7 +133,7 @@ def test_zero_adapter_forward_and_gradient_are_exact(R, O, I):
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("r", [1, 8, 13, 16, 32, 64])
 @pytest.mark.parametrize("R,O,I", [(1, 300, 200), (19, 256, 512), (200, 520, 264), (1400, 1030, 300), (2300, 2048, 512),
-                                   (1201, 640, 9216)])
+                                   (1201, 640, 9216), (3001, 1024, 1003), (3001, 1003, 1024)])
 def test_forward_and_backward(R, O, I, r, dtype):
     W, X, dY, A, B = make(R, O, I, r, dtype, seed=10 + r)
     w, nw, s = weight(W)
@@ -167,7 +167,7 @@ def test_forward_and_backward(R, O, I, r, dtype):
 @pytest.mark.parametrize("R", [1, 40, 2000])
 @pytest.mark.parametrize("r", [8, 20])
 def test_parts_of_the_gradient_alone(R, r):
-    W, X, dY, A, B = make(R, 1096, 80, r, BF)
+    W, X, dY, A, B = make(R, 1096, 1080, r, BF)
     w, _, _ = weight(W)
     full = q.qlora_linear_bwd(w, X, dY, A, B, 16.0)
     for k in range(3):
