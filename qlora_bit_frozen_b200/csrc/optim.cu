@@ -44,7 +44,7 @@ struct Batch {
   Desc d[CAP];
 };
 constexpr int kFew = 60;    // below 4 KB of parameters
-constexpr int kSome = 240;
+constexpr int kSome = 125;  // 8 KB
 constexpr int kMany = 500;
 static_assert(sizeof(Batch<kMany>) + 128 <= 32764, "kernel parameter limit");
 
@@ -184,6 +184,8 @@ struct AdamWArgs {
   float step_size, inv_rbc2;  // lr / bc1, 1 / sqrt(bc2) (when control is null)
   double lr, b1d, b2d;
   const qlora_step_control* control;
+  float z;           // -0
+  int32_t follows;  // launched over the end of the call's launch before
 };
 
 // b^t by squaring: the same 64-bit products on the host and on the device.
@@ -211,30 +213,68 @@ __device__ __forceinline__ float warp_max_bits(float x) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
 }
 
-// Byte j of w as a float, exactly: the byte becomes the low mantissa bits of
-// 2^23.  Signed bytes come with their top bit flipped (128 more).
-__device__ __forceinline__ float byte_f32(uint32_t w, int j, float bias) {
-  return __fsub_rn(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | (uint32_t)j)), bias);
+// Two fp32 operations in one instruction, each rounded to nearest.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ uint64_t twice(float x) { return pair(x, x); }
+__device__ __forceinline__ float lo_of(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float hi_of(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// A product that an addition follows, as a fused multiply-add of z = -0 (which
+// leaves it and its sign as they are): a packed multiply and add were compiled
+// to one rounding, also with a constant for z, so z is an argument of the kernel.
+__device__ __forceinline__ uint64_t prod2(uint64_t a, float b, float z) { return fma2(a, twice(b), twice(z)); }
+__device__ __forceinline__ uint64_t abs2(uint64_t a) { return a & 0x7fffffff7fffffffull; }
+// max(|a|, |b|, |c|); a NaN wins.
+__device__ __forceinline__ float top3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float root_approx(float u) {
+  float a;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(u));
+  return a;
 }
 
-// rint(top sqrt(u)) with the sign of `sign` for u in [0, 1] (a little above by
-// rounding), as the definition has it: the square root and the product rounded
-// to nearest.  The approximate root is within 2^-22, so the product is within
-// 2^-13 (top <= 255) and rounds to the same integer unless it lies that close
-// to a half; only then is the exact root taken.  1.5 2^23 added rounds to
-// nearest even and leaves the two's complement integer in the low bits.
-template <bool SIGNED>
-__device__ __forceinline__ uint32_t code_of(float u, float top, float sign) {
-  float a;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(a) : "f"(u));
-  float y = __fmul_rn(a, top);
-  float t = __fadd_rn(y, 12582912.0f);
-  if (!(fabsf(__fsub_rn(y, __fsub_rn(t, 12582912.0f))) < 0.4998f)) {
-    y = __fmul_rn(__fsqrt_rn(u), top);
-    t = __fadd_rn(y, 12582912.0f);
-  }
-  const uint32_t k = __float_as_uint(t) & 255u;
-  return SIGNED && sign < 0.0f ? 0u - k : k;
+// Bytes 2 h and 2 h + 1 of w as floats, exactly: a byte becomes the low
+// mantissa bits of 2^23, which bias (2^23, and 128 more for signed bytes with
+// their top bit flipped) takes off again.
+__device__ __forceinline__ uint64_t bytes_f32(uint32_t w, int h, float bias) {
+  return add2(pair(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | (uint32_t)(2 * h))),
+                   __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | (uint32_t)(2 * h + 1)))),
+              twice(-bias));
+}
+
+// rint(top x) for |x| <= 1 (a little above by rounding) in the low bytes of the
+// sums with M = 1.5 2^23 (nearest, ties to even; two's complement), and how far
+// top x is from that integer at most.
+__device__ __forceinline__ uint64_t rounded(uint64_t x, float top, float& worst) {
+  const uint64_t M = twice(12582912.0f), t2 = twice(top);
+  const uint64_t r = fma2(x, t2, M);
+  const uint64_t d = fma2(x, t2, fma2(r, twice(-1.0f), M));
+  worst = top3(worst, lo_of(d), hi_of(d));
+  return r;
+}
+// The same for one value by the definition: the root and the product each
+// rounded to nearest.
+__device__ __forceinline__ float rounded_exact(float u, float top) {
+  return __fadd_rn(__fmul_rn(__fsqrt_rn(u), top), 12582912.0f);
 }
 
 // Four low bytes to a word.
@@ -242,88 +282,111 @@ __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, ui
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-template <int BITS>
-struct Block {  // a lane's share of a block, as loaded
-  float g[8], p[8];
-  float m[BITS == 32 ? 8 : 1], v[BITS == 32 ? 8 : 1];
+// One block.  Bound by HBM with 32-bit states; with 8-bit ones by instructions
+// as much as by HBM (16 bytes a value), which is why all but the division and
+// the root work on pairs, and the codes' roots are the approximate ones: their
+// products are within 255 (2^-22 + 2^-24) of the definition's, so they round to
+// the same integer unless within 1e-4 of a half; only then (2e-4, one test for
+// the lane's eight values) are the exact roots taken.
+template <int BITS, bool VEC>
+__device__ __forceinline__ void adamw_block(const Desc& d, int64_t blk, int lane, const AdamWArgs& a,
+                                            float scale, float step_size, float inv_rbc2) {
+  const int64_t at = blk * kBlock;
+  const int left = d.n - at < kBlock ? (int)(d.n - at) : kBlock;
+  float g[8], p[8], mf[8], vf[8];
   uint32_t mw[2], vw[2];
-  float ms, vs;
-};
-
-template <int BITS, bool VEC>
-__device__ __forceinline__ void load_block(const Desc& d, int64_t blk, int lane, Block<BITS>& b) {
-  const int64_t at = blk * kBlock;
-  const int left = d.n - at < kBlock ? (int)(d.n - at) : kBlock;
-  load_any<VEC>(d.g, d.gbf16, at, lane, left, b.g);
-  load_any<VEC>(d.p, d.pbf16, at, lane, left, b.p);
+  float ms = 0.0f, vs = 0.0f;
+  load_any<VEC>(d.g, d.gbf16, at, lane, left, g);
+  load_any<VEC>(d.p, d.pbf16, at, lane, left, p);
   if constexpr (BITS == 32) {
-    load_f32<VEC>((const float*)d.m + at, lane, left, b.m);
-    load_f32<VEC>((const float*)d.v + at, lane, left, b.v);
+    load_f32<VEC>((const float*)d.m + at, lane, left, mf);
+    load_f32<VEC>((const float*)d.v + at, lane, left, vf);
   } else {
-    load_codes<VEC>((const uint8_t*)d.m + at, lane, left, b.mw);
-    load_codes<VEC>((const uint8_t*)d.v + at, lane, left, b.vw);
-    b.ms = d.ms[blk];
-    b.vs = d.vs[blk];
+    load_codes<VEC>((const uint8_t*)d.m + at, lane, left, mw);
+    load_codes<VEC>((const uint8_t*)d.v + at, lane, left, vw);
+    ms = d.ms[blk];
+    vs = d.vs[blk];
   }
-}
-
-template <int BITS, bool VEC>
-__device__ __forceinline__ void step_block(const Desc& d, int64_t blk, int lane, Block<BITS>& b,
-                                           const AdamWArgs& a, float scale, float step_size,
-                                           float inv_rbc2) {
-  const int64_t at = blk * kBlock;
-  const int left = d.n - at < kBlock ? (int)(d.n - at) : kBlock;
-  float m[8], r[8];
-  float mmax = 0.0f, rmax = 0.0f;
+  uint64_t m[4], r[4];
+  float mtop = 0.0f, rtop = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float v;
+  for (int j = 0; j < 4; ++j) {
+    uint64_t v;
     if constexpr (BITS == 32) {
-      m[j] = b.m[j];
-      v = b.v[j];
+      m[j] = pair(mf[2 * j], mf[2 * j + 1]);
+      v = pair(vf[2 * j], vf[2 * j + 1]);
     } else {
-      const float km = __fmul_rn(byte_f32(b.mw[j >> 2] ^ 0x80808080u, j & 3, 8388736.0f), 1.0f / 127.0f);
-      const float kv = __fmul_rn(byte_f32(b.vw[j >> 2], j & 3, 8388608.0f), 1.0f / 255.0f);
-      m[j] = __fmul_rn(__fmul_rn(km, fabsf(km)), b.ms);
-      const float root = __fmul_rn(__fmul_rn(kv, kv), b.vs);
-      v = __fmul_rn(root, root);
+      const uint64_t km = mul2(bytes_f32(mw[j >> 1] ^ 0x80808080u, j & 1, 8388736.0f), twice(1.0f / 127.0f));
+      const uint64_t kv = mul2(bytes_f32(vw[j >> 1], j & 1, 8388608.0f), twice(1.0f / 255.0f));
+      m[j] = mul2(mul2(km, abs2(km)), twice(ms));
+      const uint64_t root = mul2(mul2(kv, kv), twice(vs));
+      v = mul2(root, root);
     }
-    const float g = __fmul_rn(b.g[j], scale);
-    m[j] = __fadd_rn(__fmul_rn(m[j], a.b1), __fmul_rn(g, a.omb1));
-    v = __fadd_rn(__fmul_rn(v, a.b2), __fmul_rn(__fmul_rn(g, g), a.omb2));
-    r[j] = __fsqrt_rn(v);
-    const float step =
-        __fdiv_rn(__fmul_rn(m[j], step_size), __fadd_rn(__fmul_rn(r[j], inv_rbc2), a.eps));
-    b.p[j] = __fsub_rn(__fmul_rn(b.p[j], a.decay), step);
+    const uint64_t gs = mul2(pair(g[2 * j], g[2 * j + 1]), twice(scale));
+    m[j] = add2(prod2(m[j], a.b1, a.z), prod2(gs, a.omb1, a.z));
+    v = add2(prod2(v, a.b2, a.z), prod2(mul2(gs, gs), a.omb2, a.z));
+    r[j] = pair(__fsqrt_rn(lo_of(v)), __fsqrt_rn(hi_of(v)));
+    const uint64_t num = mul2(m[j], twice(step_size));
+    const uint64_t den = add2(prod2(r[j], inv_rbc2, a.z), twice(a.eps));
+    const uint64_t step = pair(__fdiv_rn(lo_of(num), lo_of(den)), __fdiv_rn(hi_of(num), hi_of(den)));
+    const uint64_t pn = add2(prod2(pair(p[2 * j], p[2 * j + 1]), a.decay, a.z), step ^ 0x8000000080000000ull);
+    p[2 * j] = lo_of(pn);
+    p[2 * j + 1] = hi_of(pn);
     if constexpr (BITS == 32) {
-      b.v[j] = v;
+      mf[2 * j] = lo_of(m[j]);
+      mf[2 * j + 1] = hi_of(m[j]);
+      vf[2 * j] = lo_of(v);
+      vf[2 * j + 1] = hi_of(v);
     } else {
-      mmax = __uint_as_float(max(__float_as_uint(mmax), __float_as_uint(fabsf(m[j]))));
-      rmax = __uint_as_float(max(__float_as_uint(rmax), __float_as_uint(r[j])));
+      mtop = top3(mtop, lo_of(m[j]), hi_of(m[j]));
+      rtop = top3(rtop, lo_of(r[j]), hi_of(r[j]));
     }
   }
-  store_any<VEC>(d.p, d.pbf16, at, lane, left, b.p);
+  store_any<VEC>(d.p, d.pbf16, at, lane, left, p);
   if constexpr (BITS == 32) {
-    store_f32<VEC>((float*)d.m + at, lane, left, m);
-    store_f32<VEC>((float*)d.v + at, lane, left, b.v);
+    store_f32<VEC>((float*)d.m + at, lane, left, mf);
+    store_f32<VEC>((float*)d.v + at, lane, left, vf);
   } else {
-    mmax = warp_max_bits(mmax);
-    rmax = warp_max_bits(rmax);
-    const float im = inverse_of(mmax), iv = inverse_of(rmax);
-    uint32_t km[8], kv[8];
+    mtop = warp_max_bits(mtop);
+    rtop = warp_max_bits(rtop);
+    const float im = inverse_of(mtop), iv = inverse_of(rtop);
+    const float least = iv > 0.0f ? 1.0f / 255.0f : 0.0f;  // code 1
+    uint64_t km[4], kv[4];
+    float worst = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      km[j] = code_of<true>(__fmul_rn(fabsf(m[j]), im), 127.0f, m[j]);
-      kv[j] = code_of<false>(__fmul_rn(r[j], iv), 255.0f, 0.0f);
-      if (r[j] > 0.0f && iv > 0.0f) kv[j] = max(kv[j], 1u);
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t um = mul2(abs2(m[j]), twice(im)), uv = mul2(r[j], twice(iv));
+      km[j] = rounded(pair(copysignf(root_approx(lo_of(um)), lo_of(m[j])),
+                           copysignf(root_approx(hi_of(um)), hi_of(m[j]))), 127.0f, worst);
+      kv[j] = rounded(pair(fmaxf(root_approx(lo_of(uv)), lo_of(r[j]) > 0.0f ? least : 0.0f),
+                           fmaxf(root_approx(hi_of(uv)), hi_of(r[j]) > 0.0f ? least : 0.0f)), 255.0f, worst);
     }
-    const uint32_t mw[2] = {pack4(km[0], km[1], km[2], km[3]), pack4(km[4], km[5], km[6], km[7])};
-    const uint32_t vw[2] = {pack4(kv[0], kv[1], kv[2], kv[3]), pack4(kv[4], kv[5], kv[6], kv[7])};
-    store_codes<VEC>((uint8_t*)d.m + at, lane, left, mw);
-    store_codes<VEC>((uint8_t*)d.v + at, lane, left, vw);
+    uint32_t cm[8], cv[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      cm[2 * j] = (uint32_t)km[j];
+      cm[2 * j + 1] = (uint32_t)(km[j] >> 32);
+      cv[2 * j] = (uint32_t)kv[j];
+      cv[2 * j + 1] = (uint32_t)(kv[j] >> 32);
+    }
+    if (!(worst < 0.4998f)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float mj = j & 1 ? hi_of(m[j >> 1]) : lo_of(m[j >> 1]);
+        const float rj = j & 1 ? hi_of(r[j >> 1]) : lo_of(r[j >> 1]);
+        const uint32_t k = __float_as_uint(rounded_exact(__fmul_rn(fabsf(mj), im), 127.0f)) & 255u;
+        const uint32_t u = __float_as_uint(rounded_exact(__fmul_rn(rj, iv), 255.0f)) & 255u;
+        cm[j] = mj < 0.0f ? 0u - k : k;
+        cv[j] = rj > 0.0f && iv > 0.0f ? max(u, 1u) : u;
+      }
+    }
+    const uint32_t wm[2] = {pack4(cm[0], cm[1], cm[2], cm[3]), pack4(cm[4], cm[5], cm[6], cm[7])};
+    const uint32_t wv[2] = {pack4(cv[0], cv[1], cv[2], cv[3]), pack4(cv[4], cv[5], cv[6], cv[7])};
+    store_codes<VEC>((uint8_t*)d.m + at, lane, left, wm);
+    store_codes<VEC>((uint8_t*)d.v + at, lane, left, wv);
     if (lane == 0) {
-      d.ms[blk] = mmax;
-      d.vs[blk] = rmax;
+      d.ms[blk] = mtop;
+      d.vs[blk] = rtop;
     }
   }
 }
@@ -332,10 +395,16 @@ template <int BITS, int CAP>
 __global__ void __launch_bounds__(kThreads, 4)
     adamw_kernel(const __grid_constant__ Batch<CAP> b, const AdamWArgs a) {
   __shared__ float terms[2];
+  // The launches of one call share nothing: the next one may start as this one
+  // runs out of work, and ends only after it.
+  if (threadIdx.x == 0) griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   float scale = 1.0f, step_size = a.step_size, inv_rbc2 = a.inv_rbc2;
   if (a.control) {
-    if (a.control->skip) return;
+    if (a.control->skip) {
+      if (a.follows && threadIdx.x == 0) griddep_wait();
+      return;
+    }
     scale = a.control->scale;
     if (threadIdx.x == 0) bias_terms(a.lr, a.b1d, a.b2d, a.control->step, &terms[0], &terms[1]);
     __syncthreads();
@@ -344,20 +413,14 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
   const Run run = my_run(b.blocks);
   uint32_t blk = run.lo + (threadIdx.x >> 5);
-  if (blk >= run.hi) return;
-  int i = find(b, blk);
+  int i = blk < run.hi ? find(b, blk) : 0;
   for (; blk < run.hi; blk += kThreads / 32) {
     while (i + 1 < b.count && b.d[i + 1].first <= blk) ++i;
     const Desc& d = b.d[i];
-    Block<BITS> x;
-    if (d.vec) {
-      load_block<BITS, true>(d, blk - d.first, lane, x);
-      step_block<BITS, true>(d, blk - d.first, lane, x, a, scale, step_size, inv_rbc2);
-    } else {
-      load_block<BITS, false>(d, blk - d.first, lane, x);
-      step_block<BITS, false>(d, blk - d.first, lane, x, a, scale, step_size, inv_rbc2);
-    }
+    if (d.vec) adamw_block<BITS, true>(d, blk - d.first, lane, a, scale, step_size, inv_rbc2);
+    else adamw_block<BITS, false>(d, blk - d.first, lane, a, scale, step_size, inv_rbc2);
   }
+  if (a.follows && threadIdx.x == 0) griddep_wait();
 }
 
 // ------------------------------------------------------------------- norm
@@ -484,20 +547,29 @@ unsigned ctas_for(uint32_t blocks, int sms) {
 }
 
 template <int CAP>
-cudaError_t adamw_all(const qlora_tensor* t, int32_t count, int32_t bits, const AdamWArgs& a,
-                      cudaStream_t st) {
+cudaError_t adamw_all(const qlora_tensor* t, int32_t count, int32_t bits, AdamWArgs a, cudaStream_t st) {
   const int sms = sm_count();
+  a.follows = 0;
   for (int32_t i = 0; i < count;) {
     Batch<CAP> b;
     i = fill(b, t, count, i, bits, false);
     if (b.count == 0) break;
-    if (bits == 8) adamw_kernel<8, CAP><<<ctas_for(b.blocks, sms), kThreads, 0, st>>>(b, a);
-    else adamw_kernel<32, CAP><<<ctas_for(b.blocks, sms), kThreads, 0, st>>>(b, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas_for(b.blocks, sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.follows ? 1 : 0;
+    const cudaError_t e = bits == 8 ? cudaLaunchKernelEx(&cfg, adamw_kernel<8, CAP>, b, a)
+                                    : cudaLaunchKernelEx(&cfg, adamw_kernel<32, CAP>, b, a);
     count_launch();
-    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    a.follows = 1;
   }
-  return cudaSuccess;
+  return cudaGetLastError();
 }
 
 template <int CAP>
@@ -567,6 +639,7 @@ cudaError_t launch_adamw(const qlora_tensor* t, int32_t count, int32_t bits, int
   a.b1d = beta1;
   a.b2d = beta2;
   a.control = control;
+  a.z = -0.0f;
   if (!control) bias_terms(a.lr, a.b1d, a.b2d, step, &a.step_size, &a.inv_rbc2);
   return count <= kFew    ? adamw_all<kFew>(t, count, bits, a, st)
          : count <= kSome ? adamw_all<kSome>(t, count, bits, a, st)
