@@ -102,6 +102,36 @@ qlora_status read_header(const void* ws, cudaStream_t st, uint32_t out[3]) {
   return QLORA_OK;
 }
 
+// Flags in page-locked host memory that every device can write (one page,
+// allocated once): one for each call that is waiting for its kernel.  Null
+// where there is no such memory or all are taken.
+constexpr int kHostFlags = 64;
+std::mutex g_flag_mutex;
+uint32_t* g_flags = nullptr;
+bool g_flags_tried = false;
+uint64_t g_flags_taken = 0;
+
+volatile uint32_t* take_host_flag() {
+  std::lock_guard<std::mutex> lk(g_flag_mutex);
+  if (!g_flags_tried) {
+    g_flags_tried = true;
+    void* p = nullptr;
+    if (cudaHostAlloc(&p, kHostFlags * 64, cudaHostAllocPortable | cudaHostAllocMapped) != cudaSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    g_flags = (uint32_t*)p;
+  }
+  if (!g_flags || ~g_flags_taken == 0) return nullptr;
+  const int i = __builtin_ctzll(~g_flags_taken);
+  g_flags_taken |= 1ull << i;
+  return g_flags + 16 * i;  // a cache line each
+}
+void give_host_flag(volatile uint32_t* flag) {
+  std::lock_guard<std::mutex> lk(g_flag_mutex);
+  g_flags_taken &= ~(1ull << (((uint32_t*)flag - g_flags) / 16));
+}
+
 int64_t nf4_blocks(int64_t N, int32_t B) { return (N + B - 1) / B; }
 
 qlora_status check_weight(const qlora_weight* w, bool for_linear) {
@@ -551,7 +581,19 @@ qlora_status qlora_quantize_int8(const float* W, int64_t O, int64_t I, int8_t* c
   qlora_status st = device_ready();
   if (st != QLORA_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
-  st = cuda_status(launch_int8_quantize(W, O, I, codes, scale, ws, s));
+  if (volatile uint32_t* flag = take_host_flag()) {
+    // the kernel writes the flag straight into host memory: no clearing and no
+    // copy back around it
+    *flag = 0;
+    st = cuda_status(launch_int8_quantize(W, O, I, codes, scale, (uint32_t*)flag, s));
+    // (also after an error: nothing may write to the flag once it is given back)
+    if (cudaStreamSynchronize(s) != cudaSuccess) st = QLORA_ERR_CUDA;
+    const bool bad = *flag != 0;
+    give_host_flag(flag);
+    return st != QLORA_OK ? st : bad ? QLORA_ERR_NONFINITE : QLORA_OK;
+  }
+  if (cudaMemsetAsync(ws, 0, kWsHeader, s) != cudaSuccess) return QLORA_ERR_CUDA;
+  st = cuda_status(launch_int8_quantize(W, O, I, codes, scale, (uint32_t*)ws + 2, s));
   if (st != QLORA_OK) return st;
   uint32_t h[3];
   st = read_header(ws, s, h);

@@ -112,7 +112,7 @@ struct RowsArgs {
   const float* f;      // [K] column factors, nullable
   int8_t* codes;       // [R x pitch], zeros in the padding
   float* scale;        // [R]
-  uint32_t* hdr;       // non-finite flag, nullable
+  uint32_t* bad;       // set where a row has a NaN or Inf, nullable
   Clear clear;
 };
 
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(rows_threads<NV, FACTOR>()) rows_kernel(const 
     const float inv = reciprocal(s);
     if (threadIdx.x == 0) {
       a.scale[now] = s;
-      if (a.hdr && bits >= 0x7f800000u) atomicOr(a.hdr + 2, 1u);
+      if (a.bad && bits >= 0x7f800000u) *a.bad = 1;
     }
     uint32_t* q = reinterpret_cast<uint32_t*>(a.codes + now * a.pitch);
 #pragma unroll
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads) rows_any_kernel(const RowsArgs a) {
   const float s = row_scale(top);
   if (threadIdx.x == 0) {
     a.scale[row] = s;
-    if (a.hdr && top >= 0x7f800000u) atomicOr(a.hdr + 2, 1u);
+    if (a.bad && top >= 0x7f800000u) *a.bad = 1;
   }
   int8_t* q = a.codes + row * a.pitch;
   for (int64_t k = threadIdx.x; k < a.pitch; k += kThreads) {
@@ -549,9 +549,8 @@ RowsArgs rows_args(const Int8Call& c, void* ws, Int8Clear header) {
 }  // namespace
 
 cudaError_t launch_int8_quantize(const float* W, int64_t O, int64_t I, int8_t* codes, float* scale,
-                                 void* ws, cudaStream_t st) {
-  cudaError_t e = cudaMemsetAsync(ws, 0, kWsHeader, st);
-  if (e != cudaSuccess || O == 0) return e;
+                                 uint32_t* bad, cudaStream_t st) {
+  if (O == 0) return cudaSuccess;
   RowsArgs a = {};
   a.P = W;
   a.R = O;
@@ -559,7 +558,7 @@ cudaError_t launch_int8_quantize(const float* W, int64_t O, int64_t I, int8_t* c
   a.pitch = int8_pitch(I);
   a.codes = codes;
   a.scale = scale;
-  a.hdr = (uint32_t*)ws;
+  a.bad = bad;
   return launch_rows<float>(a, st);
 }
 

@@ -14,9 +14,10 @@ constexpr int64_t kInt8MaxK = 131072;
 
 constexpr int64_t int8_pitch(int64_t n) { return (n + 15) / 16 * 16; }
 
-// codes [O x pitch], scale [O] of W [O x I]; ws: the status header.
+// codes [O x pitch], scale [O] of W [O x I]; *bad (device or mapped host
+// memory) is set where W holds a NaN or Inf.
 cudaError_t launch_int8_quantize(const float* W, int64_t O, int64_t I, int8_t* codes, float* scale,
-                                 void* ws, cudaStream_t st);
+                                 uint32_t* bad, cudaStream_t st);
 cudaError_t launch_int8_dequantize(const int8_t* codes, const float* scale, int64_t O, int64_t I,
                                    float* out, cudaStream_t st);
 

@@ -354,20 +354,31 @@ struct SplitArgs {
   SplitJob job[2];
   int32_t r, NP;
 };
+// A block takes 64 entries of every factor row; a factor given as [n x r] is
+// turned in shared memory, so that both sides are read and written in runs.
 __global__ void __launch_bounds__(256) split_kernel(const SplitArgs a) {
+  __shared__ float tile[64][65];
   if (threadIdx.x == 0) griddep_launch_dependents();
-  const int k1 = (int)blockIdx.x >= a.job[0].blocks ? 1 : 0;
-  const SplitJob& b = a.job[k1];
-  const int64_t e = ((int64_t)blockIdx.x - (k1 ? a.job[0].blocks : 0)) * 256 + threadIdx.x;
-  if (e >= (int64_t)a.r * b.ld) return;
-  // neighbouring threads on neighbouring source entries
-  const int64_t j = b.kr ? e % a.r : e / b.ld, k = b.kr ? e / a.r : e % b.ld;
-  float v = k < b.n ? __ldg(b.src + (b.kr ? k * a.r + j : j * b.n + k)) : 0.0f;
+  const int second = (int)blockIdx.x >= a.job[0].blocks ? 1 : 0;
+  const SplitJob& b = a.job[second];
+  const int64_t k0 = ((int64_t)blockIdx.x - (second ? a.job[0].blocks : 0)) * 64;
+  if (b.kr) {
+    for (int e = threadIdx.x; e < 64 * a.r; e += 256) {
+      const int k = e / a.r, j = e - k * a.r;
+      tile[j][k] = k0 + k < b.n ? __ldg(b.src + k0 * a.r + e) : 0.0f;
+    }
+    __syncthreads();
+  }
+  for (int e = threadIdx.x; e < 64 * a.r; e += 256) {
+    const int j = e >> 6, k = e & 63;
+    if (k0 + k >= b.ld) continue;
+    float v = b.kr ? tile[j][k] : k0 + k < b.n ? __ldg(b.src + (int64_t)j * b.n + k0 + k) : 0.0f;
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    const __nv_bfloat16 h = __float2bfloat16_rn(v);
-    b.dst[((int64_t)q * a.NP + j) * b.ld + k] = __bfloat16_as_ushort(h);
-    v -= __bfloat162float(h);
+    for (int q = 0; q < 3; ++q) {
+      const __nv_bfloat16 h = __float2bfloat16_rn(v);
+      b.dst[((int64_t)q * a.NP + j) * b.ld + k0 + k] = __bfloat16_as_ushort(h);
+      v -= __bfloat162float(h);
+    }
   }
 }
 
@@ -418,7 +429,7 @@ cudaError_t launch_side_split(const SideFactor* f, int count, int32_t r, cudaStr
     b.n = f[i].n;
     b.ld = side_ld(f[i].n);
     b.kr = f[i].kr ? 1 : 0;
-    b.blocks = (int)up((int64_t)r * b.ld, 256);
+    b.blocks = (int)up(b.ld, 64);
     blocks += b.blocks;
   }
   if (blocks == 0) return cudaSuccess;
