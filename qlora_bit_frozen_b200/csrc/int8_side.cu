@@ -100,12 +100,65 @@ struct SideWalk {
   }
 };
 
-// CTA whose run of the job holds unit u.
-__device__ __forceinline__ int64_t side_owner(const SideArgs& p, int job, int64_t u) {
+// CTA whose run of the job holds unit u, and where that run begins.
+__device__ __forceinline__ int64_t side_owner(const SideArgs& p, int job, int64_t u, int64_t& lo) {
   int64_t c = u * gridDim.x / p.units[job];
   while (side_lo(p, job, c + 1) <= u) ++c;
-  while (side_lo(p, job, c) > u) --c;
+  while ((lo = side_lo(p, job, c)) > u) --c;
   return c;
+}
+
+// Sum of a tile's partial sums, in CTA order.  (side_lo walks on by its
+// quotient and remainder: with three 64-bit divisions for every CTA, and one
+// CTA's sums loaded after the other's, this took 4 us a CTA.)
+template <int NP>
+__device__ __forceinline__ void side_sum(const SideArgs& p, int job, int64_t u0, int64_t u1, int at,
+                                         float (&acc)[NP]) {
+  const int64_t G = gridDim.x, quo = p.units[job] / G, rest = p.units[job] % G;
+  int64_t lo;
+  int64_t c = side_owner(p, job, u0, lo);
+  int64_t rem = p.units[job] * c - lo * G;  // units c = lo G + rem
+  int which = lo >= u0 ? 0 : 1;  // the first segment of its run, unless that began in a tile before
+  auto next = [&](int64_t& from) {  // the next CTA with a run in the tile, or -1
+    while (lo < u1) {
+      int64_t hi = lo + quo;
+      rem += rest;
+      if (rem >= G) {
+        rem -= G;
+        ++hi;
+      }
+      const bool some = hi > lo;  // (more CTAs than chunks)
+      lo = hi;
+      const int64_t slot = ((c++ * 2 + job) * 2 + which) * NP * 128 + at;
+      which = 0;
+      if (some) {
+        from = slot;
+        return true;
+      }
+    }
+    return false;
+  };
+#pragma unroll
+  for (int j = 0; j < NP; ++j) acc[j] = 0.0f;
+  constexpr int kAhead = NP <= 16 ? 4 : NP <= 32 ? 2 : 1;  // CTAs whose sums are on their way at once
+  for (bool more = true; more;) {
+    float v[kAhead][NP];
+    bool have[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      int64_t from = 0;
+      have[q] = more && next(from);
+      more = have[q];
+#pragma unroll
+      for (int j = 0; j < NP; ++j) v[q][j] = have[q] ? __ldcg(p.part + from + j * 128) : 0.0f;
+    }
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+      if (have[q]) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) acc[j] += v[q][j];
+      }
+  }
 }
 
 __host__ __device__ constexpr uint32_t idesc_bf16(int N, bool a_mn) {
@@ -316,16 +369,7 @@ __global__ void __launch_bounds__(kSideThreads, 1)
         const bool last = *last_flag != 0;
         __threadfence();
         if (last) {
-          const int64_t c0 = side_owner(p, job, u0), c1 = side_owner(p, job, u0 + o.chunks - 1);
-#pragma unroll
-          for (int j = 0; j < NP; ++j) acc[j] = 0.0f;
-          for (int64_t c = c0; c <= c1; ++c) {
-            if (side_lo(p, job, c) == side_lo(p, job, c + 1)) continue;  // more CTAs than chunks
-            // the first segment of its run, unless that began in a tile before
-            const float* part = slot(c, side_lo(p, job, c) >= u0 ? 0 : 1);
-#pragma unroll
-            for (int j = 0; j < NP; ++j) acc[j] += __ldcg(part + j * 128);
-          }
+          side_sum<NP>(p, job, u0, u0 + o.chunks, 32 * quad + lane, acc);
           side_write<NP>(o, p.r, m, acc);
         }
         asm volatile("bar.sync 1, 128;" ::: "memory");  // all have read the flag
