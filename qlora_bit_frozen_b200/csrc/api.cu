@@ -253,13 +253,12 @@ BwdLayout bwd_layout(const qlora_weight* w, int64_t R, int32_t r, int32_t comput
   return L;
 }
 
-// INT8 weights: what the first kernel of a call clears (the status header, the
-// tickets), U and V, the parts of the factors and of U and V and the partial
+// INT8 weights: the status header (cleared by the first kernel of a call), U and V, the parts of the factors and of U and V and the partial
 // sums of the tensor-core side products (or, for activations that those do not
 // take, the scratch of the fp32 ones), then the quantized rows and the
 // product's own.
 struct Int8Layout {
-  size_t tickets = 0, cleared = 0, u = 0, v = 0, fA = 0, fB = 0, fU = 0, fV = 0, part = 0, bt = 0, red = 0,
+  size_t u = 0, v = 0, fA = 0, fB = 0, fU = 0, fV = 0, part = 0, bt = 0, red = 0,
          rows = 0, total = 0;
 };
 
@@ -271,9 +270,6 @@ Int8Layout int8_layout(const qlora_weight* w, int64_t R, int32_t r, bool bwd, in
     off += align_up(bytes, 256);
     return at;
   };
-  const int64_t columns = bwd ? side_tiles(w->I) + side_tiles(w->O) : 0, rows = 2 * side_tiles(R);
-  L.tickets = take((size_t)(columns > rows ? columns : rows) * 4);
-  L.cleared = off;
   L.u = take((size_t)R * r * 4);
   if (bwd) L.v = take((size_t)R * r * 4);
   if (compute == QLORA_COMPUTE_BF16) {
@@ -321,7 +317,7 @@ cudaError_t int8_fwd(const qlora_weight* w, const void* X, int64_t R, const floa
   auto at = [&](size_t off) { return (char*)ws + off; };
   float* U = U_out ? U_out : (float*)at(L.u);
   const Int8Call c = int8_call(w, false, bf16, R, X, U, B, r, sc, Y);
-  const Int8Clear header = {ws, L.cleared};
+  const Int8Clear header = {ws, kWsZeroed};
   cudaError_t e;
   if (int8_few_applies(R, w->I, r)) {
     Int8Few f = {};
@@ -336,7 +332,7 @@ cudaError_t int8_fwd(const qlora_weight* w, const void* X, int64_t R, const floa
       const SideProduct p = {X, w->I, fA, U, nullptr, false, 1.0f};
       e = launch_side_split(&f, 1, r, s);
       if (e == cudaSuccess)
-        e = launch_side(&p, 1, false, R, r, at(L.part), (uint32_t*)at(L.tickets), (uint32_t*)ws, s);
+        e = launch_side(&p, 1, false, R, r, at(L.part), (uint32_t*)ws, s);
     } else if (e == cudaSuccess) {
       e = launch_rowdot(X, bf16, R, w->I, A, false, r, U, s);
     }
@@ -356,8 +352,7 @@ cudaError_t int8_bwd(const qlora_weight* w, const void* X, const void* dY, int64
   const float* U = U_in ? U_in : Uw;
   uint16_t *fA = (uint16_t*)at(L.fA), *fB = (uint16_t*)at(L.fB), *fU = (uint16_t*)at(L.fU),
            *fV = (uint16_t*)at(L.fV);
-  uint32_t* tickets = (uint32_t*)at(L.tickets);
-  const Int8Clear header = {ws, L.cleared};
+  const Int8Clear header = {ws, kWsZeroed};
   const Int8Call c = int8_call(w, true, bf16, R, dY, V, A, r, sc, dX);
   const bool want_v = dX || dA, new_u = dB && !U_in;
   // which matrix the tensor-core side products take (else the fp32 ones do)
@@ -369,14 +364,14 @@ cudaError_t int8_bwd(const qlora_weight* w, const void* X, const void* dY, int64
     if (dA && sX) p[n++] = {X, w->I, fV, dA, nullptr, true, sc};
     if (dB && sY) p[n++] = {dY, w->O, fU, dB, nullptr, false, sc};
     cudaError_t e = cudaSuccess;
-    if (n) e = launch_side(p, n, true, R, r, at(L.part), tickets, (uint32_t*)ws, s);
+    if (n) e = launch_side(p, n, true, R, r, at(L.part), (uint32_t*)ws, s);
     if (e == cudaSuccess && dA && !sX) e = launch_coldot(X, bf16, R, w->I, V, r, sc, false, dA, at(L.red), s);
     if (e == cudaSuccess && dB && !sY) e = launch_coldot(dY, bf16, R, w->O, U, r, sc, true, dB, at(L.red), s);
     return e;
   };
   cudaError_t e;
   if (R == 0) {
-    e = cudaMemsetAsync(ws, 0, L.cleared, s);
+    e = cudaMemsetAsync(ws, 0, kWsZeroed, s);
     return e != cudaSuccess ? e : columns();  // zeros
   }
   if (int8_few_applies(R, w->O, r) && int8_few_applies(R, w->I, r)) {
@@ -406,7 +401,7 @@ cudaError_t int8_bwd(const qlora_weight* w, const void* X, const void* dY, int64
       e = launch_int8_product(c, at(L.rows), (uint32_t*)ws, &f, s);
     return e;
   }
-  e = dX ? launch_int8_rows(c, at(L.rows), header, s) : cudaMemsetAsync(ws, 0, L.cleared, s);
+  e = dX ? launch_int8_rows(c, at(L.rows), header, s) : cudaMemsetAsync(ws, 0, kWsZeroed, s);
   // the parts of the factors, then V and U (with their own parts where a
   // tensor-core product makes them, else split after it)
   SideFactor f[2], late[2];
@@ -427,7 +422,7 @@ cudaError_t int8_bwd(const qlora_weight* w, const void* X, const void* dY, int64
     else f[nf++] = {U, fU, R, true};
   }
   if (e == cudaSuccess) e = launch_side_split(f, nf, r, s);
-  if (e == cudaSuccess && np) e = launch_side(p, np, false, R, r, at(L.part), tickets, (uint32_t*)ws, s);
+  if (e == cudaSuccess && np) e = launch_side(p, np, false, R, r, at(L.part), (uint32_t*)ws, s);
   if (e == cudaSuccess && want_v && !sY)
     e = launch_rowdot(dY, bf16, R, w->O, B, true, r, V, s, nullptr, nullptr, 0, 0, 1.0f, nullptr,
                       (float*)at(L.bt));

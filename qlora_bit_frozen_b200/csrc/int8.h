@@ -88,7 +88,6 @@ int side_np(int32_t r);
 int64_t side_ld(int64_t n);
 size_t side_parts_bytes(int64_t n, int32_t r);
 size_t side_part_ws(int32_t r);     // scratch of one launch
-int64_t side_tiles(int64_t m);      // tickets it takes for m rows of output
 bool side_takes(const void* P, int64_t R, int64_t N);
 struct SideFactor {
   const float* src;
@@ -106,9 +105,8 @@ struct SideProduct {
   bool transposed;
   float s;
 };
-// One or two products in one launch: P L^T (rows) or P^T T (columns).  tickets:
-// side_tiles of each output, zero, left zero.
+// One or two products in one launch: P L^T (rows) or P^T T (columns).
 cudaError_t launch_side(const SideProduct* f, int count, bool columns, int64_t R, int32_t r, void* part,
-                        uint32_t* tickets, uint32_t* hdr, cudaStream_t st);
+                        uint32_t* hdr, cudaStream_t st);
 
 }  // namespace qlora

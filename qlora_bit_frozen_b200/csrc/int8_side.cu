@@ -14,9 +14,11 @@
 // 2e-7 of the result where one running sum over 8192 tokens had 3e-6 to 9e-6.
 //
 // Each product's chunks, tile after tile, are dealt out in equal runs over the
-// SMs; a tile that several CTAs share is summed by the last of them, in CTA
-// order.  (The runs do not depend on what else is in the launch: a gradient has
-// the same bits whichever others are wanted.)  Bound by HBM on the large matrix.
+// SMs; the partial sums of a tile that several CTAs share are added up in CTA
+// order by a second, small launch.  (By the last CTA of a tile, that held up its
+// own run: 73 us where this takes 50.)  The runs do not depend on what else is in
+// the launch: a gradient has the same bits whichever others are wanted.  Bound
+// by HBM on the large matrix.
 #include "common.cuh"
 #include "int8.h"
 #include "int8_dev.cuh"
@@ -58,15 +60,14 @@ struct SideArgs {
   SideOut job[2];
   int64_t tiles[2];   // the second may be 0
   int64_t units[2];   // chunks of all the job's tiles
-  int32_t r;
+  int32_t r, ctas;
   float* part;        // [CTAs][2 jobs][2][NP][128]
-  uint32_t* tickets;  // [tiles of both], zero, left zero
   uint32_t* err;
   uint64_t wait_ns;
 };
 
 __device__ __forceinline__ int64_t side_lo(const SideArgs& p, int job, int64_t cta) {
-  return p.units[job] * cta / gridDim.x;
+  return p.units[job] * cta / p.ctas;
 }
 
 // The chunks of this CTA: its run of job 0, then its run of job 1.
@@ -102,63 +103,10 @@ struct SideWalk {
 
 // CTA whose run of the job holds unit u, and where that run begins.
 __device__ __forceinline__ int64_t side_owner(const SideArgs& p, int job, int64_t u, int64_t& lo) {
-  int64_t c = u * gridDim.x / p.units[job];
+  int64_t c = u * p.ctas / p.units[job];
   while (side_lo(p, job, c + 1) <= u) ++c;
   while ((lo = side_lo(p, job, c)) > u) --c;
   return c;
-}
-
-// Sum of a tile's partial sums, in CTA order.  (side_lo walks on by its
-// quotient and remainder: with three 64-bit divisions for every CTA, and one
-// CTA's sums loaded after the other's, this took 4 us a CTA.)
-template <int NP>
-__device__ __forceinline__ void side_sum(const SideArgs& p, int job, int64_t u0, int64_t u1, int at,
-                                         float (&acc)[NP]) {
-  const int64_t G = gridDim.x, quo = p.units[job] / G, rest = p.units[job] % G;
-  int64_t lo;
-  int64_t c = side_owner(p, job, u0, lo);
-  int64_t rem = p.units[job] * c - lo * G;  // units c = lo G + rem
-  int which = lo >= u0 ? 0 : 1;  // the first segment of its run, unless that began in a tile before
-  auto next = [&](int64_t& from) {  // the next CTA with a run in the tile, or -1
-    while (lo < u1) {
-      int64_t hi = lo + quo;
-      rem += rest;
-      if (rem >= G) {
-        rem -= G;
-        ++hi;
-      }
-      const bool some = hi > lo;  // (more CTAs than chunks)
-      lo = hi;
-      const int64_t slot = ((c++ * 2 + job) * 2 + which) * NP * 128 + at;
-      which = 0;
-      if (some) {
-        from = slot;
-        return true;
-      }
-    }
-    return false;
-  };
-#pragma unroll
-  for (int j = 0; j < NP; ++j) acc[j] = 0.0f;
-  constexpr int kAhead = NP <= 16 ? 4 : NP <= 32 ? 2 : 1;  // CTAs whose sums are on their way at once
-  for (bool more = true; more;) {
-    float v[kAhead][NP];
-    bool have[kAhead];
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
-      int64_t from = 0;
-      have[q] = more && next(from);
-      more = have[q];
-#pragma unroll
-      for (int j = 0; j < NP; ++j) v[q][j] = have[q] ? __ldcg(p.part + from + j * 128) : 0.0f;
-    }
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q)
-      if (have[q]) {
-#pragma unroll
-        for (int j = 0; j < NP; ++j) acc[j] += v[q][j];
-      }
-  }
 }
 
 __host__ __device__ constexpr uint32_t idesc_bf16(int N, bool a_mn) {
@@ -209,11 +157,10 @@ __global__ void __launch_bounds__(kSideThreads, 1)
   uint64_t* acc_empty = acc_full + 2;
   volatile uint32_t* tmem_slot = (volatile uint32_t*)(acc_empty + 2);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  volatile uint32_t* last_flag = tmem_slot + 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    griddep_launch_dependents();  // what is queued behind waits for this grid itself
+    griddep_launch_dependents();  // the summing launch waits for this grid itself
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
@@ -351,28 +298,9 @@ __global__ void __launch_bounds__(kSideThreads, 1)
       if (run == o.chunks) {
         side_write<NP>(o, p.r, m, acc);
       } else {
-        const int64_t id = (job ? p.tiles[0] : 0) + tile, u0 = tile * o.chunks;
-        auto slot = [&](int64_t cta, int which) {
-          return p.part + ((cta * 2 + job) * 2 + which) * NP * 128 + 32 * quad + lane;
-        };
-        float* mine = slot(blockIdx.x, segment ? 1 : 0);
+        float* mine = p.part + (((int64_t)blockIdx.x * 2 + job) * 2 + (segment ? 1 : 0)) * NP * 128 + 32 * quad + lane;
 #pragma unroll
         for (int j = 0; j < NP; ++j) mine[j * 128] = acc[j];
-        __threadfence();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (warp == 2 && lane == 0) {
-          const bool last = atomicAdd(p.tickets + id, (uint32_t)run) + (uint32_t)run == (uint32_t)o.chunks;
-          if (last) p.tickets[id] = 0;
-          *last_flag = last;
-        }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        const bool last = *last_flag != 0;
-        __threadfence();
-        if (last) {
-          side_sum<NP>(p, job, u0, u0 + o.chunks, 32 * quad + lane, acc);
-          side_write<NP>(o, p.r, m, acc);
-        }
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // all have read the flag
       }
       run = 0;
       segment = run_ends ? 0 : segment + 1;
@@ -384,6 +312,62 @@ __global__ void __launch_bounds__(kSideThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 2 * kCols);
   }
+}
+
+// The tiles that several CTAs shared: their partial sums in CTA order.  One CTA
+// a tile, a thread an output row, a few CTAs' sums on their way at once.
+template <int NP>
+__global__ void __launch_bounds__(128) side_sum_kernel(const SideArgs p) {
+  const int job = (int64_t)blockIdx.x >= p.tiles[0] ? 1 : 0;
+  const SideOut& o = p.job[job];
+  const int64_t tile = (int64_t)blockIdx.x - (job ? p.tiles[0] : 0), u0 = tile * o.chunks, u1 = u0 + o.chunks;
+  int64_t lo;
+  int64_t c = side_owner(p, job, u0, lo);
+  griddep_wait();  // every CTA: this grid ends only after the one before it
+  if (side_lo(p, job, c + 1) >= u1) return;  // one CTA had it all (and has written it)
+  // walk on from CTA c by the quotient and remainder of units c / ctas
+  const int64_t quo = p.units[job] / p.ctas, rest = p.units[job] % p.ctas;
+  int64_t rem = p.units[job] * c - lo * p.ctas;
+  int which = lo >= u0 ? 0 : 1;  // the first segment of its run, unless that began in a tile before
+  auto next = [&](int64_t& from) {  // the next CTA with a run in the tile
+    while (lo < u1) {
+      int64_t hi = lo + quo;
+      rem += rest;
+      if (rem >= p.ctas) {
+        rem -= p.ctas;
+        ++hi;
+      }
+      const bool some = hi > lo;  // (more CTAs than chunks)
+      lo = hi;
+      from = ((c++ * 2 + job) * 2 + which) * NP * 128 + threadIdx.x;
+      which = 0;
+      if (some) return true;
+    }
+    return false;
+  };
+  float acc[NP];
+#pragma unroll
+  for (int j = 0; j < NP; ++j) acc[j] = 0.0f;
+  constexpr int kAhead = NP <= 16 ? 4 : NP <= 32 ? 2 : 1;
+  for (bool more = true; more;) {
+    float v[kAhead][NP];
+    bool have[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      int64_t from = 0;
+      have[q] = more && next(from);
+      more = have[q];
+#pragma unroll
+      for (int j = 0; j < NP; ++j) v[q][j] = have[q] ? __ldcg(p.part + from + j * 128) : 0.0f;
+    }
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+      if (have[q]) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) acc[j] += v[q][j];
+      }
+  }
+  side_write<NP>(o, p.r, tile * 128 + threadIdx.x, acc);
 }
 
 // The three bf16 parts of up to two fp32 factors, [3][NP][ld], zeros past n
@@ -429,22 +413,35 @@ __global__ void __launch_bounds__(256) split_kernel(const SplitArgs a) {
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <bool A_MN, int NP>
-cudaError_t side_go(const CUtensorMap* t, const SideArgs& a, unsigned ctas, cudaStream_t st) {
+cudaError_t side_go(const CUtensorMap* t, const SideArgs& a, cudaStream_t st) {
   static std::atomic<bool> done[kMaxDevices];
-  const cudaError_t e = allow_smem(side_kernel<A_MN, NP>, SideCfg<NP>::kSmem, done);
+  cudaError_t e = allow_smem(side_kernel<A_MN, NP>, SideCfg<NP>::kSmem, done);
   if (e != cudaSuccess) return e;
-  side_kernel<A_MN, NP><<<ctas, kSideThreads, SideCfg<NP>::kSmem, st>>>(t[0], t[1], t[2], t[3], a);
+  side_kernel<A_MN, NP><<<(unsigned)a.ctas, kSideThreads, SideCfg<NP>::kSmem, st>>>(t[0], t[1], t[2], t[3], a);
   count_launch();
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.tiles[0] + a.tiles[1]));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, side_sum_kernel<NP>, a);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <bool A_MN>
-cudaError_t side_rank(const CUtensorMap* t, const SideArgs& a, int NP, unsigned ctas, cudaStream_t st) {
+cudaError_t side_rank(const CUtensorMap* t, const SideArgs& a, int NP, cudaStream_t st) {
   switch (NP) {
-    case 8: return side_go<A_MN, 8>(t, a, ctas, st);
-    case 16: return side_go<A_MN, 16>(t, a, ctas, st);
-    case 32: return side_go<A_MN, 32>(t, a, ctas, st);
-    default: return side_go<A_MN, 64>(t, a, ctas, st);
+    case 8: return side_go<A_MN, 8>(t, a, st);
+    case 16: return side_go<A_MN, 16>(t, a, st);
+    case 32: return side_go<A_MN, 32>(t, a, st);
+    default: return side_go<A_MN, 64>(t, a, st);
   }
 }
 
@@ -456,7 +453,6 @@ size_t side_parts_bytes(int64_t n, int32_t r) {
   return align_up((size_t)3 * side_np(r) * (size_t)side_ld(n) * 2, 256);
 }
 size_t side_part_ws(int32_t r) { return (size_t)sm_count() * 4 * side_np(r) * 128 * 4; }
-int64_t side_tiles(int64_t m) { return up(m, 128); }
 bool side_takes(const void* P, int64_t R, int64_t N) {
   return R > 0 && R <= INT32_MAX - 256 && N % 8 == 0 && (uintptr_t)P % 16 == 0;
 }
@@ -483,7 +479,7 @@ cudaError_t launch_side_split(const SideFactor* f, int count, int32_t r, cudaStr
 }
 
 cudaError_t launch_side(const SideProduct* f, int count, bool columns, int64_t R, int32_t r, void* part,
-                        uint32_t* tickets, uint32_t* hdr, cudaStream_t st) {
+                        uint32_t* hdr, cudaStream_t st) {
   const int NP = side_np(r);
   CUtensorMap t[4];
   SideArgs a = {};
@@ -498,7 +494,7 @@ cudaError_t launch_side(const SideProduct* f, int count, bool columns, int64_t R
     o.chunks = (int32_t)up(o.steps, kChunk);
     o.transposed = f[i].transposed ? 1 : 0;
     o.s = f[i].s;
-    a.tiles[i] = side_tiles(M);
+    a.tiles[i] = up(M, 128);
     a.units[i] = a.tiles[i] * o.chunks;
     const int64_t ld = side_ld(K);
     if (!make_map_2d(&t[2 * i], f[i].P, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)N, (uint64_t)R,
@@ -514,11 +510,10 @@ cudaError_t launch_side(const SideProduct* f, int count, bool columns, int64_t R
   }
   a.r = r;
   a.part = (float*)part;
-  a.tickets = tickets;
   a.err = hdr;
   a.wait_ns = kWaitLimitNs;
-  const unsigned ctas = (unsigned)sm_count();
-  return columns ? side_rank<true>(t, a, NP, ctas, st) : side_rank<false>(t, a, NP, ctas, st);
+  a.ctas = sm_count();
+  return columns ? side_rank<true>(t, a, NP, st) : side_rank<false>(t, a, NP, st);
 }
 
 }  // namespace qlora
