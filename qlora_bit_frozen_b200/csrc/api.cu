@@ -258,7 +258,7 @@ BwdLayout bwd_layout(const qlora_weight* w, int64_t R, int32_t r, int32_t comput
 // take, the scratch of the fp32 ones), then the quantized rows and the
 // product's own.
 struct Int8Layout {
-  size_t u = 0, v = 0, fA = 0, fB = 0, fU = 0, fV = 0, part = 0, bt = 0, red = 0,
+  size_t u = 0, v = 0, fA = 0, fB = 0, fU = 0, fV = 0, part = 0, red = 0,
          rows = 0, total = 0;
 };
 
@@ -282,7 +282,6 @@ Int8Layout int8_layout(const qlora_weight* w, int64_t R, int32_t r, bool bwd, in
     L.part = take(side_part_ws(r));
   }
   if (bwd) {
-    L.bt = take((size_t)r * w->O * 4);
     const size_t a = coldot_ws(R, w->I, r), b = coldot_ws(R, w->O, r);
     L.red = take(a > b ? a : b);
   }
@@ -334,7 +333,8 @@ cudaError_t int8_fwd(const qlora_weight* w, const void* X, int64_t R, const floa
       if (e == cudaSuccess)
         e = launch_side(&p, 1, false, R, r, at(L.part), (uint32_t*)ws, s);
     } else if (e == cudaSuccess) {
-      e = launch_rowdot(X, bf16, R, w->I, A, false, r, U, s);
+      const Int8Dot d = {X, A, U, w->I, false};
+      e = launch_int8_dots(&d, 1, bf16, R, r, s);
     }
   }
   if (e == cudaSuccess) e = launch_int8_product(c, at(L.rows), (uint32_t*)ws, nullptr, s);
@@ -423,10 +423,11 @@ cudaError_t int8_bwd(const qlora_weight* w, const void* X, const void* dY, int64
   }
   if (e == cudaSuccess) e = launch_side_split(f, nf, r, s);
   if (e == cudaSuccess && np) e = launch_side(p, np, false, R, r, at(L.part), (uint32_t*)ws, s);
-  if (e == cudaSuccess && want_v && !sY)
-    e = launch_rowdot(dY, bf16, R, w->O, B, true, r, V, s, nullptr, nullptr, 0, 0, 1.0f, nullptr,
-                      (float*)at(L.bt));
-  if (e == cudaSuccess && new_u && !sX) e = launch_rowdot(X, bf16, R, w->I, A, false, r, Uw, s);
+  Int8Dot d[2];
+  int nd = 0;
+  if (want_v && !sY) d[nd++] = {dY, B, V, w->O, true};
+  if (new_u && !sX) d[nd++] = {X, A, Uw, w->I, false};
+  if (e == cudaSuccess && nd) e = launch_int8_dots(d, nd, bf16, R, r, s);
   if (e == cudaSuccess) e = launch_side_split(late, nlate, r, s);
   if (e == cudaSuccess) e = columns();
   if (e == cudaSuccess && dX) e = launch_int8_product(c, at(L.rows), (uint32_t*)ws, nullptr, s);

@@ -375,101 +375,129 @@ __device__ __forceinline__ void few_row(const T* x, int64_t k, int64_t K, float 
   }
 }
 
-// A token and eight columns of its factor per CTA; the CTA of the first eight
-// also quantizes the token.  In a wide call K and r are multiples of 8 and 4
-// and everything is 16-byte aligned.  A factor [r x K] is read eight elements
-// a thread, a factor [K x r] one row a thread (eight rows in flight), so that
-// either way neighbouring threads read neighbouring bytes.
-template <typename T, bool KR, bool WIDE>
-__device__ __forceinline__ void few_token(const FewArgs& a, const FewJob& job, int t, int j0, float (*sums)[8],
-                                          uint32_t* buf) {
+// TOK tokens and eight columns of their factor per CTA; with one token the CTA
+// of the first eight columns also quantizes it.  In a wide call K is a multiple
+// of 8 (and, for factors [K x r], r of 4) and everything is 16-byte aligned.  A
+// factor [r x K] is read eight elements a thread, a factor [K x r] one row a
+// thread (eight rows in flight), so that either way neighbouring threads read
+// neighbouring bytes.
+template <typename T, bool KR, bool WIDE, int TOK>
+__device__ __forceinline__ void few_tokens(const FewArgs& a, const FewJob& job, int t0, int j0,
+                                           float (*sums)[8 * TOK], uint32_t* buf) {
   const int64_t K = job.K;
-  const T* x = (const T*)job.P + t * K;
-  const bool quantize = job.quantize && j0 == 0;
+  const T* x = (const T*)job.P + t0 * K;
+  const bool quantize = TOK == 1 && job.quantize && j0 == 0;
   const float* f = a.rows.f;
-  const int cols = min(8, a.r - j0), threads = (int)blockDim.x;
-  float acc[8] = {};
+  const int cols = min(8, a.r - j0), toks = TOK == 1 ? 1 : min(TOK, a.R - t0), threads = (int)blockDim.x;
+  float acc[TOK][8] = {};
   uint32_t top = 0;
   for (int64_t base = 0; base < K; base += threads * 8) {
-    float v[8] = {};
-    if (KR) {
+    float v[TOK][8] = {};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t k = base + threads * i + threadIdx.x;
-        if (k < K) v[i] = to_f32(x[k]);
+    for (int t = 0; t < TOK; ++t) {
+      if (t >= toks) continue;
+      if (KR) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t k = base + threads * i + threadIdx.x;
+          if (k < K) v[t][i] = to_f32(x[t * K + k]);
+        }
+      } else {
+        few_row<T, WIDE>(x + t * K, base + (int64_t)threadIdx.x * 8, K, v[t]);
       }
-    } else {
-      few_row<T, WIDE>(x, base + (int64_t)threadIdx.x * 8, K, v);
     }
-    float l[8][8];
-    if (KR) {
+    // Row q of the factor's block: its row j0 + q of [r x K], or row k of [K x r].
+    auto factor = [&](int q, float (&l)[8]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t k = base + threads * i + threadIdx.x;
+      for (int i = 0; i < 8; ++i) l[i] = 0.0f;
+      if (KR) {
+        const int64_t k = base + threads * q + threadIdx.x;
+        if (k >= K) return;
+        const float* p = job.L + k * a.r + j0;
 #pragma unroll
         for (int j = 0; j < 8; j += 4) {
-          float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (k < K) {
-            const float* p = job.L + k * a.r + j0 + j;
-            if (WIDE) {
-              if (j < cols) w = __ldg(reinterpret_cast<const float4*>(p));
-            } else {
-              if (j < cols) w.x = __ldg(p);
-              if (j + 1 < cols) w.y = __ldg(p + 1);
-              if (j + 2 < cols) w.z = __ldg(p + 2);
-              if (j + 3 < cols) w.w = __ldg(p + 3);
+          if (WIDE) {
+            if (j < cols) {
+              const float4 w = __ldg(reinterpret_cast<const float4*>(p + j));
+              l[j] = w.x; l[j + 1] = w.y; l[j + 2] = w.z; l[j + 3] = w.w;
             }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (j + i < cols) l[j + i] = __ldg(p + j + i);
           }
-          l[i][j] = w.x; l[i][j + 1] = w.y; l[i][j + 2] = w.z; l[i][j + 3] = w.w;
         }
+      } else if (q < cols) {
+        few_row<float, WIDE>(job.L + (int64_t)(j0 + q) * K, base + (int64_t)threadIdx.x * 8, K, l);
       }
+    };
+    if constexpr (TOK == 1) {
+      // All of it on its way before the first product; this loop nest is what the
+      // compiler keeps in that order (16 loads a thread in flight).
+      float l[8][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int q = 0; q < 8; ++q) factor(q, l[q]);
+      if (KR) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = fmaf(v[i], l[i][j], acc[j]);
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[0][j] = fmaf(v[0][q], l[q][j], acc[0][j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[0][j] = fmaf(v[0][i], l[j][i], acc[0][j]);
+      }
     } else {
-      const int64_t k = base + (int64_t)threadIdx.x * 8;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int q = 0; q < 8; ++q) {
+        float l[8];
+        factor(q, l);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) l[j][i] = 0.0f;
-        if (j < cols) few_row<float, WIDE>(job.L + (int64_t)(j0 + j) * K, k, K, l[j]);
+        for (int t = 0; t < TOK; ++t)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (KR) acc[t][i] = fmaf(v[t][q], l[i], acc[t][i]);
+            else acc[t][q] = fmaf(v[t][i], l[i], acc[t][q]);
+          }
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[j] = fmaf(v[i], l[j][i], acc[j]);
     }
     if (quantize) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int64_t k = KR ? base + threads * i + threadIdx.x : base + (int64_t)threadIdx.x * 8 + i;
-        float y = v[i];
+        float y = v[0][i];
         if (f && k < K) y = __fmul_rn(y, __ldg(f + k));
         top = max(top, __float_as_uint(fabsf(y)));
       }
     }
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int t = 0; t < TOK; ++t)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[t][j] += __shfl_xor_sync(0xffffffffu, acc[t][j], o);
   if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sums[threadIdx.x >> 5][j] = acc[j];
+    for (int t = 0; t < TOK; ++t)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sums[threadIdx.x >> 5][8 * t + j] = acc[t][j];
   }
   top = block_max_bits(top, buf);
-  if ((int)threadIdx.x < cols) {
+  if ((int)threadIdx.x < 8 * toks && (int)(threadIdx.x & 7) < cols) {
     float s = 0.0f;
     for (int w = 0; w < threads / 32; ++w) s += sums[w][threadIdx.x];
-    job.out[(int64_t)t * a.r + j0 + threadIdx.x] = s;
-    if (job.parts) put_parts(a, job.parts, t, j0 + threadIdx.x, s);
+    const int64_t t = t0 + (threadIdx.x >> 3);
+    const int j = j0 + (threadIdx.x & 7);
+    job.out[t * a.r + j] = s;
+    if (job.parts) put_parts(a, job.parts, t, j, s);
   }
   if (!quantize) return;
   const float s = row_scale(top);
   const float inv = reciprocal(s);
-  if (threadIdx.x == 0) a.rows.scale[t] = s;
-  uint2* q = reinterpret_cast<uint2*>(a.rows.codes + t * a.rows.pitch);
+  if (threadIdx.x == 0) a.rows.scale[t0] = s;
+  uint2* q = reinterpret_cast<uint2*>(a.rows.codes + t0 * a.rows.pitch);
   for (int64_t k = (int64_t)threadIdx.x * 8; k < a.rows.pitch; k += threads * 8) {
     float v[8] = {};
     uint32_t c[2];
@@ -487,12 +515,14 @@ __device__ __forceinline__ void few_token(const FewArgs& a, const FewJob& job, i
   }
 }
 
-// Latency is what bounds it: one pass over a row beside eight factor rows (or
-// columns), a block reduction, and a second pass for the codes.  The last CTAs
-// of the grid clear.
-template <typename T, bool WIDE>
+// One token a CTA: latency is what bounds it, a pass over a row beside eight
+// factor rows (or columns), a block reduction, and a second pass for the codes.
+// Four tokens a CTA (fp32 or unaligned activations by themselves): a quarter of
+// the factor's reads from L2, which are what bounds that.  The last CTAs of the
+// grid clear.
+template <typename T, bool WIDE, int TOK>
 __global__ void __launch_bounds__(512) few_kernel(const FewArgs a) {
-  __shared__ float sums[16][8];
+  __shared__ float sums[16][8 * TOK];
   __shared__ uint32_t buf[32];
   if (threadIdx.x == 0) griddep_launch_dependents();
   int cta = (int)blockIdx.x;
@@ -508,13 +538,43 @@ __global__ void __launch_bounds__(512) few_kernel(const FewArgs a) {
         put_parts(a, job.parts, e / a.r, (int)(e % a.r), __ldg(job.in + e));
       return;
     }
-    const int t = cta / a.groups, j0 = 8 * (cta % a.groups);
-    if (job.kr) few_token<T, true, WIDE>(a, job, t, j0, sums, buf);
-    else few_token<T, false, WIDE>(a, job, t, j0, sums, buf);
+    const int t0 = TOK * (cta / a.groups), j0 = 8 * (cta % a.groups);
+    if (job.kr) few_tokens<T, true, WIDE, TOK>(a, job, t0, j0, sums, buf);
+    else few_tokens<T, false, WIDE, TOK>(a, job, t0, j0, sums, buf);
     return;
   }
   const int used = a.job[0].ctas + a.job[1].ctas;
   clear_part(a.rows.clear, cta, (int64_t)gridDim.x - used);
+}
+
+// The jobs of `a` (R, r and the jobs' matrices filled in), `extra` CTAs for
+// clearing.
+template <int TOK>
+cudaError_t few_go(FewArgs& a, bool bf16, unsigned extra, cudaStream_t st) {
+  a.groups = (a.r + 7) / 8;
+  bool wide = true;
+  int64_t K = 0;
+  for (FewJob& job : a.job) {
+    if (!job.P) continue;
+    if (a.r == 1) job.kr = 0;  // the same bytes
+    job.ctas = (a.R + TOK - 1) / TOK * a.groups;
+    if (job.K > K) K = job.K;
+    if (job.K % 8 != 0 || (uintptr_t)job.P % 16 != 0 || (uintptr_t)job.L % 16 != 0 || (job.kr && a.r % 4 != 0))
+      wide = false;
+  }
+  int threads = (int)((K + 255) / 256) * 32;
+  threads = threads < 128 ? 128 : threads > 512 ? 512 : threads;
+  const unsigned ctas = (unsigned)(a.job[0].ctas + a.job[1].ctas) + extra;
+  if (ctas == 0) return cudaSuccess;
+  if (bf16) {
+    if (wide) few_kernel<__nv_bfloat16, true, TOK><<<ctas, threads, 0, st>>>(a);
+    else few_kernel<__nv_bfloat16, false, TOK><<<ctas, threads, 0, st>>>(a);
+  } else {
+    if (wide) few_kernel<float, true, TOK><<<ctas, threads, 0, st>>>(a);
+    else few_kernel<float, false, TOK><<<ctas, threads, 0, st>>>(a);
+  }
+  count_launch();
+  return cudaGetLastError();
 }
 
 struct Layout {
@@ -600,30 +660,21 @@ cudaError_t launch_int8_few(const Int8Call& c, const Int8Few& f, void* ws, Int8C
   a.rows = rows_args(c, ws, header);
   a.R = (int32_t)c.R;
   a.r = c.r;
-  a.groups = (c.r + 7) / 8;
   a.NP = f.NP;
   a.ld = f.ld;
-  if (f.T)
-    a.job[0] = {c.P, f.F, f.T, nullptr, f.T_parts, a.rows.K, c.dx ? 1 : 0, c.out ? 1 : 0, a.R * a.groups};
-  if (f.U_new) a.job[1] = {f.X, f.A, f.U_new, nullptr, f.U_parts, c.I, 0, 0, a.R * a.groups};
+  if (f.T) a.job[0] = {c.P, f.F, f.T, nullptr, f.T_parts, a.rows.K, c.dx ? 1 : 0, c.out ? 1 : 0, 0};
+  if (f.U_new) a.job[1] = {f.X, f.A, f.U_new, nullptr, f.U_parts, c.I, 0, 0, 0};
   else if (f.U_parts)
     a.job[1] = {nullptr, nullptr, nullptr, f.U, f.U_parts, 0, 0, 0, (int32_t)((c.R * c.r + 4095) / 4096)};
-  const int64_t K = f.U_new && c.I > a.rows.K ? c.I : a.rows.K;
-  bool wide = c.r % 4 == 0;
-  for (const FewJob& job : a.job)
-    if (job.P && (job.K % 8 != 0 || (uintptr_t)job.P % 16 != 0 || (uintptr_t)job.L % 16 != 0)) wide = false;
-  int threads = (int)((K + 255) / 256) * 32;
-  threads = threads < 128 ? 128 : threads > 512 ? 512 : threads;
-  const unsigned ctas = (unsigned)(a.job[0].ctas + a.job[1].ctas) + clear_ctas(a.rows.clear);
-  if (c.bf16) {
-    if (wide) few_kernel<__nv_bfloat16, true><<<ctas, threads, 0, st>>>(a);
-    else few_kernel<__nv_bfloat16, false><<<ctas, threads, 0, st>>>(a);
-  } else {
-    if (wide) few_kernel<float, true><<<ctas, threads, 0, st>>>(a);
-    else few_kernel<float, false><<<ctas, threads, 0, st>>>(a);
-  }
-  count_launch();
-  return cudaGetLastError();
+  return few_go<1>(a, c.bf16, clear_ctas(a.rows.clear), st);
+}
+
+cudaError_t launch_int8_dots(const Int8Dot* d, int count, bool bf16, int64_t R, int32_t r, cudaStream_t st) {
+  FewArgs a = {};
+  a.R = (int32_t)R;
+  a.r = r;
+  for (int i = 0; i < count; ++i) a.job[i] = {d[i].P, d[i].L, d[i].out, nullptr, nullptr, d[i].K, d[i].kr ? 1 : 0, 0, 0};
+  return few_go<4>(a, bf16, 0, st);
 }
 
 }  // namespace qlora

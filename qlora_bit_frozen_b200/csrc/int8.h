@@ -68,6 +68,16 @@ struct Int8Few {
   int64_t ld;
 };
 cudaError_t launch_int8_few(const Int8Call& c, const Int8Few& f, void* ws, Int8Clear header, cudaStream_t st);
+// Row products out[t, j] = sum_k P[t, k] L(k, j) by fp32 FMAs, for activations
+// that the tensor-core ones do not take: L [r x K], or [K x r] (kr).
+struct Int8Dot {
+  const void* P;
+  const float* L;
+  float* out;
+  int64_t K;
+  bool kr;
+};
+cudaError_t launch_int8_dots(const Int8Dot* d, int count, bool bf16, int64_t R, int32_t r, cudaStream_t st);
 // The product, over rows quantized before it, once T is computed; few:
 // nullable, dA and dB.
 cudaError_t launch_int8_product(const Int8Call& c, void* ws, uint32_t* hdr, const Int8Few* few,

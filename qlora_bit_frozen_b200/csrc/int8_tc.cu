@@ -349,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int64_t n = n0 + 64 * c64;
         const bool some = n < p.e.N;  // the same for the whole warp
         if (some) {
-          if (p.e.tma_out && lane == 0)  // the buffer's last store has been read
+          if (lane == 0)  // the buffer's last store has been read
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           __syncwarp();
         }
@@ -380,15 +380,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const float v = __fmul_rn(__fmul_rn((float)(int)acc[j], sx), wscale[col + j]);
             acc[j] = __float_as_uint(__fadd_rn(v, sum2(d)));
           }
-          if (!p.e.tma_out) {
-            if (in) {
-              OUT* o = (OUT*)p.e.out + row * p.e.N + n + 32 * c;
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (n + 32 * c + j < p.e.N) o[j] = from_f32<OUT>(__uint_as_float(acc[j]));
-            }
-            continue;
-          }
           const uint32_t line = buf + (uint32_t)lane * 128;
           if (sizeof(OUT) == 4) {  // 32 columns fill the buffer
             if (c == 1) {
@@ -410,10 +401,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
           }
           if (sizeof(OUT) == 4 || c == 1) {
+            const int64_t x = sizeof(OUT) == 4 ? n + 32 * c : n;
+            if (!p.e.tma_out) {  // rows that TMA does not take: row after row, in runs
+              __syncwarp();
+              const int64_t row0 = row - lane;
+#pragma unroll 4
+              for (int i = 0; i < 32; ++i) {
+                if (row0 + i >= p.e.R) break;
+                OUT* o = (OUT*)p.e.out + (row0 + i) * p.e.N + x;
+#pragma unroll
+                for (int e = lane; e < (int)(128 / sizeof(OUT)); e += 32) {
+                  const int byte = e * (int)sizeof(OUT);
+                  const uint32_t at = buf + (uint32_t)(i * 128 + ((((byte >> 4) ^ (i & 7)) << 4) | (byte & 15)));
+                  if (x + e < p.e.N) o[e] = *reinterpret_cast<const OUT*>(outbuf + (at - smem_u32(outbuf)));
+                }
+              }
+              __syncwarp();
+              continue;
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              const int64_t x = sizeof(OUT) == 4 ? n + 32 * c : n;
               if (in && x < p.e.N) tma_store_2d(&tm_out, buf, (int32_t)x, (int32_t)row);
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
@@ -463,7 +471,7 @@ template <int BN, int RT>
 struct StreamCfg {
   static constexpr int kTok = BN * kBK;
   static constexpr int kStage = kHalf + kTok;
-  static constexpr int kStages = BN <= 16 ? 11 : BN <= 32 ? 10 : BN <= 64 ? (RT > 16 ? 7 : 8) : RT > 16 ? 5 : 6;
+  static constexpr int kStages = BN <= 16 ? 11 : BN <= 32 ? 10 : BN <= 64 ? (RT > 32 ? 7 : 8) : RT > 16 ? 5 : 6;
   static constexpr int kCols = BN < 32 ? 32 : BN;  // TMEM columns of one accumulator
   // the tokens' rows of T, their scales, and (up to 16 tokens) rows of U
   static constexpr int kSide = BN * (RT + 1) * 4 + (BN == 16 ? BN * RT * 4 : 0);
@@ -476,6 +484,7 @@ constexpr int kStreamThreads = 64 + kStreamEpi;  // after the producer and the M
 struct StreamArgs {
   Epi e = {};
   int32_t KB, tok_tiles;
+  int32_t ctas;   // those with a run (the others have side sums only)
   int64_t tiles;  // one token tile after the other, then the next weight tile
   int32_t shared;       // deal out K steps (tiles may be shared by CTAs), else whole tiles
   int32_t* part;        // [tiles][BN][128] sums of tiles that several CTAs share (zeroed)
@@ -554,7 +563,8 @@ struct Walk {
   int32_t kb, mt, tt;
   __device__ __forceinline__ explicit Walk(const StreamArgs& p) {
     const int64_t n = p.shared ? p.tiles * p.KB : p.tiles;
-    const int64_t lo = n * blockIdx.x / gridDim.x, hi = n * (blockIdx.x + 1) / gridDim.x;
+    const int64_t c = (int)blockIdx.x < p.ctas ? (int)blockIdx.x : p.ctas;
+    const int64_t lo = n * c / p.ctas, hi = (int)blockIdx.x < p.ctas ? n * (c + 1) / p.ctas : lo;
     tile = p.shared ? lo / p.KB : lo;
     kb = p.shared ? (int32_t)(lo - tile * p.KB) : 0;
     steps = p.shared ? hi - lo : (hi - lo) * p.KB;
@@ -747,15 +757,25 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       // this tile's side inputs, while its products run
       uint64_t l[RT / 2];
       const bool in = n < p.e.N;
+      if (!DX && (p.e.r & 3) == 0 && ((uintptr_t)p.e.L & 15) == 0) {
 #pragma unroll
-      for (int j = 0; j < RT / 2; ++j) {
-        float v[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int q = 2 * j + i;
-          v[i] = in && q < p.e.r ? __ldg(p.e.L + (DX ? (int64_t)q * p.e.N + n : n * p.e.r + q)) : 0.0f;
+        for (int j = 0; j < RT / 4; ++j) {
+          const float4 v = in && 4 * j < p.e.r ? __ldg(reinterpret_cast<const float4*>(p.e.L + n * p.e.r) + j)
+                                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          l[2 * j] = pack2(v.x, v.y);
+          l[2 * j + 1] = pack2(v.z, v.w);
         }
-        l[j] = pack2(v[0], v[1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < RT / 2; ++j) {
+          float v[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int q = 2 * j + i;
+            v[i] = in && q < p.e.r ? __ldg(p.e.L + (DX ? (int64_t)q * p.e.N + n : n * p.e.r + q)) : 0.0f;
+          }
+          l[j] = pack2(v[0], v[1]);
+        }
       }
       const float sw = !DX && in ? __ldg(p.e.ws + n) : 1.0f;
       if (tt != staged) {
@@ -863,16 +883,19 @@ struct Plan {
 // kernel pays whole rounds of tiles over the CTA pairs and the last tile's
 // epilogue; the stream kernel pays whole rounds of tiles over the SMs, or, with
 // tiles shared, an equal run of steps and the meeting of the partial sums, which
-// grows with the token tile.
+// grows with the token tile.  A tile takes no less than its epilogue: about nine
+// steps for either kernel's (the pair kernel's outputs are twice as many).
 Plan plan_for(int64_t R, int64_t N, int64_t K) {
   const int64_t sms = sm_count(), KB = up(K, kBK);
   Plan p;
   p.bn = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128;
   const int64_t pair_tiles = up(R, 256) * up(N, 256), tiles = up(R, p.bn) * up(N, 128);
   const int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
-  const int64_t cost_pair = up(pair_tiles, pairs) * KB + 10;
-  const int64_t cost_whole = up(tiles, sms) * KB + 5;
-  const int64_t cost_shared = up(tiles * KB, sms) + 4 + p.bn / 8;
+  const int64_t cost_pair = up(pair_tiles, pairs) * (KB > 9 ? KB : 9) + 10;
+  const int64_t least = p.bn / 14;  // epilogue of a stream tile, in steps
+  const int64_t cost_whole = up(tiles, sms) * (KB > least ? KB : least) + 5;
+  const int64_t run = up(tiles * KB, sms), ends = up(tiles, sms) * 2 * least;
+  const int64_t cost_shared = (run > ends ? run : ends) + 4 + p.bn / 8;
   p.shared = cost_shared < cost_whole;
   p.pair = R > 128 && cost_pair < (p.shared ? cost_shared : cost_whole);
   if (p.pair) {
@@ -963,7 +986,6 @@ cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& b
     a.tiles_n = (int32_t)up(e.N, 256);
     return go_pair<DX, OUT, RT>(pl, mx, mw, mo, a, st);
   }
-  constexpr int SRT = RT <= 16 ? RT : 64;
   StreamArgs a = {};
   a.e = e;
   a.KB = (int32_t)up(K, kBK);
@@ -971,10 +993,11 @@ cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& b
   a.tiles = pl.tiles;
   a.shared = pl.shared ? 1 : 0;
   Plan run = pl;
-  if (!c.out) {  // only the side sums
-    a.tiles = 0;
-    const int64_t want = up(c.I + c.O, kStreamEpi);
-    run.ctas = (int)(want < sm_count() ? want : sm_count());
+  a.ctas = pl.ctas;
+  if (!c.out) a.tiles = 0;  // only the side sums
+  if (DX && few && (few->dA || few->dB)) {
+    const int64_t want = up(c.I + c.O, kStreamEpi), most = want < sm_count() ? want : sm_count();
+    if (run.ctas < most) run.ctas = (int)most;
   }
   a.part = (int32_t*)ws;
   a.tickets = (uint32_t*)((char*)ws + stream_part_bytes(pl));
@@ -988,10 +1011,10 @@ cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& b
     a.O = c.O;
   }
   switch (pl.bn) {
-    case 16: return go_stream<DX, 16, SRT>(run, mx, mw, a, st);
-    case 32: return go_stream<DX, 32, SRT>(run, mx, mw, a, st);
-    case 64: return go_stream<DX, 64, SRT>(run, mx, mw, a, st);
-    default: return go_stream<DX, 128, SRT>(run, mx, mw, a, st);
+    case 16: return go_stream<DX, 16, RT>(run, mx, mw, a, st);
+    case 32: return go_stream<DX, 32, RT>(run, mx, mw, a, st);
+    case 64: return go_stream<DX, 64, RT>(run, mx, mw, a, st);
+    default: return go_stream<DX, 128, RT>(run, mx, mw, a, st);
   }
 }
 
