@@ -702,7 +702,7 @@ size_t qlora_linear_workspace_bytes(const qlora_weight* w, int64_t R, int32_t r,
   if (!w || R < 0 || r < 1 || r > 64) return 0;
   if (compute != QLORA_COMPUTE_FP32 && compute != QLORA_COMPUTE_BF16) return 0;
   if (w->fmt == QLORA_FMT_INT8) {
-    if (w->O < 1 || w->I < 1 || w->O > kInt8MaxK || w->I > kInt8MaxK) return 0;
+    if (w->O < 1 || w->I < 1 || w->O > kInt8MaxK || w->I > kInt8MaxK || R > kInt8MaxTokens) return 0;
     if (op != QLORA_OP_FWD && op != QLORA_OP_BWD) return 0;
     return int8_layout(w, R, r, op == QLORA_OP_BWD, compute).total;
   }
@@ -733,7 +733,7 @@ qlora_status qlora_linear_fwd(const qlora_weight* w, const void* X, int64_t R, c
   const size_t esz = compute == QLORA_COMPUTE_BF16 ? 2 : 4;
   if (!aligned(X, esz) || !aligned(Y, esz) || !al4(U_out)) return QLORA_ERR_ALIGNMENT;
   const bool int8 = w->fmt == QLORA_FMT_INT8;
-  if (int8 && R > INT32_MAX) return QLORA_ERR_SHAPE;
+  if (int8 && R > kInt8MaxTokens) return QLORA_ERR_SHAPE;
   const FwdLayout L = int8 ? FwdLayout() : fwd_layout(w, R, r, compute);
   if (ws_bytes < (int8 ? int8_layout(w, R, r, false, compute).total : L.total)) return QLORA_ERR_WORKSPACE;
   st = device_ready();
@@ -788,7 +788,7 @@ qlora_status qlora_linear_bwd(const qlora_weight* w, const void* X, const void* 
       !al4(dB))
     return QLORA_ERR_ALIGNMENT;
   const bool int8 = w->fmt == QLORA_FMT_INT8;
-  if (int8 && R > INT32_MAX) return QLORA_ERR_SHAPE;
+  if (int8 && R > kInt8MaxTokens) return QLORA_ERR_SHAPE;
   const BwdLayout L = int8 ? BwdLayout() : bwd_layout(w, R, r, compute);
   if (ws_bytes < (int8 ? int8_layout(w, R, r, true, compute).total : L.total)) return QLORA_ERR_WORKSPACE;
   st = device_ready();

@@ -602,7 +602,7 @@ RowsArgs rows_args(const Int8Call& c, void* ws, Int8Clear header) {
   a.clear.p[0] = (uint4*)header.p;
   a.clear.n[0] = (int64_t)(header.bytes / 16);
   a.clear.p[1] = (uint4*)((char*)ws + l.total);  // the product's sums and tickets
-  a.clear.n[1] = (int64_t)(int8_tc_zeroed(c.dx, c.R, c.O, c.I) / 16);
+  a.clear.n[1] = (int64_t)(int8_tc_zeroed(c.dx, c.R, c.O, c.I, c.r) / 16);
   return a;
 }
 

@@ -12,6 +12,9 @@ namespace qlora {
 // Longest reduction whose 32-bit sum cannot overflow: 127^2 * 2^17 < 2^31.
 constexpr int64_t kInt8MaxK = 131072;
 
+// Most tokens of a call: counts of CTAs and token coordinates stay in 32 bits.
+constexpr int64_t kInt8MaxTokens = 1 << 28;
+
 constexpr int64_t int8_pitch(int64_t n) { return (n + 15) / 16 * 16; }
 
 // codes [O x pitch], scale [O] of W [O x I]; *bad (device or mapped host
@@ -87,7 +90,7 @@ cudaError_t launch_int8_product(const Int8Call& c, void* ws, uint32_t* hdr, cons
 // xs; ws: int8_tc_ws bytes, of which the first int8_tc_zeroed are zero; few:
 // the backward's side sums, nullable.
 size_t int8_tc_ws(bool dx, int64_t R, int64_t O, int64_t I, int32_t r);
-size_t int8_tc_zeroed(bool dx, int64_t R, int64_t O, int64_t I);
+size_t int8_tc_zeroed(bool dx, int64_t R, int64_t O, int64_t I, int32_t r);
 cudaError_t launch_int8_tc(const Int8Call& c, const int8_t* xq, const float* xs, const Int8Few* few, void* ws,
                            uint32_t* hdr, cudaStream_t st);
 

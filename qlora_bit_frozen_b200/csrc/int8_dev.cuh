@@ -80,7 +80,6 @@ __device__ __forceinline__ float sum2(uint64_t a) {
 
 // ------------------------------------------------------------------- host
 
-
 constexpr int kMaxDevices = 64;
 
 inline int sm_count() {
@@ -105,6 +104,26 @@ inline cudaError_t allow_smem(K kern, int bytes, std::atomic<bool>* done) {
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess && dev < kMaxDevices) done[dev].store(true, std::memory_order_relaxed);
   return e;
+}
+
+// Launches a kernel that may start before the grid before it has ended; each of
+// its CTAs calls griddep_wait() before it reads what that grid writes and before
+// it ends.
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kern)(P...), int ctas, int threads, int smem, cudaStream_t st,
+                                const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 using EncodeTiled = PFN_cuTensorMapEncodeTiled_v12000;

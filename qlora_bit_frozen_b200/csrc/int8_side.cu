@@ -114,18 +114,21 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int N, bool a_mn) {
          ((uint32_t)(128 >> 4) << 24);
 }
 
-template <int NP>
-__device__ __forceinline__ void side_write(const SideOut& o, int r, int64_t m, const float (&acc)[NP]) {
+// Columns j0 .. j0 + J of row m of a product's result.
+template <int NP, int J>
+__device__ __forceinline__ void side_write(const SideOut& o, int r, int64_t m, int j0, const float (&acc)[J]) {
   if (m >= o.M) {
     // the parts' rows end with zeros: they meet zero rows of the large matrix
     if (o.parts && m < o.ld)
-      for (int q = 0; q < 3 * r; ++q) o.parts[((int64_t)(q / r) * NP + q % r) * o.ld + m] = 0;
+      for (int j = j0; j < min(r, j0 + J); ++j)
+        for (int q = 0; q < 3; ++q) o.parts[((int64_t)q * NP + j) * o.ld + m] = 0;
     return;
   }
 #pragma unroll
-  for (int j = 0; j < NP; ++j) {
+  for (int i = 0; i < J; ++i) {
+    const int j = j0 + i;
     if (j < r) {
-      const float v = o.s * acc[j];
+      const float v = o.s * acc[i];
       o.out[o.transposed ? (int64_t)j * o.M + m : m * r + j] = v;
       if (o.parts) {
         float rest = v;
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(kSideThreads, 1)
       // the segment of this CTA in the tile is done
       const int64_t m = tile * 128 + 32 * quad + lane;
       if (run == o.chunks) {
-        side_write<NP>(o, p.r, m, acc);
+        side_write<NP, NP>(o, p.r, m, 0, acc);
       } else {
         float* mine = p.part + (((int64_t)blockIdx.x * 2 + job) * 2 + (segment ? 1 : 0)) * NP * 128 + 32 * quad + lane;
 #pragma unroll
@@ -315,12 +318,17 @@ __global__ void __launch_bounds__(kSideThreads, 1)
 }
 
 // The tiles that several CTAs shared: their partial sums in CTA order.  One CTA
-// a tile, a thread an output row, a few CTAs' sums on their way at once.
+// for eight columns of a tile, a thread an output row, four CTAs' sums on their
+// way at once.  (All columns by one CTA: 22 us after the products of 8192 tokens
+// at rank 64, where this takes 8.)
 template <int NP>
 __global__ void __launch_bounds__(128) side_sum_kernel(const SideArgs p) {
-  const int job = (int64_t)blockIdx.x >= p.tiles[0] ? 1 : 0;
+  constexpr int kGroups = NP / 8;
+  const int64_t at = blockIdx.x / kGroups;
+  const int j0 = 8 * (int)(blockIdx.x % kGroups);
+  const int job = at >= p.tiles[0] ? 1 : 0;
   const SideOut& o = p.job[job];
-  const int64_t tile = (int64_t)blockIdx.x - (job ? p.tiles[0] : 0), u0 = tile * o.chunks, u1 = u0 + o.chunks;
+  const int64_t tile = at - (job ? p.tiles[0] : 0), u0 = tile * o.chunks, u1 = u0 + o.chunks;
   int64_t lo;
   int64_t c = side_owner(p, job, u0, lo);
   griddep_wait();  // every CTA: this grid ends only after the one before it
@@ -345,12 +353,10 @@ __global__ void __launch_bounds__(128) side_sum_kernel(const SideArgs p) {
     }
     return false;
   };
-  float acc[NP];
-#pragma unroll
-  for (int j = 0; j < NP; ++j) acc[j] = 0.0f;
-  constexpr int kAhead = NP <= 16 ? 4 : NP <= 32 ? 2 : 1;
+  float acc[8] = {};
+  constexpr int kAhead = 4;
   for (bool more = true; more;) {
-    float v[kAhead][NP];
+    float v[kAhead][8];
     bool have[kAhead];
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) {
@@ -358,16 +364,16 @@ __global__ void __launch_bounds__(128) side_sum_kernel(const SideArgs p) {
       have[q] = more && next(from);
       more = have[q];
 #pragma unroll
-      for (int j = 0; j < NP; ++j) v[q][j] = have[q] ? __ldcg(p.part + from + j * 128) : 0.0f;
+      for (int j = 0; j < 8; ++j) v[q][j] = have[q] ? __ldcg(p.part + from + (j0 + j) * 128) : 0.0f;
     }
 #pragma unroll
     for (int q = 0; q < kAhead; ++q)
       if (have[q]) {
 #pragma unroll
-        for (int j = 0; j < NP; ++j) acc[j] += v[q][j];
+        for (int j = 0; j < 8; ++j) acc[j] += v[q][j];
       }
   }
-  side_write<NP>(o, p.r, tile * 128 + threadIdx.x, acc);
+  side_write<NP, 8>(o, p.r, tile * 128 + threadIdx.x, j0, acc);
 }
 
 // The three bf16 parts of up to two fp32 factors, [3][NP][ld], zeros past n
@@ -382,29 +388,38 @@ struct SplitArgs {
   SplitJob job[2];
   int32_t r, NP;
 };
-// A block takes 64 entries of every factor row; a factor given as [n x r] is
+// A block takes 64 entries of 16 factor rows; a factor given as [n x r] is
 // turned in shared memory, so that both sides are read and written in runs.
+// (All rows of 64 entries in one block: 12 us at rank 64 over 4096 entries, where
+// this takes 4.6.)
+constexpr int kSplitRows = 16;
 __global__ void __launch_bounds__(256) split_kernel(const SplitArgs a) {
-  __shared__ float tile[64][65];
+  __shared__ float tile[kSplitRows][65];
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int second = (int)blockIdx.x >= a.job[0].blocks ? 1 : 0;
-  const SplitJob& b = a.job[second];
-  const int64_t k0 = ((int64_t)blockIdx.x - (second ? a.job[0].blocks : 0)) * 64;
-  if (b.kr) {
-    for (int e = threadIdx.x; e < 64 * a.r; e += 256) {
-      const int k = e / a.r, j = e - k * a.r;
-      tile[j][k] = k0 + k < b.n ? __ldg(b.src + k0 * a.r + e) : 0.0f;
-    }
-    __syncthreads();
+  const SplitJob b = second ? a.job[1] : a.job[0];
+  const int groups = (a.r + kSplitRows - 1) / kSplitRows;
+  const int block = (int)blockIdx.x - (second ? a.job[0].blocks : 0);
+  const int64_t k0 = (int64_t)(block / groups) * 64;
+  const int j0 = block % groups * kSplitRows, rows = min(kSplitRows, a.r - j0);
+#pragma unroll
+  for (int e = threadIdx.x; e < 64 * kSplitRows; e += 256) {
+    const int j = b.kr ? e % kSplitRows : e >> 6, k = b.kr ? e / kSplitRows : e & 63;
+    float v = 0.0f;
+    if (j < rows && k0 + k < b.n)
+      v = __ldg(b.src + (b.kr ? (k0 + k) * a.r + j0 + j : (int64_t)(j0 + j) * b.n + k0 + k));
+    tile[j][k] = v;
   }
-  for (int e = threadIdx.x; e < 64 * a.r; e += 256) {
+  __syncthreads();
+#pragma unroll
+  for (int e = threadIdx.x; e < 64 * kSplitRows; e += 256) {
     const int j = e >> 6, k = e & 63;
-    if (k0 + k >= b.ld) continue;
-    float v = b.kr ? tile[j][k] : k0 + k < b.n ? __ldg(b.src + (int64_t)j * b.n + k0 + k) : 0.0f;
+    if (j >= rows || k0 + k >= b.ld) continue;
+    float v = tile[j][k];
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
       const __nv_bfloat16 h = __float2bfloat16_rn(v);
-      b.dst[((int64_t)q * a.NP + j) * b.ld + k0 + k] = __bfloat16_as_ushort(h);
+      b.dst[((int64_t)q * a.NP + j0 + j) * b.ld + k0 + k] = __bfloat16_as_ushort(h);
       v -= __bfloat162float(h);
     }
   }
@@ -421,18 +436,9 @@ cudaError_t side_go(const CUtensorMap* t, const SideArgs& a, cudaStream_t st) {
   count_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.tiles[0] + a.tiles[1]));
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, side_sum_kernel<NP>, a);
+  e = launch_after(side_sum_kernel<NP>, (int)(a.tiles[0] + a.tiles[1]) * (NP / 8), 128, 0, st, a);
   count_launch();
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return e;
 }
 
 template <bool A_MN>
@@ -469,7 +475,7 @@ cudaError_t launch_side_split(const SideFactor* f, int count, int32_t r, cudaStr
     b.n = f[i].n;
     b.ld = side_ld(f[i].n);
     b.kr = f[i].kr ? 1 : 0;
-    b.blocks = (int)up(b.ld, 64);
+    b.blocks = (int)(up(b.ld, 64) * up(r, kSplitRows));
     blocks += b.blocks;
   }
   if (blocks == 0) return cudaSuccess;

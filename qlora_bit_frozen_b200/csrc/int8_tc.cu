@@ -14,7 +14,10 @@
 //               for the same work; at the integer rate the latter asks L2 for
 //               more bytes a cycle than an SM can take).  Persistent, two
 //               accumulators in TMEM: the epilogue of one tile runs under the
-//               next one's products.
+//               next one's products.  16384 tokens, 17408 x 5120, rank 16: 916 us,
+//               3.2 POP/s; the tensor pipes are busy for nearly all of a CTA's
+//               time and the clock is what the power limit leaves (1.4 to 1.6 of
+//               1.965 GHz).
 // stream_kernel few tokens or few tiles: the weight tile is the MMA's M side
 //               (128 outputs x 16..128 tokens), so few tokens cost no wasted
 //               rows and the kernel runs at the weight's bandwidth; the K
@@ -22,9 +25,16 @@
 //               what several CTAs add to one tile meets in 32-bit integer
 //               atomics, exact in any order.
 //
-// The adapter term s T L^T is added in the epilogue with fp32 FMAs: at rank r
-// that is r FMAs an output against K integer products, it costs no second
-// accumulator, and it keeps the adapter at fp32 accuracy.
+// The adapter term s T L^T keeps fp32 accuracy in both.  The stream kernel adds
+// it in its epilogue by fp32 FMAs: r an output against K integer products.  In
+// the pair kernel that epilogue, whose factor comes out of shared memory at 16
+// bytes for two FMAs, outlasted the products from rank 16 on (8192 tokens of 4096 x
+// 4096: 86, 114, 186 and 341 us at ranks 8, 16, 32 and 64), so T and L are split
+// into three bf16 parts and the term is one to six more K steps on the tensor
+// cores (88, 90, 93 and 99 us).  It has no TMEM of its own: the epilogue warps
+// take a tile's integer sums into registers, the adapter's product then fills the
+// same columns from zero while the next tile's integer products run into the other
+// half, and the warps add the two.
 //
 // Every wait is bounded; on expiry the kernel records QLORA_ERR_TIMEOUT,
 // stops issuing, and still reaches its barriers and frees its TMEM.
@@ -46,8 +56,7 @@ struct Epi {
   const float* xs;   // [R] row scale
   const float* ws;   // [N] channel scale (forward), else null
   const float* T;    // [R x r] U or V
-  const float* L;    // packed [Npad x RT] s L (pair) or the factor itself (stream)
-  const float* wpad; // pair: channel scales [Npad] (1 in the input gradient)
+  const float* L;    // B [N x r] or A [r x N]
   int32_t r;
   float s;
   void* out;
@@ -61,6 +70,19 @@ struct Epi {
 __host__ __device__ constexpr uint32_t idesc_i8(int M, int N, bool a_mn, bool b_mn) {
   return (2u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// kind::f16: bf16 x bf16 -> fp32, both K-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void umma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 template <int CTAS>
@@ -141,15 +163,26 @@ constexpr int kPairStages = 5;
 constexpr int kStage = 2 * kHalf;  // A and B half tiles of one CTA
 constexpr int kEpiWarps = 8;       // two to a TMEM lane quarter, 64 columns in turn
 constexpr int kOutBuf = 4096;      // staged output of a warp: 32 rows x 128 bytes
-constexpr int kFactor = 32768;     // staged adapter factor: 256 outputs (128 above rank 32)
-constexpr int kPairSmem = 1024 + kPairStages * kStage + kEpiWarps * kOutBuf + kFactor + 1024 + 256;
+constexpr int kPairSmem = 1024 + kPairStages * kStage + kEpiWarps * kOutBuf + 2 * 1024 + 256;
 static_assert(kPairSmem <= 227 * 1024, "one CTA per SM");
 constexpr int kPairThreads = 128 + 32 * kEpiWarps;
+// The epilogue warps hold 128 sums each and take registers from the other four:
+// 128 kPairRegs + 256 kEpiRegs is no more than the 384 x 168 of the launch.
+constexpr int kPairRegs = 72, kEpiRegs = 216;
+static_assert(128 * kPairRegs + 32 * kEpiWarps * kEpiRegs <= kPairThreads * 168, "registers of the launch");
 
 struct PairArgs {
   Epi e = {};
   int32_t KB, tiles_m, tiles_n;
+  int32_t KA;   // K steps of the adapter's product
+  int32_t at;   // the step of a tile before which the last tile's adapter product is issued
 };
+
+// Parts of T and of L that meet in the adapter's product, one pair of them after
+// another along its K (see pack_kernel): the small ones first, so that the tensor
+// core's own rounding, which goes with the sum so far, is small until the last.
+__host__ __device__ constexpr int part_T(int c) { return c == 0 ? 2 : c == 1 || c == 3 ? 1 : 0; }
+__host__ __device__ constexpr int part_L(int c) { return c == 2 ? 2 : c == 1 || c == 4 ? 1 : 0; }
 
 // Tile t of the persistent order: groups of kGroup token tiles, every output
 // tile of a group before the next, so that what runs at once shares its
@@ -163,23 +196,24 @@ __device__ __forceinline__ void pair_tile(int64_t t, int tiles_m, int tiles_n, i
   n = in / size;
 }
 
-template <bool DX, typename OUT, int RT>
+template <bool DX, typename OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_l,
                 const __grid_constant__ CUtensorMap tm_out, const PairArgs p) {
-  constexpr uint32_t kIdesc = idesc_i8(256, 256, false, DX);
+  constexpr uint32_t kIdesc = idesc_i8(256, 256, false, DX), kAdapter = idesc_bf16(256, 256);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* outbuf = smem + kPairStages * kStage;
-  float* factor = (float*)(outbuf + kEpiWarps * kOutBuf);
-  float* wscale = factor + kFactor / 4;
-  uint64_t* bars = (uint64_t*)(wscale + 256);
+  float* wscale = (float*)(outbuf + kEpiWarps * kOutBuf);  // [2][256]
+  uint64_t* bars = (uint64_t*)(wscale + 512);
   uint64_t* full = bars;                      // leader: both CTAs' loads landed
   uint64_t* empty = bars + kPairStages;       // both: the step's products are done
-  uint64_t* acc_full = bars + 2 * kPairStages;
-  uint64_t* acc_empty = acc_full + 2;         // leader: drained by the epilogue warps of both
-  uint64_t* fac_full = acc_empty + 2;         // the factor (and the scales) of a tile landed
-  volatile uint32_t* tmem_slot = (volatile uint32_t*)(fac_full + 1);
+  uint64_t* int_full = bars + 2 * kPairStages;  // both: the integer sums of a tile
+  uint64_t* int_read = int_full + 2;          // leader: in the registers of both CTAs' epilogue warps
+  uint64_t* acc_full = int_read + 2;          // both: the adapter's sums, in the same place
+  uint64_t* acc_read = acc_full + 2;          // leader: read by the epilogue warps of both
+  volatile uint32_t* tmem_slot = (volatile uint32_t*)(acc_read + 2);
   volatile uint32_t* abort_flag = tmem_slot + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -193,14 +227,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(smem_u32(&empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&int_full[b]), 1);
+      mbar_init(smem_u32(&int_read[b]), 2 * kEpiWarps);
       mbar_init(smem_u32(&acc_full[b]), 1);
-      mbar_init(smem_u32(&acc_empty[b]), 2 * kEpiWarps);
+      mbar_init(smem_u32(&acc_read[b]), 2 * kEpiWarps);
     }
-    mbar_init(smem_u32(fac_full), 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&tm_x);
     prefetch_tensormap(&tm_w);
+    prefetch_tensormap(&tm_t);
+    prefetch_tensormap(&tm_l);
     prefetch_tensormap(&tm_out);
   }
   if (warp == 1) {
@@ -215,34 +252,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  griddep_wait();
 
-  if (warp == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegs));
+    if (warp == 0) {
     // ---------------------------------------------------------- producer
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
+    // One step: a box of each operand, into this CTA's half of the stage.
+    auto step = [&](const CUtensorMap* ma, int xa, int ya, const CUtensorMap* mb, int xb, int yb) {
+      if (!ok) return;
+      if (!warp_wait(smem_u32(&empty[s]), ph ^ 1u, p.e.wait_ns, p.e.err, 0x501)) {
+        *abort_flag = 1;
+        ok = false;
+        return;
+      }
+      if (elect_one()) {
+        const uint32_t fb = smem_u32(&full[s]), dst = smem_u32(smem + s * kStage);
+        if (rank == 0) mbar_arrive_expect_tx(fb, 2 * kStage);
+        const uint32_t lead = at_rank(fb, 0);
+        tma_load_pair(dst, ma, lead, xa, ya);
+        tma_load_pair(dst + kHalf, mb, lead, xb, yb);
+      }
+      __syncwarp();
+      if (++s == kPairStages) { s = 0; ph ^= 1u; }
+    };
+    int m0 = 0, n0 = 0;
+    bool last = false;  // a tile before this one, at m0, n0
     for (int64_t t = cluster; t < tiles && ok; t += clusters) {
       int tm, tn;
       pair_tile(t, p.tiles_m, p.tiles_n, tm, tn);
-      const int m0 = tm * 256 + 128 * (int)rank, n0 = tn * 256 + 128 * (int)rank;
-      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-      for (int kb = 0; kb < p.KB; ++kb) {
-        if (!warp_wait(smem_u32(&empty[s]), ph ^ 1u, p.e.wait_ns, p.e.err, 0x501)) {
-          *abort_flag = 1;
-          ok = false;
-          break;
-        }
-        if (elect_one()) {
-          const uint32_t fb = smem_u32(&full[s]), dst = smem_u32(smem + s * kStage);
-          if (rank == 0) mbar_arrive_expect_tx(fb, 2 * kStage);
-          const uint32_t lead = at_rank(fb, 0);
-          tma_load_pair(dst, &tm_x, lead, kb * kBK, m0);
-          tma_load_pair(dst + kHalf, &tm_w, lead, DX ? n0 : kb * kBK, DX ? kb * kBK : n0);
-        }
-        __syncwarp();
-        if (++s == kPairStages) { s = 0; ph ^= 1u; }
+      const int m1 = tm * 256 + 128 * (int)rank, n1 = tn * 256 + 128 * (int)rank;
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) {
+        ok = false;
+        break;
       }
+      for (int kb = 0; kb < p.KB; ++kb) {
+        if (last && kb == p.at)
+          for (int k = 0; k < p.KA; ++k) step(&tm_t, 64 * k, m0, &tm_l, 64 * k, n0);
+        step(&tm_x, kb * kBK, m1, &tm_w, DX ? n1 : kb * kBK, DX ? kb * kBK : n1);
+      }
+      m0 = m1;
+      n0 = n1;
+      last = true;
     }
+    if (last)
+      for (int k = 0; k < p.KA; ++k) step(&tm_t, 64 * k, m0, &tm_l, 64 * k, n0);
     // every copy has landed and every commit to this CTA's barriers has
     // arrived before the pair may exit
     for (int i = 0; i < kPairStages; ++i) {
@@ -252,23 +309,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     // -------------------------------------------------------- MMA issuer
     if (rank == 0) {
-      int s = 0, b = 0;
-      uint32_t ph = 0, pa = 0;
+      int s = 0;
+      uint32_t ph = 0;
       bool ok = true;
-      for (int64_t t = cluster; t < tiles && ok; t += clusters) {
-        if (!warp_wait(smem_u32(&acc_empty[b]), pa ^ 1u, p.e.wait_ns, p.e.err, 0x503)) {
+      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t where) {
+        if (ok && !warp_wait(smem_u32(bar), parity, p.e.wait_ns, p.e.err, where)) {
           *abort_flag = 1;
-          break;
+          ok = false;
         }
         tc_fence_after();
+        return ok;
+      };
+      // Tile i's adapter product, into the columns that its integer sums left.
+      auto adapter = [&](int64_t i) {
+        const int b = (int)(i & 1);
+        if (!wait(&int_read[b], (uint32_t)(i >> 1) & 1u, 0x503)) return;
+        const uint32_t d = tmem + 256u * (uint32_t)b;
+        for (int k = 0; k < p.KA; ++k) {
+          if (!wait(&full[s], ph, 0x504)) return;
+          if (elect_one()) {
+            const uint32_t base = smem_u32(smem + s * kStage);
+            const uint64_t ad = sdesc(base, 16, 1024), bd = sdesc(base + kHalf, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, kAdapter, (k | kk) ? 1u : 0u);
+            umma_commit_pair(smem_u32(&empty[s]));
+            if (k + 1 == p.KA) umma_commit_pair(smem_u32(&acc_full[b]));
+          }
+          __syncwarp();
+          if (++s == kPairStages) { s = 0; ph ^= 1u; }
+        }
+      };
+      int64_t i = 0;
+      for (int64_t t = cluster; t < tiles && ok; t += clusters, ++i) {
+        const int b = (int)(i & 1);
+        if (!wait(&acc_read[b], ((uint32_t)(i >> 1) & 1u) ^ 1u, 0x505)) break;
         const uint32_t d = tmem + 256u * (uint32_t)b;
         for (int kb = 0; kb < p.KB; ++kb) {
-          if (!warp_wait(smem_u32(&full[s]), ph, p.e.wait_ns, p.e.err, 0x504)) {
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+          if (i > 0 && kb == p.at) adapter(i - 1);
+          if (!wait(&full[s], ph, 0x506)) break;
           if (elect_one()) {
             const uint32_t base = smem_u32(smem + s * kStage);
             const uint64_t ad = sdesc(base, 16, 1024);
@@ -277,163 +356,127 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             for (int kk = 0; kk < kBK / 32; ++kk)
               umma_i8<2>(d, ad + 2 * kk, bd + (DX ? 256 : 2) * kk, kIdesc, (kb | kk) ? 1u : 0u);
             umma_commit_pair(smem_u32(&empty[s]));
-            if (kb + 1 == p.KB) umma_commit_pair(smem_u32(&acc_full[b]));
+            if (kb + 1 == p.KB) umma_commit_pair(smem_u32(&int_full[b]));
           }
           __syncwarp();
           if (++s == kPairStages) { s = 0; ph ^= 1u; }
         }
-        if (++b == 2) { b = 0; pa ^= 1u; }
       }
+      if (i > 0 && ok) adapter(i - 1);
     }
-  } else if (warp >= 4) {
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     // ---------------------------------------------------------- epilogue
-    // Lane = token.  Warp `half` of a quarter takes 64-column runs half, half
-    // + 2.  The adapter factor and the channel scales of a tile sit in shared
-    // memory (a bulk copy issued as soon as the tile before has done with
-    // them), read as broadcasts.
+    // Lane = token.  A warp takes 128 columns of its lane quarter: their integer
+    // sums into registers, which frees the TMEM columns for the adapter's sums.
     const int ew = warp - 4, quad = warp & 3, half = ew >> 2;
-    const uint32_t buf = smem_u32(outbuf + ew * kOutBuf);
-    constexpr int kLoads = RT > 32 ? 2 : 1;           // copies a tile's factor takes
-    constexpr uint32_t kFacBytes = 256 / kLoads * RT * 4;
-    auto fetch = [&](int64_t t, int part) {           // one thread
-      int tm, tn;
-      pair_tile(t, p.tiles_m, p.tiles_n, tm, tn);
-      const uint32_t fb = smem_u32(fac_full);
-      mbar_arrive_expect_tx(fb, kFacBytes + (part == 0 ? 1024u : 0u));
-      bulk_load(smem_u32(factor), p.e.L + ((int64_t)tn * 256 + part * (256 / kLoads)) * RT, kFacBytes, fb);
-      if (part == 0) bulk_load(smem_u32(wscale), p.e.wpad + (int64_t)tn * 256, 1024u, fb);
-    };
-    if (ew == 0 && lane == 0 && cluster < tiles) fetch(cluster, 0);
+    uint8_t* mine = outbuf + ew * kOutBuf;
+    const uint32_t buf = smem_u32(mine);
     int b = 0;
-    uint32_t pa = 0, pf = 0;
+    uint32_t pa = 0;
     bool ok = true;
     for (int64_t t = cluster; t < tiles; t += clusters) {
       int tm, tn;
       pair_tile(t, p.tiles_m, p.tiles_n, tm, tn);
-      const int64_t row = (int64_t)tm * 256 + 128 * (int)rank + 32 * quad + lane;
+      const int64_t row0 = (int64_t)tm * 256 + 128 * (int)rank + 32 * quad, row = row0 + lane;
       const int64_t n0 = (int64_t)tn * 256;
-      const bool in = row < p.e.R;
-      const float sx = in ? __ldg(p.e.xs + row) : 0.0f;
-      uint64_t u[RT / 2];
-      const float* T = p.e.T + row * p.e.r;
-      if (in && (p.e.r & 3) == 0 && ((uintptr_t)p.e.T & 15) == 0) {
-#pragma unroll
-        for (int j = 0; j < RT / 4; ++j) {
-          const float4 v = 4 * j < p.e.r ? __ldg(reinterpret_cast<const float4*>(T) + j)
-                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          u[2 * j] = pack2(v.x, v.y);
-          u[2 * j + 1] = pack2(v.z, v.w);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < RT / 2; ++j)
-          u[j] = pack2(in && 2 * j < p.e.r ? __ldg(T + 2 * j) : 0.0f,
-                       in && 2 * j + 1 < p.e.r ? __ldg(T + 2 * j + 1) : 0.0f);
+      const float sx = row < p.e.R ? __ldcg(p.e.xs + row) : 0.0f;
+      if (!DX) {
+        const int64_t n = n0 + threadIdx.x - 128;
+        wscale[256 * b + threadIdx.x - 128] = n < p.e.N ? __ldg(p.e.ws + n) : 0.0f;
       }
-      // one answer for all warps, which meet at barriers below
-      ok = mbar_wait(smem_u32(fac_full), pf, p.e.wait_ns, p.e.err, 0x505) && ok;
-      ok = mbar_wait(smem_u32(&acc_full[b]), pa, p.e.wait_ns, p.e.err, 0x506) && ok;
-      pf ^= 1u;
+      // one answer for all warps, which also have the scales then
+      ok = mbar_wait(smem_u32(&int_full[b]), pa, p.e.wait_ns, p.e.err, 0x507) && ok;
       if (!all_of<32 * kEpiWarps>(ok)) {
         *abort_flag = 1;
         break;
       }
       tc_fence_after();
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        if (h == 1 && kLoads == 2) {
-          ok = mbar_wait(smem_u32(fac_full), pf, p.e.wait_ns, p.e.err, 0x507);
-          pf ^= 1u;
+      const uint32_t cols = tmem + ((uint32_t)(quad * 32) << 16) + 256u * (uint32_t)b + 128u * (uint32_t)half;
+      uint32_t v[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(cols + 32u * (uint32_t)c, v[c]);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_remote(at_rank(smem_u32(&int_read[b]), 0));
+      const float4* sw = reinterpret_cast<const float4*>(wscale + 256 * b + 128 * half);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          float4 w = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+          if (!DX) w = sw[(32 * c + j) / 4];
+          v[c][j] = __float_as_uint(__fmul_rn(__fmul_rn((float)(int)v[c][j], sx), w.x));
+          v[c][j + 1] = __float_as_uint(__fmul_rn(__fmul_rn((float)(int)v[c][j + 1], sx), w.y));
+          v[c][j + 2] = __float_as_uint(__fmul_rn(__fmul_rn((float)(int)v[c][j + 2], sx), w.z));
+          v[c][j + 3] = __float_as_uint(__fmul_rn(__fmul_rn((float)(int)v[c][j + 3], sx), w.w));
         }
-        const int c64 = 2 * h + half;
-        const int64_t n = n0 + 64 * c64;
-        const bool some = n < p.e.N;  // the same for the whole warp
-        if (some) {
+      // (after an expired wait what follows is not right, and the call reports it)
+      ok = mbar_wait(smem_u32(&acc_full[b]), pa, p.e.wait_ns, p.e.err, 0x508) && ok;
+      __syncwarp();
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t a[32];
+        tmem_ld_32x32b_x32(cols + 32u * (uint32_t)c, a);
+        tmem_ld_wait();
+        if (c == 3) {  // the columns may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_remote(at_rank(smem_u32(&acc_read[b]), 0));
+        }
+        const int64_t n = n0 + 128 * half + 32 * c;
+        if (n >= p.e.N && (sizeof(OUT) == 4 || (c & 1) == 0)) continue;  // the same for the whole warp
+        if (sizeof(OUT) == 2 && n - 32 * (c & 1) >= p.e.N) continue;
+        if (sizeof(OUT) == 4 || (c & 1) == 0) {
           if (lane == 0)  // the buffer's last store has been read
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           __syncwarp();
         }
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          uint32_t acc[32];
-          tmem_ld_32x32b_x32(tmem + ((uint32_t)(quad * 32) << 16) + 256u * (uint32_t)b +
-                                 (uint32_t)(64 * c64 + 32 * c),
-                             acc);
-          tmem_ld_wait();
-          if (h == 1 && c == 1) {  // the accumulator may be overwritten
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_remote(at_rank(smem_u32(&acc_empty[b]), 0));
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          a[j] = __float_as_uint(__fadd_rn(__uint_as_float(v[c][j]), __uint_as_float(a[j])));
+        const uint32_t line = buf + (uint32_t)lane * 128;
+        if (sizeof(OUT) == 4) {  // 32 columns fill the buffer
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            st_shared_v4(line + (uint32_t)((q ^ (lane & 7)) << 4), a[4 * q], a[4 * q + 1], a[4 * q + 2],
+                         a[4 * q + 3]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_bf16x2(__uint_as_float(a[8 * q + 2 * i]), __uint_as_float(a[8 * q + 2 * i + 1]));
+            st_shared_v4(line + (uint32_t)(((4 * (c & 1) + q) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
           }
-          if (!some) continue;
-          const int col = 64 * c64 + 32 * c;
-          const float* f = factor + (kLoads == 2 ? col - 128 * h : col) * RT;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            uint64_t d = 0;
-#pragma unroll
-            for (int q = 0; q < RT / 4; ++q) {
-              const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(f + j * RT + 4 * q);
-              d = fma2(u[2 * q], l.x, d);
-              d = fma2(u[2 * q + 1], l.y, d);
-            }
-            const float v = __fmul_rn(__fmul_rn((float)(int)acc[j], sx), wscale[col + j]);
-            acc[j] = __float_as_uint(__fadd_rn(v, sum2(d)));
-          }
-          const uint32_t line = buf + (uint32_t)lane * 128;
-          if (sizeof(OUT) == 4) {  // 32 columns fill the buffer
-            if (c == 1) {
-              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-              __syncwarp();
-            }
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              st_shared_v4(line + (uint32_t)((q ^ (lane & 7)) << 4), acc[4 * q], acc[4 * q + 1],
-                           acc[4 * q + 2], acc[4 * q + 3]);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = pack_bf16x2(__uint_as_float(acc[8 * q + 2 * i]), __uint_as_float(acc[8 * q + 2 * i + 1]));
-              st_shared_v4(line + (uint32_t)(((4 * c + q) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
-            }
-          }
-          if (sizeof(OUT) == 4 || c == 1) {
-            const int64_t x = sizeof(OUT) == 4 ? n + 32 * c : n;
-            if (!p.e.tma_out) {  // rows that TMA does not take: row after row, in runs
-              __syncwarp();
-              const int64_t row0 = row - lane;
-#pragma unroll 4
-              for (int i = 0; i < 32; ++i) {
-                if (row0 + i >= p.e.R) break;
-                OUT* o = (OUT*)p.e.out + (row0 + i) * p.e.N + x;
-#pragma unroll
-                for (int e = lane; e < (int)(128 / sizeof(OUT)); e += 32) {
-                  const int byte = e * (int)sizeof(OUT);
-                  const uint32_t at = buf + (uint32_t)(i * 128 + ((((byte >> 4) ^ (i & 7)) << 4) | (byte & 15)));
-                  if (x + e < p.e.N) o[e] = *reinterpret_cast<const OUT*>(outbuf + (at - smem_u32(outbuf)));
-                }
-              }
-              __syncwarp();
-              continue;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (in && x < p.e.N) tma_store_2d(&tm_out, buf, (int32_t)x, (int32_t)row);
-              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            }
-          }
+          if ((c & 1) == 0) continue;
         }
-        if (h == 1 || kLoads == 2) {
-          // all epilogue warps have read the factor: fetch the next one
-          asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
-          if (ew == 0 && lane == 0) {
-            if (h == 0) fetch(t, 1);
-            else if (t + clusters < tiles) fetch(t + clusters, 0);
+        const int64_t x = sizeof(OUT) == 4 ? n : n - 32;  // of the buffer's first column
+        if (p.e.tma_out) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row < p.e.R) tma_store_2d(&tm_out, buf, (int32_t)x, (int32_t)row);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
+        } else {  // rows that TMA does not take: row after row, in runs
+          __syncwarp();
+          const int rows = (int)min((int64_t)32, p.e.R - row0);
+          OUT* o = (OUT*)p.e.out + row0 * p.e.N + x;
+#pragma unroll
+          for (int e0 = 0; e0 < (int)(128 / sizeof(OUT)); e0 += 32) {
+            const int e = e0 + lane, byte = e * (int)sizeof(OUT);
+            if (x + e >= p.e.N) continue;
+#pragma unroll 8
+            for (int i = 0; i < rows; ++i)
+              o[i * p.e.N + e] =
+                  *reinterpret_cast<const OUT*>(mine + i * 128 + ((((byte >> 4) ^ (i & 7)) << 4) | (byte & 15)));
+          }
+          __syncwarp();
         }
       }
       if (++b == 2) { b = 0; pa ^= 1u; }
@@ -449,20 +492,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-// The adapter factor and the channel scales as the pair kernel reads them:
-// [Npad x RT], s L, zeros outside; [Npad], 1 where there is no channel scale.
-template <bool DX>
-__global__ void __launch_bounds__(256)
-    pack_kernel(const float* __restrict__ L, const float* __restrict__ ws, int64_t N, int64_t Npad, int r,
-                int RT, float s, float* __restrict__ out, float* __restrict__ wpad) {
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (e < Npad) wpad[e] = !DX && e < N ? ws[e] : 1.0f;
-  if (e >= Npad * RT) return;
-  // consecutive threads along n for [r x N], along j for [N x r]
-  const int64_t n = DX ? e % Npad : e / RT;
-  const int j = DX ? (int)(e / Npad) : (int)(e % RT);
-  const float v = n < N && j < r ? s * L[DX ? (int64_t)j * N + n : n * r + j] : 0.0f;
-  out[n * RT + j] = v;
+// T and s L as the pair kernel's adapter product reads them: an fp32 value is
+// the sum of three bf16 parts (each remainder is exact), a row's six runs of RP
+// hold the parts that part_T or part_L names, and the product over the whole row
+// is s T L^T but for terms below 2^-24 of its summands.  Zeros past r.
+struct PackJob {
+  const float* src;  // [n x r] (kr), or [r x n]
+  uint16_t* dst;     // [n x 6 RP]
+  int64_t n;
+  float s;
+  int32_t kr, right, blocks;
+};
+struct PackArgs {
+  PackJob job[2];
+  int32_t r;
+};
+// Rows of a block: one or two pairs of values a thread.
+__host__ __device__ constexpr int pack_rows(int RP) { return RP == 8 ? 64 : RP == 64 ? 16 : 32; }
+template <int RP>
+__global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
+  constexpr int kRows = pack_rows(RP);
+  __shared__ float tile[kRows][RP + 1];
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int second = (int)blockIdx.x >= a.job[0].blocks ? 1 : 0;
+  const PackJob b = second ? a.job[1] : a.job[0];
+  const int64_t n0 = ((int64_t)blockIdx.x - (second ? a.job[0].blocks : 0)) * kRows;
+  const int rows = (int)min((int64_t)kRows, b.n - n0);
+  griddep_wait();  // T is there (and every CTA waits: the grid ends after the ones before it)
+  // consecutive threads along the source's rows
+#pragma unroll
+  for (int e0 = 0; e0 < kRows * RP; e0 += 256) {
+    const int e = e0 + threadIdx.x, k = b.kr ? e / RP : e % kRows, j = b.kr ? e % RP : e / kRows;
+    tile[k][j] = k < rows && j < a.r ? b.s * __ldcg(b.src + (b.kr ? (n0 + k) * a.r + j : j * b.n + n0 + k)) : 0.0f;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e0 = 0; e0 < kRows * RP / 2; e0 += 256) {
+    const int e = e0 + threadIdx.x, k = e / (RP / 2), j = 2 * (e % (RP / 2));
+    if (k >= rows) continue;
+    uint32_t part[3] = {};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float v = tile[k][j + i];
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(v);
+        part[q] |= (uint32_t)__bfloat16_as_ushort(h) << (16 * i);
+        v -= __bfloat162float(h);
+      }
+    }
+    uint32_t* out = reinterpret_cast<uint32_t*>(b.dst + (n0 + k) * 6 * RP + j);
+#pragma unroll
+    for (int c = 0; c < 6; ++c) out[c * RP / 2] = b.right ? part[part_L(c)] : part[part_T(c)];
+  }
 }
 
 // ---------------------------------------------------------- stream kernel
@@ -729,9 +811,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     auto stage_side = [&](int64_t t0, int toks) {
       for (int e = et; e < toks * RT; e += kStreamEpi) {
         const int t = e / RT, j = e % RT;
-        side[e] = j < p.e.r ? p.e.s * __ldg(p.e.T + (t0 + t) * p.e.r + j) : 0.0f;
+        side[e] = j < p.e.r ? p.e.s * __ldcg(p.e.T + (t0 + t) * p.e.r + j) : 0.0f;
       }
-      for (int e = et; e < toks; e += kStreamEpi) side[BN * RT + e] = __ldg(p.e.xs + t0 + e);
+      for (int e = et; e < toks; e += kStreamEpi) side[BN * RT + e] = __ldcg(p.e.xs + t0 + e);
     };
     if constexpr (BN == 16 && DX) {
       if (p.dA || p.dB) {  // a single token tile
@@ -740,7 +822,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         if (p.dB)
           for (int e = et; e < (int)p.e.R * RT; e += kStreamEpi) {
             const int t = e / RT, j = e % RT;
-            su[e] = j < p.e.r ? p.e.s * __ldg(p.U + t * p.e.r + j) : 0.0f;
+            su[e] = j < p.e.r ? p.e.s * __ldcg(p.U + t * p.e.r + j) : 0.0f;
           }
         staged = 0;
         asm volatile("bar.sync 1, %0;" ::"n"(kStreamEpi) : "memory");
@@ -869,6 +951,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// K steps of the pair kernel's adapter product: 64 bf16 each of 6 RP.
+int adapter_steps(int r) { return (6 * rank_pad(r) + 63) / 64; }
+
 struct Plan {
   bool pair;
   int bn;          // stream: token tile
@@ -880,24 +965,29 @@ struct Plan {
 // Pair or stream, and how the latter's work is dealt out, by cost in K steps
 // of one SM (512 cycles: what the products of a 128 x 256 half tile take, and
 // also what the 32 KB of a 128 x 128 stream step take from L2).  The pair
-// kernel pays whole rounds of tiles over the CTA pairs and the last tile's
-// epilogue; the stream kernel pays whole rounds of tiles over the SMs, or, with
-// tiles shared, an equal run of steps and the meeting of the partial sums, which
-// grows with the token tile.  A tile takes no less than its epilogue: about nine
-// steps for either kernel's (the pair kernel's outputs are twice as many).
-Plan plan_for(int64_t R, int64_t N, int64_t K) {
-  const int64_t sms = sm_count(), KB = up(K, kBK);
+// kernel pays whole rounds of tiles over the CTA pairs, with the adapter's steps,
+// and the last tile's epilogue; the stream kernel pays whole rounds of tiles over
+// the SMs, or, with tiles shared, an equal run of steps and the meeting of the
+// partial sums, which grows with the token tile.  A tile takes no less than its
+// epilogue: about nine steps for the pair kernel's, and for the stream kernel's as
+// many as its adapter term reads from shared memory (nine at 128 tokens and rank
+// 8).  On both sides of the choice: 777 tokens of 2048 x 1024 at rank 8, stream
+// 11.6 us, pair 13; 79 tokens of 4084 x 2704 at rank 64, stream 41, pair 18 + 4
+// for packing its factors.
+Plan plan_for(int64_t R, int64_t N, int64_t K, int r) {
+  const int64_t sms = sm_count(), KB = up(K, kBK), RT = rank_pad(r);
   Plan p;
   p.bn = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128;
   const int64_t pair_tiles = up(R, 256) * up(N, 256), tiles = up(R, p.bn) * up(N, 128);
   const int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
-  const int64_t cost_pair = up(pair_tiles, pairs) * (KB > 9 ? KB : 9) + 10;
-  const int64_t least = p.bn / 14;  // epilogue of a stream tile, in steps
+  const int64_t pair_tile = KB + adapter_steps(r), pair_least = 9;
+  const int64_t cost_pair = up(pair_tiles, pairs) * (pair_tile > pair_least ? pair_tile : pair_least) + 10;
+  const int64_t least = p.bn * RT / 112;  // epilogue of a stream tile, in steps
   const int64_t cost_whole = up(tiles, sms) * (KB > least ? KB : least) + 5;
   const int64_t run = up(tiles * KB, sms), ends = up(tiles, sms) * 2 * least;
   const int64_t cost_shared = (run > ends ? run : ends) + 4 + p.bn / 8;
   p.shared = cost_shared < cost_whole;
-  p.pair = R > 128 && cost_pair < (p.shared ? cost_shared : cost_whole);
+  p.pair = R > 64 && cost_pair < (p.shared ? cost_shared : cost_whole);
   if (p.pair) {
     p.tiles = pair_tiles;
     p.ctas = (int)(2 * (pair_tiles < pairs ? pair_tiles : pairs));
@@ -912,21 +1002,61 @@ Plan plan_for(int64_t R, int64_t N, int64_t K) {
   return p;
 }
 
-size_t pair_pack_bytes(int64_t N, int r) {
-  return (size_t)up(N, 256) * 256 * ((size_t)rank_pad(r) + 1) * 4;
-}
+size_t pack_bytes(int64_t n, int r) { return align_up((size_t)n * 12 * (size_t)rank_pad(r), 256); }
 size_t stream_part_bytes(const Plan& p) { return !p.shared ? 0 : align_up((size_t)p.tiles * (size_t)p.bn * 128 * 4, 256); }
 size_t stream_ticket_bytes(const Plan& p) { return !p.shared ? 0 : align_up((size_t)p.tiles * 4, 256); }
 
-template <bool DX, typename OUT, int RT>
-cudaError_t go_pair(const Plan& pl, const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& o,
-                    const PairArgs& a, cudaStream_t st) {
-  static std::atomic<bool> done[kMaxDevices];
-  cudaError_t e = allow_smem(pair_kernel<DX, OUT, RT>, kPairSmem, done);
-  if (e != cudaSuccess) return e;
-  pair_kernel<DX, OUT, RT><<<pl.ctas, kPairThreads, kPairSmem, st>>>(x, w, o, a);
+template <int RP>
+cudaError_t go_pack(const PackArgs& a, cudaStream_t st) {
+  const cudaError_t e = launch_after(pack_kernel<RP>, a.job[0].blocks + a.job[1].blocks, 256, 0, st, a);
   count_launch();
-  return cudaGetLastError();
+  return e;
+}
+
+template <bool DX, typename OUT>
+cudaError_t go_pair(const Plan& pl, const Int8Call& c, const CUtensorMap& x, const CUtensorMap& w, Epi e,
+                    int64_t K, void* ws, cudaStream_t st) {
+  const int RP = rank_pad(e.r);
+  uint16_t *t6 = (uint16_t*)ws, *l6 = (uint16_t*)((char*)ws + pack_bytes(e.R, e.r));
+  PackArgs k = {};
+  k.job[0] = {e.T, t6, e.R, 1.0f, 1, 0, (int32_t)up(e.R, pack_rows(RP))};
+  k.job[1] = {e.L, l6, e.N, e.s, DX ? 0 : 1, 1, (int32_t)up(e.N, pack_rows(RP))};
+  k.r = e.r;
+  cudaError_t err = RP == 8 ? go_pack<8>(k, st) : RP == 16 ? go_pack<16>(k, st)
+                                                : RP == 32 ? go_pack<32>(k, st) : go_pack<64>(k, st);
+  if (err != cudaSuccess) return err;
+  CUtensorMap mt, ml, mo;
+  const uint64_t row = (uint64_t)6 * RP;
+  if (!make_map_2d(&mt, t6, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, row, (uint64_t)e.R, 2 * row, 64, 128) ||
+      !make_map_2d(&ml, l6, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, row, (uint64_t)e.N, 2 * row, 64, 128))
+    return cudaErrorInvalidValue;
+  e.tma_out = ((uintptr_t)c.out % 16 == 0 && (e.N * sizeof(OUT)) % 16 == 0) ? 1 : 0;
+  if (e.tma_out &&
+      !make_map_2d(&mo, c.out, sizeof(OUT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                (uint64_t)e.N, (uint64_t)c.R, (uint64_t)e.N * sizeof(OUT), 128 / sizeof(OUT), 32))
+    return cudaErrorInvalidValue;
+  if (!e.tma_out) mo = x;  // not used
+  PairArgs a;
+  a.e = e;
+  a.KB = (int32_t)up(K, kBK);
+  a.tiles_m = (int32_t)up(e.R, 256);
+  a.tiles_n = (int32_t)up(e.N, 256);
+  a.KA = adapter_steps(e.r);
+  a.at = a.KB / 2 < 6 ? a.KB / 2 : 6;
+  static std::atomic<bool> done[kMaxDevices];
+  err = allow_smem(pair_kernel<DX, OUT>, kPairSmem, done);
+  if (err != cudaSuccess) return err;
+  // the epilogue warps' registers come out of the launch's own: a build with fewer
+  // would wait for them
+  static const bool fits = [] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, pair_kernel<DX, OUT>) == cudaSuccess &&
+           f.numRegs * kPairThreads >= 128 * kPairRegs + 32 * kEpiWarps * kEpiRegs;
+  }();
+  if (!fits) return cudaErrorLaunchOutOfResources;
+  err = launch_after(pair_kernel<DX, OUT>, pl.ctas, kPairThreads, kPairSmem, st, x, w, mt, ml, mo, a);
+  count_launch();
+  return err;
 }
 
 template <bool DX, int BN, int RT>
@@ -936,56 +1066,14 @@ cudaError_t go_stream(const Plan& pl, const CUtensorMap& x, const CUtensorMap& w
   auto kern = stream_kernel<DX, BN, RT>;
   cudaError_t e = allow_smem(kern, (StreamCfg<BN, RT>::kSmem), done);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)pl.ctas);
-  cfg.blockDim = dim3(kStreamThreads);
-  cfg.dynamicSmemBytes = (StreamCfg<BN, RT>::kSmem);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, x, w, a);
+  e = launch_after(kern, pl.ctas, kStreamThreads, StreamCfg<BN, RT>::kSmem, st, x, w, a);
   count_launch();
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return e;
 }
 
-template <bool DX, typename OUT, int RT>
-cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& base, const Int8Few* few,
-               int64_t K, void* ws, cudaStream_t st) {
-  Epi e = base;
-  CUtensorMap mx, mw, mo;
-  const int64_t xp = int8_pitch(K), wp = int8_pitch(c.I);
-  if (!make_map_2d(&mw, c.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)wp, (uint64_t)c.O, (uint64_t)wp, 128,
-                128) ||
-      !make_map_2d(&mx, xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)xp, (uint64_t)c.R, (uint64_t)xp, 128,
-                pl.pair ? 128 : (uint32_t)pl.bn))
-    return cudaErrorInvalidValue;
-  if (pl.pair) {
-    float* pk = (float*)ws;
-    const int64_t Npad = up(e.N, 256) * 256;
-    float* wpad = pk + Npad * RT;
-    pack_kernel<DX><<<(unsigned)up(Npad * RT, 256), 256, 0, st>>>(e.L, e.ws, e.N, Npad, e.r, RT, e.s, pk,
-                                                                  wpad);
-    count_launch();
-    const cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    e.L = pk;
-    e.wpad = wpad;
-    e.tma_out = ((uintptr_t)c.out % 16 == 0 && (e.N * sizeof(OUT)) % 16 == 0) ? 1 : 0;
-    if (e.tma_out &&
-        !make_map_2d(&mo, c.out, sizeof(OUT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                  (uint64_t)e.N, (uint64_t)c.R, (uint64_t)e.N * sizeof(OUT), 128 / sizeof(OUT), 32))
-      return cudaErrorInvalidValue;
-    if (!e.tma_out) mo = mx;  // not used
-    PairArgs a;
-    a.e = e;
-    a.KB = (int32_t)up(K, kBK);
-    a.tiles_m = (int32_t)up(c.R, 256);
-    a.tiles_n = (int32_t)up(e.N, 256);
-    return go_pair<DX, OUT, RT>(pl, mx, mw, mo, a, st);
-  }
+template <bool DX, int RT>
+cudaError_t go(const Plan& pl, const Int8Call& c, const CUtensorMap& mx, const CUtensorMap& mw, const Epi& e,
+               const Int8Few* few, int64_t K, void* ws, cudaStream_t st) {
   StreamArgs a = {};
   a.e = e;
   a.KB = (int32_t)up(K, kBK);
@@ -1018,14 +1106,24 @@ cudaError_t go(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& b
   }
 }
 
-template <bool DX, typename OUT>
+template <bool DX>
 cudaError_t go_rank(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& e, const Int8Few* few,
-                    int64_t K, void* ws, cudaStream_t st) {
+                    void* ws, cudaStream_t st) {
+  CUtensorMap mx, mw;
+  const int64_t K = DX ? c.O : c.I, xp = int8_pitch(K), wp = int8_pitch(c.I);
+  if (!make_map_2d(&mw, c.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)wp, (uint64_t)c.O, (uint64_t)wp, 128,
+                128) ||
+      !make_map_2d(&mx, xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)xp, (uint64_t)c.R, (uint64_t)xp, 128,
+                pl.pair ? 128 : (uint32_t)pl.bn))
+    return cudaErrorInvalidValue;
+  if (pl.pair)
+    return c.bf16 ? go_pair<DX, __nv_bfloat16>(pl, c, mx, mw, e, K, ws, st)
+                  : go_pair<DX, float>(pl, c, mx, mw, e, K, ws, st);
   switch (rank_pad(c.r)) {
-    case 8: return go<DX, OUT, 8>(pl, c, xq, e, few, K, ws, st);
-    case 16: return go<DX, OUT, 16>(pl, c, xq, e, few, K, ws, st);
-    case 32: return go<DX, OUT, 32>(pl, c, xq, e, few, K, ws, st);
-    default: return go<DX, OUT, 64>(pl, c, xq, e, few, K, ws, st);
+    case 8: return go<DX, 8>(pl, c, mx, mw, e, few, K, ws, st);
+    case 16: return go<DX, 16>(pl, c, mx, mw, e, few, K, ws, st);
+    case 32: return go<DX, 32>(pl, c, mx, mw, e, few, K, ws, st);
+    default: return go<DX, 64>(pl, c, mx, mw, e, few, K, ws, st);
   }
 }
 
@@ -1033,20 +1131,20 @@ cudaError_t go_rank(const Plan& pl, const Int8Call& c, const int8_t* xq, const E
 
 size_t int8_tc_ws(bool dx, int64_t R, int64_t O, int64_t I, int32_t r) {
   if (R == 0) return 0;
-  const Plan p = plan_for(R, dx ? I : O, dx ? O : I);
-  return p.pair ? pair_pack_bytes(dx ? I : O, r) : stream_part_bytes(p) + stream_ticket_bytes(p);
+  const int64_t N = dx ? I : O;
+  const Plan p = plan_for(R, N, dx ? O : I, r);
+  return p.pair ? pack_bytes(R, r) + pack_bytes(N, r) : stream_part_bytes(p) + stream_ticket_bytes(p);
 }
 
-size_t int8_tc_zeroed(bool dx, int64_t R, int64_t O, int64_t I) {
+size_t int8_tc_zeroed(bool dx, int64_t R, int64_t O, int64_t I, int32_t r) {
   if (R == 0) return 0;
-  const Plan p = plan_for(R, dx ? I : O, dx ? O : I);
+  const Plan p = plan_for(R, dx ? I : O, dx ? O : I, r);
   return p.pair ? 0 : stream_part_bytes(p) + stream_ticket_bytes(p);
 }
 
 cudaError_t launch_int8_tc(const Int8Call& c, const int8_t* xq, const float* xs, const Int8Few* few, void* ws,
                            uint32_t* hdr, cudaStream_t st) {
-  const int64_t K = c.dx ? c.O : c.I;
-  const Plan pl = plan_for(c.R, c.dx ? c.I : c.O, K);
+  const Plan pl = plan_for(c.R, c.dx ? c.I : c.O, c.dx ? c.O : c.I, c.r);
   Epi e = {};
   e.R = c.R;
   e.N = c.dx ? c.I : c.O;
@@ -1057,15 +1155,10 @@ cudaError_t launch_int8_tc(const Int8Call& c, const int8_t* xq, const float* xs,
   e.r = c.r;
   e.s = c.s;
   e.out = c.out;
-  e.tma_out = 0;
   e.bf16 = c.bf16 ? 1 : 0;
   e.err = hdr;
   e.wait_ns = kWaitLimitNs;
-  if (c.dx)
-    return c.bf16 ? go_rank<true, __nv_bfloat16>(pl, c, xq, e, few, K, ws, st)
-                  : go_rank<true, float>(pl, c, xq, e, few, K, ws, st);
-  return c.bf16 ? go_rank<false, __nv_bfloat16>(pl, c, xq, e, few, K, ws, st)
-                : go_rank<false, float>(pl, c, xq, e, few, K, ws, st);
+  return c.dx ? go_rank<true>(pl, c, xq, e, few, ws, st) : go_rank<false>(pl, c, xq, e, few, ws, st);
 }
 
 }  // namespace qlora

@@ -107,6 +107,17 @@ def test_workspace_sizes(lib, R, O, I):
     assert lib.qlora_linear_workspace_bytes(ctypes.byref(w), R, 8, 0, 1) == 0
 
 
+def test_token_limit(lib, d):
+    """More tokens than the counts of CTAs hold are refused, and have no workspace."""
+    w, n = weight(d, O=16, I=16), 1 << 62
+    for R, ok in ((1 << 28, True), ((1 << 28) + 1, False)):
+        for op in (0, 1):
+            assert (lib.qlora_linear_workspace_bytes(ctypes.byref(w), R, 64, op, 1) > 0) == ok
+        fwd = lib.qlora_linear_fwd(ctypes.byref(w), d, R, d, d, 64, 1.0, 1, d, None, d, 256 if ok else n, None)
+        bwd = lib.qlora_linear_bwd(ctypes.byref(w), d, d, R, d, d, 64, 1.0, None, 1, d, d, d, d, 256 if ok else n, None)
+        assert fwd == bwd == (_ffi.ERR_WORKSPACE if ok else _ffi.ERR_SHAPE)
+
+
 def tensors(d, n=(16,), **kw):
     a = (_ffi.qlora_tensor * len(n))()
     for t, k in zip(a, n):
