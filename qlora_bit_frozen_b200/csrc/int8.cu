@@ -110,7 +110,7 @@ struct RowsArgs {
   const void* P;       // [R x K]
   int64_t R, K, pitch;
   const float* f;      // [K] column factors, nullable
-  int8_t* codes;       // [R x pitch], zeros in the padding
+  int8_t* codes;       // [R x pitch], zeros from K to the next multiple of 16
   float* scale;        // [R]
   uint32_t* bad;       // set where a row has a NaN or Inf, nullable
   Clear clear;
@@ -584,7 +584,7 @@ Layout layout(int64_t R, int64_t K) {
   Layout l;
   l.scale = 0;
   l.codes = align_up((size_t)R * 4, 256);
-  l.total = l.codes + align_up((size_t)R * (size_t)int8_pitch(K), 256);
+  l.total = l.codes + align_up((size_t)R * (size_t)int8_act_pitch(K), 256);
   return l;
 }
 
@@ -595,7 +595,7 @@ RowsArgs rows_args(const Int8Call& c, void* ws, Int8Clear header) {
   a.P = c.P;
   a.R = c.R;
   a.K = K;
-  a.pitch = int8_pitch(K);
+  a.pitch = int8_act_pitch(K);
   a.f = c.dx ? c.wscale : nullptr;
   a.codes = (int8_t*)ws + l.codes;
   a.scale = (float*)((char*)ws + l.scale);

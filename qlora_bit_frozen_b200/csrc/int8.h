@@ -16,6 +16,10 @@ constexpr int64_t kInt8MaxK = 131072;
 constexpr int64_t kInt8MaxTokens = 1 << 28;
 
 constexpr int64_t int8_pitch(int64_t n) { return (n + 15) / 16 * 16; }
+// Of the activations' codes, which only these kernels see: above 1024 columns
+// the rows lie on 128 bytes, since a 128-byte box row that straddles two lines
+// costs L2 two requests (9421 tokens of 2048 x 6992: 110 us, so 88).
+constexpr int64_t int8_act_pitch(int64_t n) { return n > 1024 ? (n + 127) / 128 * 128 : int8_pitch(n); }
 
 // codes [O x pitch], scale [O] of W [O x I]; *bad (device or mapped host
 // memory) is set where W holds a NaN or Inf.
@@ -86,7 +90,7 @@ cudaError_t launch_int8_dots(const Int8Dot* d, int count, bool bf16, int64_t R, 
 cudaError_t launch_int8_product(const Int8Call& c, void* ws, uint32_t* hdr, const Int8Few* few,
                                 cudaStream_t st);
 
-// int8_tc.cu: the product over codes xq [R x int8_pitch(K)] with row scales
+// int8_tc.cu: the product over codes xq [R x int8_act_pitch(K)] with row scales
 // xs; ws: int8_tc_ws bytes, of which the first int8_tc_zeroed are zero; few:
 // the backward's side sums, nullable.
 size_t int8_tc_ws(bool dx, int64_t R, int64_t O, int64_t I, int32_t r);

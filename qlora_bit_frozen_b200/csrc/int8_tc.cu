@@ -1110,10 +1110,10 @@ template <bool DX>
 cudaError_t go_rank(const Plan& pl, const Int8Call& c, const int8_t* xq, const Epi& e, const Int8Few* few,
                     void* ws, cudaStream_t st) {
   CUtensorMap mx, mw;
-  const int64_t K = DX ? c.O : c.I, xp = int8_pitch(K), wp = int8_pitch(c.I);
+  const int64_t K = DX ? c.O : c.I, xp = int8_act_pitch(K), wp = int8_pitch(c.I);
   if (!make_map_2d(&mw, c.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)wp, (uint64_t)c.O, (uint64_t)wp, 128,
                 128) ||
-      !make_map_2d(&mx, xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)xp, (uint64_t)c.R, (uint64_t)xp, 128,
+      !make_map_2d(&mx, xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)int8_pitch(K), (uint64_t)c.R, (uint64_t)xp, 128,
                 pl.pair ? 128 : (uint32_t)pl.bn))
     return cudaErrorInvalidValue;
   if (pl.pair)
