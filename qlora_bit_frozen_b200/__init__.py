@@ -86,6 +86,17 @@ def workspace(nbytes: int, device="cuda") -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+def _scratch(nbytes: int, dev, stream) -> torch.Tensor:
+    """The workspace of one call, allocated for the stream that the call runs on
+    (else it could be handed out again while that stream still uses it)."""
+    if stream is None:
+        return workspace(nbytes, dev)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        return workspace(nbytes, dev)
+
+
 @dataclass
 class QuantizedWeight:
     """Device buffers of a frozen quantized weight (immutable by convention)."""
@@ -449,7 +460,7 @@ def qlora_grad_norm(tensors: OptimTensors, max_norm: float, control: torch.Tenso
     _need(f, "control", control, dev, (4,), torch.int32)
     with _on(dev):
         if ws is None:
-            ws = workspace(qlora_grad_norm_workspace_bytes(tensors), dev)
+            ws = _scratch(qlora_grad_norm_workspace_bytes(tensors), dev, stream)
         _need(f, "ws", ws, dev)
         st = _ffi.load().qlora_grad_norm(tensors._c, len(tensors.grads), float(max_norm), _ptr(control),
                                          _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
@@ -505,7 +516,7 @@ def qlora_linear_fwd(w: QuantizedWeight, X: torch.Tensor, A: torch.Tensor, B: to
         U_out = A.new_empty((R, r))
     cw = ctypes.byref(w.c_struct())
     if ws is None:
-        ws = workspace(lib.qlora_linear_workspace_bytes(cw, R, r, OP_FWD, compute), X.device)
+        ws = _scratch(lib.qlora_linear_workspace_bytes(cw, R, r, OP_FWD, compute), X.device, stream)
     dev, f = w.codes.device, "qlora_linear_fwd"
     _need(f, "X", X, dev, (R, w.I))
     _need(f, "A", A, dev, (r, w.I), torch.float32)
@@ -539,7 +550,7 @@ def qlora_linear_bwd(w: QuantizedWeight, X: Optional[torch.Tensor], dY: torch.Te
         dB = torch.empty((w.O, r), dtype=torch.float32, device=dev)
     cw = ctypes.byref(w.c_struct())
     if ws is None:
-        ws = workspace(lib.qlora_linear_workspace_bytes(cw, R, r, OP_BWD, compute), dev)
+        ws = _scratch(lib.qlora_linear_workspace_bytes(cw, R, r, OP_BWD, compute), dev, stream)
     wd, f = w.codes.device, "qlora_linear_bwd"
     _need(f, "dY", dY, wd, (R, w.O))
     _need(f, "X", X, wd, (R, w.I), dY.dtype)

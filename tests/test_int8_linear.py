@@ -177,6 +177,105 @@ def test_parts_of_the_gradient_alone(R, r):
         assert torch.equal(part[k], full[k])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("r", [1, 5, 16, 33, 64])
+@pytest.mark.parametrize("R,O,I", [(65, 1500, 136), (100, 4100, 520), (129, 272, 2064), (257, 264, 130), (2600, 777, 1100)])
+def test_ranks_over_token_counts(R, O, I, r, dtype):
+    test_forward_and_backward(R, O, I, r, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("r", [1, 8, 16, 40, 64])
+@pytest.mark.parametrize("R,O,I", [(2, 512, 384), (14, 512, 384), (90, 1024, 640), (640, 1024, 512), (2500, 1536, 1024)])
+def test_adapter_keeps_all_bits(R, O, I, r, dtype):
+    """Sums of one term each, a factor's value times a power of two: the 24 bits of the factor come
+    through, but for the tensor core's last bit (one truncated addition: 2^-23)."""
+    W, _, _, A, B = make(R, O, I, r, dtype)
+    w, _, _ = weight(torch.zeros_like(W))
+    rows = torch.arange(R, device="cuda")
+    at = rows * 37 % I
+    X = torch.zeros(R, I, dtype=dtype, device="cuda")
+    X[rows, at] = 2.0 ** (rows % 9 - 4).float().to(dtype)
+    _, Ug = q.qlora_linear_fwd(w, X, A, torch.zeros_like(B), float(r))
+    u = 2.0 ** (rows % 9 - 4).double()[:, None] * A.double()[:, at].T
+    close(Ug, u, 2 * U * u.abs())
+    # U has one power of two a token, so that Y = U B^T holds the values of B
+    j = rows % r
+    one = torch.zeros(r, I, device="cuda")
+    k = torch.arange(r, device="cuda") * (I // r)
+    one[torch.arange(r), k] = 0.25
+    X.zero_()
+    X[rows, k[j]] = 2.0
+    Y, _ = q.qlora_linear_fwd(w, X, one, B, float(r))
+    y = 0.5 * B.double()[:, j].T
+    close(Y, y, (HALF[dtype] + 2 * U) * 1.01 * y.abs())
+    # and the same of V, dX = V A, dA = V^T X and dB = dY^T U with one token that counts
+    dY = torch.zeros(R, O, dtype=dtype, device="cuda")
+    o = rows * 29 % O
+    dY[rows, o] = 0.5
+    dX, _, _ = q.qlora_linear_bwd(w, X, dY, A, torch.zeros_like(B).index_fill_(1, torch.tensor([r - 1], device="cuda"), 4.0),
+                                  float(r))
+    close(dX, 2 * A.double()[r - 1].expand(R, I), (HALF[dtype] + 2 * U) * 1.01 * 2 * A.double()[r - 1].abs())
+    t = R // 2
+    X.zero_()
+    X[t] = 2.0 ** (torch.arange(I, device="cuda") % 7 - 3).float().to(dtype)
+    dY.zero_()
+    dY[t] = 2.0 ** (torch.arange(O, device="cuda") % 5 - 2).float().to(dtype)
+    Uin = normal(5, R, r)
+    one = torch.zeros_like(B)
+    one[3] = B[3]
+    _, dA, dB = q.qlora_linear_bwd(w, X, dY, A, one, float(r), U=Uin)
+    v = dY.double()[t, 3] * B.double()[3]
+    ref = v[:, None] * X.double()[t][None, :]
+    close(dA, ref, 4 * U * ref.abs())
+    ref = dY.double()[t][:, None] * Uin.double()[t][None, :]
+    close(dB, ref, 2 * U * ref.abs())
+
+
+@pytest.mark.parametrize("R,r", [(90, 64), (700, 8), (3000, 16)])
+def test_nonfinite_values_keep_to_their_rows_and_columns(R, r):
+    """A bad token changes its own row only, a bad row of a factor its own output only."""
+    O, I = 1100, 1030
+    W, X, dY, A, B = make(R, O, I, r, BF)
+    w, _, _ = weight(W)
+    bad = torch.tensor([0, R // 2, R - 1], device="cuda")
+    X[bad] = 0
+    Y, Ug = q.qlora_linear_fwd(w, X, A, B, 16.0)
+    X2, B2 = X.clone(), B.clone()
+    X2[bad, 7] = torch.tensor([float("nan"), float("inf"), float("-inf")], dtype=BF, device="cuda")
+    B2[5, 0] = float("inf")
+    B2[O - 1, r - 1] = float("nan")
+    Y2, U2 = q.qlora_linear_fwd(w, X2, A, B2, 16.0)
+    rows = torch.ones(R, dtype=torch.bool, device="cuda")
+    rows[bad] = False
+    cols = torch.ones(O, dtype=torch.bool, device="cuda")
+    cols[[5, O - 1]] = False
+    assert torch.equal(Y2[rows][:, cols], Y[rows][:, cols]) and torch.equal(U2[rows], Ug[rows])
+    assert bool(torch.isnan(Y2[bad]).all()) and not bool(torch.isfinite(Y2[:, ~cols]).any())
+
+
+@pytest.mark.parametrize("R", [3, 300, 2000])
+def test_a_call_on_a_stream_of_its_own_keeps_its_workspace(R):
+    """The workspace that a call allocates is not handed out while its stream still uses it."""
+    W, X, dY, A, B = make(R, 1024, 1024, 16, BF)
+    w, _, _ = weight(W)
+    Y, Ug = q.qlora_linear_fwd(w, X, A, B, 16.0)
+    g = q.qlora_linear_bwd(w, X, dY, A, B, 16.0, U=Ug)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        outs = [(torch.empty_like(Y), torch.empty_like(Ug), [torch.empty_like(x) for x in g]) for _ in range(4)]
+        torch.cuda.synchronize()
+        for y, u, (dx, da, db) in outs:
+            q.qlora_linear_fwd(w, X, A, B, 16.0, Y=y, U_out=u, stream=stream)
+            q.qlora_linear_bwd(w, X, dY, A, B, 16.0, U=u, dX=dx, dA=da, dB=db, stream=stream)
+            n = max(q.qlora_linear_workspace_bytes(w, R, 16, op, q.COMPUTE_BF16) for op in (0, 1))
+            for _ in range(3):  # takes what the current stream's pool has to give
+                torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        for y, u, grads in outs:
+            assert torch.equal(y, Y) and torch.equal(u, Ug) and all(torch.equal(a, b) for a, b in zip(grads, g))
+
+
 def test_no_rows():
     W, X, dY, A, B = make(1, 48, 32, 8, BF)
     w, _, _ = weight(W)
