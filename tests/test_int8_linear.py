@@ -460,3 +460,40 @@ def test_another_device_than_the_current_one():
         ref = q.qlora_linear_fwd(q.qlora_quantize_int8(W), X, A, B, 8.0)[0]
     got = q.qlora_linear_fwd(q.qlora_quantize_int8(W), X, A, B, 8.0)[0]
     assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("R,O,I", [(2, 131072, 16400), (130, 131072, 16400), (1_100_000, 2048, 1000), (1_100_000, 1000, 2048)])
+def test_offsets_past_32_bits(R, O, I):
+    """More than 2^31 weight codes, activations or outputs: the first and last rows and columns."""
+    r, c = 8, 2.0
+    W, A, B = (normal(k, *s, std=0.02) for k, s in enumerate(((O, I), (r, I), (O, r))))
+    w = q.qlora_quantize_int8(W)
+    X, dY = (normal(k, R, n).to(BF) for k, n in ((5, I), (6, O)))
+    Y, Ug = q.qlora_linear_fwd(w, X, A, B, c * r)
+    dX, dA, dB = q.qlora_linear_bwd(w, X, dY, A, B, c * r, U=Ug)
+    rows = sorted({0, 1, R // 2, R - 2, R - 1})
+    outs = torch.tensor([0, 1, O // 2, O - 2, O - 1], device="cuda")
+    nw, s = rows64(W[outs])
+    n, sx = rows64(X[rows].float())
+    u, du = products(X[rows], A)
+    base = (n @ nw.T) * sx.double()[:, None] * s.double()[None, :]
+    b = B[outs].double()
+    off = 4 * U * base.abs() + c * (du @ b.abs().T + (r + 3) * U * (u.abs() @ b.abs().T))
+    ref = base + c * (u @ b.T)
+    close(Y[rows][:, outs], ref, HALF[BF] * (ref.abs() + off) + off)
+    cols = torch.tensor([0, 1, I // 2, I - 2, I - 1], device="cuda")
+    n, sg = rows64(dY[rows].float() * w.scale[None, :])
+    v, dv = products(dY[rows], B.T)
+    a = A[:, cols].double()
+    base = (n @ w.codes[:, cols].double()) * sg.double()[:, None]
+    off = 4 * U * base.abs() + c * (dv @ a.abs() + (r + 3) * U * (v.abs() @ a.abs()))
+    ref = base + c * (v @ a)
+    close(dX[rows][:, cols], ref, HALF[BF] * (ref.abs() + off) + off)
+    # the gradients' last columns, over all tokens
+    v, dv = products(dY, B.T)
+    x = X[:, cols].double()
+    rel = 2.0 ** -16 + (R + 3) * U
+    close(dA[:, cols], c * v.T @ x, c * (rel * v.abs().T @ x.abs() + dv.T @ x.abs()) * 1.001)
+    u, du = products(X, A)
+    g = dY[:, outs].double()
+    close(dB[outs], c * g.T @ u, c * (rel * g.abs().T @ u.abs() + g.abs().T @ du) * 1.001)
