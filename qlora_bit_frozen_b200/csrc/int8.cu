@@ -264,10 +264,25 @@ __global__ void __launch_bounds__(kThreads) rows_any_kernel(const RowsArgs a) {
   }
 }
 
+// Grid: what the SMs hold at once of this kernel, each CTA over rows in turn
+// (more would read the column factors again); few rows get extra CTAs for
+// clearing.
+template <typename T, int NV, bool FACTOR>
+void rows_launch(const RowsArgs& a, unsigned clear, int threads, cudaStream_t st) {
+  static const int regs = [] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, rows_kernel<T, NV, FACTOR>) == cudaSuccess ? (f.numRegs + 7) / 8 * 8 : 64;
+  }();
+  const int by_regs = 65536 / (regs * threads), by_threads = 2048 / threads;
+  const int64_t most = (int64_t)sm_count() * (by_regs < 1 ? 1 : by_regs < by_threads ? by_regs : by_threads);
+  unsigned ctas = (unsigned)(a.R < most ? a.R : most);
+  if (ctas < clear) ctas = clear;
+  rows_kernel<T, NV, FACTOR><<<ctas, threads, 0, st>>>(a);
+}
 template <typename T, int NV>
-void rows_go(const RowsArgs& a, unsigned ctas, int threads, cudaStream_t st) {
-  if (a.f) rows_kernel<T, NV, true><<<ctas, threads, 0, st>>>(a);
-  else rows_kernel<T, NV, false><<<ctas, threads, 0, st>>>(a);
+void rows_go(const RowsArgs& a, unsigned clear, int threads, cudaStream_t st) {
+  if (a.f) rows_launch<T, NV, true>(a, clear, threads, st);
+  else rows_launch<T, NV, false>(a, clear, threads, st);
 }
 
 // CTAs worth giving to clearing.
@@ -277,8 +292,7 @@ unsigned clear_ctas(const Clear& c) {
 }
 
 // Vector rows: up to four vectors a thread (32768 bf16 or 16384 fp32 columns,
-// 20480 or 10240 with factors).  The CTAs are as many as the SMs hold at once,
-// each over rows in turn; few rows get extra CTAs for clearing.
+// 20480 or 10240 with factors).
 template <typename T>
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
   const int64_t nvec = a.K / Vec<T>::N;
@@ -289,13 +303,10 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
     // 768 threads reach, else four from 512 vectors on
     const int nv = nvec <= 256 ? 1 : nvec <= (a.f ? 2 * 768 : 512) ? 2 : 4;
     const int threads = (int)((nvec + nv - 1) / nv + 31) / 32 * 32;
-    const int64_t most = (int64_t)sm_count() * (2048 / threads);
-    unsigned ctas = (unsigned)(a.R < most ? a.R : most);
-    if (ctas < clear) ctas = clear;
     switch (nv) {
-      case 1: rows_go<T, 1>(a, ctas, threads, st); break;
-      case 2: rows_go<T, 2>(a, ctas, threads, st); break;
-      default: rows_go<T, 4>(a, ctas, threads, st); break;
+      case 1: rows_go<T, 1>(a, clear, threads, st); break;
+      case 2: rows_go<T, 2>(a, clear, threads, st); break;
+      default: rows_go<T, 4>(a, clear, threads, st); break;
     }
   } else {
     rows_any_kernel<T><<<(unsigned)(a.R > clear ? a.R : clear), kThreads, 0, st>>>(a);
