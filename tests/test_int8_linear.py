@@ -497,3 +497,18 @@ def test_offsets_past_32_bits(R, O, I):
     u, du = products(X, A)
     g = dY[:, outs].double()
     close(dB[outs], c * g.T @ u, c * (rel * g.abs().T @ u.abs() + g.abs().T @ du) * 1.001)
+
+
+@pytest.mark.parametrize("O,I", [(3, 7), (5, 8), (700, 4100), (4096, 1028), (131072, 32771), (131072, 32772)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_dequantize_is_exact(O, I, shift):
+    """One product a weight, also past 2^32 weights and into an unaligned output (the rows at either end)."""
+    codes = torch.randint(-127, 128, (O, q.qlora_int8_pitch(I)), dtype=torch.int8, device="cuda", generator=gen(1))
+    scale = torch.rand(O, device="cuda", generator=gen(2))
+    w = q.QuantizedWeight(q.FMT_INT8, O, I, I, 0, 8, codes, scale=scale)
+    buf = torch.full((O * I + 9,), 7.0, device="cuda")
+    q.qlora_dequantize(w, out=buf[shift:shift + O * I].view(O, I))
+    got = buf[shift:shift + O * I].view(O, I)
+    rows = torch.unique(torch.cat([torch.arange(min(O, 700)), torch.arange(max(0, O - 700), O)])).cuda()
+    assert torch.equal(got[rows], codes[rows, :I].float() * scale[rows, None])
+    assert bool((buf[:shift] == 7).all()) and bool((buf[shift + O * I:] == 7).all())
