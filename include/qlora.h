@@ -428,8 +428,8 @@ size_t qlora_linear_workspace_bytes(const qlora_weight* w, int64_t R, int32_t r,
  * type of Y; U uses the unquantized X.  `compute` is the type of X and Y.  A
  * token that holds a NaN or Inf gives a row of NaN; other tokens do not see
  * it.  U (and, in the backward, V, dA and dB) use all 24 bits of the fp32
- * factors (in bf16 mode split into three bf16 parts, or multiplied in fp32),
- * and so does the adapter's term in Y and dX.
+ * factors and of fp32 activations (split into three bf16 parts, or multiplied
+ * in fp32), and so does the adapter's term in Y and dX.
  * Requires codes on a 16-byte boundary, 1 <= O, I <= 131072 (above which the
  * 32-bit sum could overflow: QLORA_ERR_UNSUPPORTED) and R <= 2^28.
  */

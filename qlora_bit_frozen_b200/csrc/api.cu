@@ -253,13 +253,13 @@ BwdLayout bwd_layout(const qlora_weight* w, int64_t R, int32_t r, int32_t comput
   return L;
 }
 
-// INT8 weights: the status header (cleared by the first kernel of a call), U and V, the parts of the factors and of U and V and the partial
-// sums of the tensor-core side products (or, for activations that those do not
-// take, the scratch of the fp32 ones), then the quantized rows and the
+// INT8 weights: the status header (cleared by the first kernel of a call), U and V,
+// copies of X and dY that the tensor-core side products need, the parts of the
+// factors and of U and V, the products' partial sums, the scratch of the fp32 ones
+// (for activations that the others do not take), then the quantized rows and the
 // product's own.
 struct Int8Layout {
-  size_t u = 0, v = 0, fA = 0, fB = 0, fU = 0, fV = 0, part = 0, red = 0,
-         rows = 0, total = 0;
+  size_t u = 0, v = 0, cX = 0, cY = 0, fA = 0, fB = 0, fU = 0, fV = 0, part = 0, red = 0, rows = 0, total = 0;
 };
 
 Int8Layout int8_layout(const qlora_weight* w, int64_t R, int32_t r, bool bwd, int32_t compute) {
@@ -272,15 +272,20 @@ Int8Layout int8_layout(const qlora_weight* w, int64_t R, int32_t r, bool bwd, in
   };
   L.u = take((size_t)R * r * 4);
   if (bwd) L.v = take((size_t)R * r * 4);
-  if (compute == QLORA_COMPUTE_BF16) {
-    L.fA = take(side_parts_bytes(w->I, r));
-    if (bwd) {
-      L.fB = take(side_parts_bytes(w->O, r));
-      L.fU = take(side_parts_bytes(R, r));
-      L.fV = take(side_parts_bytes(R, r));
-    }
-    L.part = take(side_part_ws(r));
+  const bool bf16 = compute == QLORA_COMPUTE_BF16;
+  const bool copyX = side_copies(bf16, R, w->I, r), copyY = bwd && side_copies(bf16, R, w->O, r);
+  const int parts = bf16 ? 1 : 3;
+  if (copyX) L.cX = take(side_copy_bytes(bf16, R, w->I));
+  if (copyY) L.cY = take(side_copy_bytes(bf16, R, w->O));
+  if (bf16 || copyX) {
+    L.fA = take(side_parts_bytes(copyX ? parts * side_ld(w->I) : w->I, r));
+    if (bwd) L.fV = take(side_parts_bytes(copyX ? parts * R : R, r));
   }
+  if (bwd && (bf16 || copyY)) {
+    L.fB = take(side_parts_bytes(copyY ? parts * side_ld(w->O) : w->O, r));
+    L.fU = take(side_parts_bytes(copyY ? parts * R : R, r));
+  }
+  if (bf16 || copyX || copyY) L.part = take(side_part_ws(r));
   if (bwd) {
     const size_t a = coldot_ws(R, w->I, r), b = coldot_ws(R, w->O, r);
     L.red = take(a > b ? a : b);
@@ -325,11 +330,14 @@ cudaError_t int8_fwd(const qlora_weight* w, const void* X, int64_t R, const floa
     e = launch_int8_few(c, f, at(L.rows), header, s);
   } else {
     e = launch_int8_rows(c, at(L.rows), header, s);
-    if (e == cudaSuccess && bf16 && side_takes(X, R, w->I)) {
+    const SideMatrix m = side_matrix(X, bf16, R, w->I, r, at(L.cX));
+    if (e == cudaSuccess && m.parts) {
       uint16_t* fA = (uint16_t*)at(L.fA);
-      const SideFactor f = {A, fA, w->I, false};
-      const SideProduct p = {X, w->I, fA, U, nullptr, false, 1.0f};
-      e = launch_side_split(&f, 1, r, s);
+      const SideFactor f = side_factor_of_columns(A, fA, false, m);
+      const SideProduct p = {m, fA, U, nullptr, false, 1.0f};
+      const SideCopy copy = {X, m};
+      e = launch_side_copy(&copy, m.P != X, bf16, R, s);
+      if (e == cudaSuccess) e = launch_side_split(&f, 1, r, s);
       if (e == cudaSuccess)
         e = launch_side(&p, 1, false, R, r, at(L.part), (uint32_t*)ws, s);
     } else if (e == cudaSuccess) {
@@ -355,14 +363,15 @@ cudaError_t int8_bwd(const qlora_weight* w, const void* X, const void* dY, int64
   const Int8Clear header = {ws, kWsZeroed};
   const Int8Call c = int8_call(w, true, bf16, R, dY, V, A, r, sc, dX);
   const bool want_v = dX || dA, new_u = dB && !U_in;
-  // which matrix the tensor-core side products take (else the fp32 ones do)
-  const bool sX = bf16 && side_takes(X, R, w->I), sY = bf16 && side_takes(dY, R, w->O);
+  // what the tensor-core side products take (else the fp32 ones do)
+  const SideMatrix mX = side_matrix(X, bf16, R, w->I, r, at(L.cX)), mY = side_matrix(dY, bf16, R, w->O, r, at(L.cY));
+  const bool sX = mX.parts != 0, sY = mY.parts != 0;
   // dA = s V^T X, dB = s dY^T U: from the parts of V and U, or from V and U
   auto columns = [&]() {
     SideProduct p[2];
     int n = 0;
-    if (dA && sX) p[n++] = {X, w->I, fV, dA, nullptr, true, sc};
-    if (dB && sY) p[n++] = {dY, w->O, fU, dB, nullptr, false, sc};
+    if (dA && sX) p[n++] = {mX, fV, dA, nullptr, true, sc};
+    if (dB && sY) p[n++] = {mY, fU, dB, nullptr, false, sc};
     cudaError_t e = cudaSuccess;
     if (n) e = launch_side(p, n, true, R, r, at(L.part), (uint32_t*)ws, s);
     if (e == cudaSuccess && dA && !sX) e = launch_coldot(X, bf16, R, w->I, V, r, sc, false, dA, at(L.red), s);
@@ -402,25 +411,30 @@ cudaError_t int8_bwd(const qlora_weight* w, const void* X, const void* dY, int64
     return e;
   }
   e = dX ? launch_int8_rows(c, at(L.rows), header, s) : cudaMemsetAsync(ws, 0, kWsZeroed, s);
-  // the parts of the factors, then V and U (with their own parts where a
-  // tensor-core product makes them, else split after it)
+  // the copies, the parts of the factors, then V and U (with their own parts where
+  // a tensor-core product makes them as they are wanted, else split after it)
+  SideCopy copy[2];
   SideFactor f[2], late[2];
   SideProduct p[2];
-  int nf = 0, np = 0, nlate = 0;
+  int nc = 0, nf = 0, np = 0, nlate = 0;
   const bool parts_v = dA && sX, parts_u = dB && sY;
+  if (sX && mX.P != X && (dA || new_u)) copy[nc++] = {X, mX};
+  if (sY && mY.P != dY && (dB || want_v)) copy[nc++] = {dY, mY};
+  const bool own_v = parts_v && want_v && sY && mX.parts == 1, own_u = parts_u && new_u && sX && mY.parts == 1;
   if (want_v && sY) {
-    f[nf++] = {B, fB, w->O, true};
-    p[np++] = {dY, w->O, fB, V, parts_v ? fV : nullptr, false, 1.0f};
-  } else if (parts_v) {
-    late[nlate++] = {V, fV, R, true};
+    f[nf++] = side_factor_of_columns(B, fB, true, mY);
+    p[np++] = {mY, fB, V, own_v ? fV : nullptr, false, 1.0f};
   }
+  if (parts_v && !own_v) late[nlate++] = side_factor_of_rows(V, fV, R, mX);
   if (new_u && sX) {
-    f[nf++] = {A, fA, w->I, false};
-    p[np++] = {X, w->I, fA, Uw, parts_u ? fU : nullptr, false, 1.0f};
-  } else if (parts_u) {
-    if (new_u) late[nlate++] = {U, fU, R, true};
-    else f[nf++] = {U, fU, R, true};
+    f[nf++] = side_factor_of_columns(A, fA, false, mX);
+    p[np++] = {mX, fA, Uw, own_u ? fU : nullptr, false, 1.0f};
   }
+  if (parts_u && !own_u) {
+    if (new_u || nf == 2) late[nlate++] = side_factor_of_rows(U, fU, R, mY);
+    else f[nf++] = side_factor_of_rows(U, fU, R, mY);
+  }
+  if (e == cudaSuccess) e = launch_side_copy(copy, nc, bf16, R, s);
   if (e == cudaSuccess) e = launch_side_split(f, nf, r, s);
   if (e == cudaSuccess && np) e = launch_side(p, np, false, R, r, at(L.part), (uint32_t*)ws, s);
   Int8Dot d[2];

@@ -98,27 +98,53 @@ size_t int8_tc_zeroed(bool dx, int64_t R, int64_t O, int64_t I, int32_t r);
 cudaError_t launch_int8_tc(const Int8Call& c, const int8_t* xq, const float* xs, const Int8Few* few, void* ws,
                            uint32_t* hdr, cudaStream_t st);
 
-// int8_side.cu: the adapter's thin products over bf16 matrices P [R x N].
+// int8_side.cu: the adapter's thin products over bf16 matrices: P [R x N] itself
+// or a copy of it in bf16 parts (one of bf16 values whose rows do not start on 16
+// bytes, three of fp32 values), a row's parts one after the other, `pitch` columns
+// each.  parts 0: the fp32 kernels take P.
+struct SideMatrix {
+  const void* P;   // [R x parts * pitch]
+  int64_t N, pitch;
+  int parts;
+};
+bool side_takes(const void* P, int64_t R, int64_t N);
+// Whether P [R x N], which side_takes refuses for its type or N, is worth a copy.
+bool side_copies(bool bf16, int64_t R, int64_t N, int32_t r);
+size_t side_copy_bytes(bool bf16, int64_t R, int64_t N);
+SideMatrix side_matrix(const void* P, bool bf16, int64_t R, int64_t N, int32_t r, void* copy);
+struct SideCopy {
+  const void* src;
+  SideMatrix m;  // m.P: the copy
+};
+cudaError_t launch_side_copy(const SideCopy* c, int count, bool bf16, int64_t R, cudaStream_t st);
 // Parts: an fp32 factor [n x r] or [r x n] as three bf16 parts, [3][side_np(r)]
-// rows of side_ld(n), zeros past n.
+// rows of side_ld(len): entry e is the factor's entry e % wrap (row products: once
+// for each part of the matrix's rows) or, with wrap 0, e / div (column products),
+// zero past n.
 int side_np(int32_t r);
 int64_t side_ld(int64_t n);
-size_t side_parts_bytes(int64_t n, int32_t r);
+size_t side_parts_bytes(int64_t len, int32_t r);
 size_t side_part_ws(int32_t r);     // scratch of one launch
-bool side_takes(const void* P, int64_t R, int64_t N);
 struct SideFactor {
   const float* src;
   uint16_t* parts;
   int64_t n;
   bool kr;  // [n x r]
+  int64_t len, wrap;
+  int div;
 };
+inline SideFactor side_factor_of_columns(const float* src, uint16_t* parts, bool kr, const SideMatrix& m) {
+  return {src, parts, m.N, kr, m.parts * m.pitch, m.pitch, 1};
+}
+inline SideFactor side_factor_of_rows(const float* src, uint16_t* parts, int64_t R, const SideMatrix& m) {
+  return {src, parts, R, true, m.parts * R, 0, m.parts};
+}
 cudaError_t launch_side_split(const SideFactor* f, int count, int32_t r, cudaStream_t st);
 struct SideProduct {
-  const void* P;
-  int64_t N;
-  const uint16_t* factor;  // parts over N (row products) or over R (column products)
+  SideMatrix m;
+  const uint16_t* factor;  // its parts over m's columns (row products) or rows (column products)
   float* out;              // s times the product: [R x r]; [N x r] or, transposed, [r x N]
-  uint16_t* parts;         // nullable: its own parts (row products)
+  uint16_t* parts;         // nullable: its own parts (row products), [3][NP][side_ld(R)]
   bool transposed;
   float s;
 };

@@ -13,6 +13,11 @@
 // warps drain it into fp32 registers while the other one fills.  Measured error
 // 2e-7 of the result where one running sum over 8192 tokens had 3e-6 to 9e-6.
 //
+// Matrices that TMA does not take as they are (fp32 values, or rows that do not
+// start on 16 bytes) are copied in bf16 parts first, where that pays: the parts'
+// products meet in the same sums.  The backward of 8192 tokens of 4096 x 4096 in
+// fp32 at rank 64: 465 us, by fp32 FMAs 3250.
+
 // Each product's chunks, tile after tile, are dealt out in equal runs over the
 // SMs; the partial sums of a tile that several CTAs share are added up in CTA
 // order by a second, small launch.  (By the last CTA of a tile, that held up its
@@ -376,12 +381,13 @@ __global__ void __launch_bounds__(128) side_sum_kernel(const SideArgs p) {
   side_write<NP, 8>(o, p.r, tile * 128 + threadIdx.x, j0, acc);
 }
 
-// The three bf16 parts of up to two fp32 factors, [3][NP][ld], zeros past n
-// entries of a row: F(k, j) = src[k r + j] (kr) or src[j n + k].
+// The three bf16 parts of up to two fp32 factors, [3][NP][ld], zeros past a
+// row's entries: F(k, j) = src[k r + j] (kr) or src[j n + k].
 struct SplitJob {
   const float* src;
   uint16_t* dst;
-  int64_t n, ld;
+  int64_t n, len, ld;
+  uint32_t wrap, div;
   int32_t kr, blocks;
 };
 struct SplitArgs {
@@ -403,11 +409,13 @@ __global__ void __launch_bounds__(256) split_kernel(const SplitArgs a) {
   const int64_t k0 = (int64_t)(block / groups) * 64;
   const int j0 = block % groups * kSplitRows, rows = min(kSplitRows, a.r - j0);
 #pragma unroll
-  for (int e = threadIdx.x; e < 64 * kSplitRows; e += 256) {
-    const int j = b.kr ? e % kSplitRows : e >> 6, k = b.kr ? e / kSplitRows : e & 63;
+  for (int i = threadIdx.x; i < 64 * kSplitRows; i += 256) {
+    const int j = b.kr ? i % kSplitRows : i >> 6, k = b.kr ? i / kSplitRows : i & 63;
+    const uint32_t e = (uint32_t)(k0 + k);
+    const int64_t at = b.wrap ? e % b.wrap : e / b.div;
     float v = 0.0f;
-    if (j < rows && k0 + k < b.n)
-      v = __ldg(b.src + (b.kr ? (k0 + k) * a.r + j0 + j : (int64_t)(j0 + j) * b.n + k0 + k));
+    if (j < rows && k0 + k < b.len && at < b.n)
+      v = __ldg(b.src + (b.kr ? at * a.r + j0 + j : (int64_t)(j0 + j) * b.n + at));
     tile[j][k] = v;
   }
   __syncthreads();
@@ -421,6 +429,48 @@ __global__ void __launch_bounds__(256) split_kernel(const SplitArgs a) {
       const __nv_bfloat16 h = __float2bfloat16_rn(v);
       b.dst[((int64_t)q * a.NP + j0 + j) * b.ld + k0 + k] = __bfloat16_as_ushort(h);
       v -= __bfloat162float(h);
+    }
+  }
+}
+
+// Copies of up to two matrices [R x N] in bf16 parts: a thread takes eight
+// columns of a row.  Zeros past N.
+struct CopyArgs {
+  const void* src[2];
+  uint4* dst[2];
+  int64_t N[2], pitch[2];
+  int64_t R;
+};
+template <typename T>
+__global__ void __launch_bounds__(256) side_copy_kernel(const CopyArgs a) {
+  constexpr int kParts = sizeof(T) == 2 ? 1 : 3;
+  const int job = blockIdx.y;
+  const int64_t N = job ? a.N[1] : a.N[0], per = (job ? a.pitch[1] : a.pitch[0]) / 8, count = a.R * per;
+  const T* src = (const T*)(job ? a.src[1] : a.src[0]);
+  uint4* dst = job ? a.dst[1] : a.dst[0];
+  const bool wide = sizeof(T) == 4 && N % 4 == 0 && (uintptr_t)src % 16 == 0;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < count; e += (int64_t)gridDim.x * 256) {
+    const int64_t row = count <= UINT32_MAX ? (int64_t)((uint32_t)e / (uint32_t)per) : e / per, k = 8 * (e - row * per);
+    const T* p = src + row * N + k;
+    float v[8];
+    if (wide && k + 8 <= N) {
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(p)), y = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = k + i < N ? to_f32(p[i]) : 0.0f;
+    }
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) {
+      uint32_t w[4] = {};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(v[i]);
+        w[i / 2] |= (uint32_t)__bfloat16_as_ushort(h) << (16 * (i & 1));
+        v[i] -= __bfloat162float(h);
+      }
+      dst[(row * kParts + q) * per + k / 8] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -455,12 +505,49 @@ cudaError_t side_rank(const CUtensorMap* t, const SideArgs& a, int NP, cudaStrea
 
 int side_np(int32_t r) { return r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : 64; }
 int64_t side_ld(int64_t n) { return up(n, 8) * 8; }
-size_t side_parts_bytes(int64_t n, int32_t r) {
-  return align_up((size_t)3 * side_np(r) * (size_t)side_ld(n) * 2, 256);
+size_t side_parts_bytes(int64_t len, int32_t r) {
+  return align_up((size_t)3 * side_np(r) * (size_t)side_ld(len) * 2, 256);
 }
 size_t side_part_ws(int32_t r) { return (size_t)sm_count() * 4 * side_np(r) * 128 * 4; }
 bool side_takes(const void* P, int64_t R, int64_t N) {
   return R > 0 && R <= INT32_MAX - 256 && N % 8 == 0 && (uintptr_t)P % 16 == 0;
+}
+
+// The copy costs its bytes (16 a value in fp32, with what the product reads, 6 in
+// bf16), the fp32 kernels their products (eight columns of the factor at least).
+// 8192 x 4096 in fp32 at rank 16 (2^29): U in 102 us with the copy, 141 by FMAs;
+// at rank 8 100 and 70.  8191 x 4097 in bf16 at rank 8 (2^28): 48 and 110.
+bool side_copies(bool bf16, int64_t R, int64_t N, int32_t r) {
+  if (R <= 256 || (bf16 && N % 8 == 0)) return false;
+  return (double)R * (double)N * ((r + 7) / 8 * 8) >= (bf16 ? 134217728.0 : 536870912.0);
+}
+size_t side_copy_bytes(bool bf16, int64_t R, int64_t N) {
+  return align_up((size_t)R * (bf16 ? 1 : 3) * (size_t)side_ld(N) * 2, 256);
+}
+SideMatrix side_matrix(const void* P, bool bf16, int64_t R, int64_t N, int32_t r, void* copy) {
+  if (bf16 && side_takes(P, R, N)) return {P, N, N, 1};
+  if (side_copies(bf16, R, N, r)) return {copy, N, side_ld(N), bf16 ? 1 : 3};
+  return {P, N, N, 0};
+}
+
+cudaError_t launch_side_copy(const SideCopy* c, int count, bool bf16, int64_t R, cudaStream_t st) {
+  if (count == 0) return cudaSuccess;
+  CopyArgs a = {};
+  a.R = R;
+  int64_t most = 0;
+  for (int i = 0; i < count; ++i) {
+    a.src[i] = c[i].src;
+    a.dst[i] = (uint4*)c[i].m.P;
+    a.N[i] = c[i].m.N;
+    a.pitch[i] = c[i].m.pitch;
+    const int64_t blocks = up(R * c[i].m.pitch / 8, 256);
+    if (blocks > most) most = blocks;
+  }
+  const dim3 grid((unsigned)(most < sm_count() * 16 ? most : sm_count() * 16), (unsigned)count);
+  if (bf16) side_copy_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
+  else side_copy_kernel<float><<<grid, 256, 0, st>>>(a);
+  count_launch();
+  return cudaGetLastError();
 }
 
 cudaError_t launch_side_split(const SideFactor* f, int count, int32_t r, cudaStream_t st) {
@@ -473,7 +560,10 @@ cudaError_t launch_side_split(const SideFactor* f, int count, int32_t r, cudaStr
     b.src = f[i].src;
     b.dst = f[i].parts;
     b.n = f[i].n;
-    b.ld = side_ld(f[i].n);
+    b.len = f[i].len;
+    b.ld = side_ld(f[i].len);
+    b.wrap = (uint32_t)f[i].wrap;
+    b.div = (uint32_t)f[i].div;
     b.kr = f[i].kr ? 1 : 0;
     b.blocks = (int)(up(b.ld, 64) * up(r, kSplitRows));
     blocks += b.blocks;
@@ -490,7 +580,10 @@ cudaError_t launch_side(const SideProduct* f, int count, bool columns, int64_t R
   CUtensorMap t[4];
   SideArgs a = {};
   for (int i = 0; i < count; ++i) {
-    const int64_t N = f[i].N, K = columns ? R : N, M = columns ? N : R;
+    // P as [R x parts pitch] (rows: one output row each) or [parts R x pitch]
+    const SideMatrix& m = f[i].m;
+    const int64_t cols = columns ? m.pitch : m.parts * m.pitch, rows = columns ? m.parts * R : R;
+    const int64_t K = columns ? rows : cols, M = columns ? m.N : R;
     SideOut& o = a.job[i];
     o.out = f[i].out;
     o.parts = f[i].parts;
@@ -503,8 +596,8 @@ cudaError_t launch_side(const SideProduct* f, int count, bool columns, int64_t R
     a.tiles[i] = up(M, 128);
     a.units[i] = a.tiles[i] * o.chunks;
     const int64_t ld = side_ld(K);
-    if (!make_map_2d(&t[2 * i], f[i].P, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)N, (uint64_t)R,
-                     (uint64_t)N * 2, 64, columns ? 64 : 128) ||
+    if (!make_map_2d(&t[2 * i], m.P, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)cols, (uint64_t)rows,
+                     (uint64_t)cols * 2, 64, columns ? 64 : 128) ||
         !make_map_2d(&t[2 * i + 1], f[i].factor, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)ld,
                      (uint64_t)3 * NP, (uint64_t)ld * 2, 64, (uint32_t)side_n(NP)))
       return cudaErrorInvalidValue;

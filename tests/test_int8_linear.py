@@ -512,3 +512,60 @@ def test_dequantize_is_exact(O, I, shift):
     rows = torch.unique(torch.cat([torch.arange(min(O, 700)), torch.arange(max(0, O - 700), O)])).cuda()
     assert torch.equal(got[rows], codes[rows, :I].float() * scale[rows, None])
     assert bool((buf[:shift] == 7).all()) and bool((buf[shift + O * I:] == 7).all())
+
+
+# fp32 activations, and bf16 rows that do not start on 16 bytes, in numbers that go to the tensor cores in parts
+COPIES = [(2200, 4096, 4100, 64, F32), (2200, 264, 4100, 64, F32), (2200, 4100, 264, 64, F32), (9000, 4100, 1030, 16, F32),
+          (1200, 2047, 2050, 64, BF), (1200, 2048, 2047, 64, BF), (1200, 2047, 2048, 64, BF), (9001, 1001, 1003, 16, BF)]
+
+
+@pytest.mark.parametrize("R,O,I,r,dtype", COPIES)
+def test_activations_in_parts(R, O, I, r, dtype):
+    test_forward_and_backward(R, O, I, r, dtype)
+
+
+@pytest.mark.parametrize("R,O,I,r,dtype", COPIES)
+def test_activations_in_parts_keep_to_the_workspace_and_to_each_other(R, O, I, r, dtype):
+    """The stated workspace is enough, on any content; each gradient has the same bits alone."""
+    W, X, dY, A, B = make(R, O, I, r, dtype)
+    w, _, _ = weight(W)
+    Y, Ug = q.qlora_linear_fwd(w, X, A, B, 16.0)
+    full = q.qlora_linear_bwd(w, X, dY, A, B, 16.0)
+    compute = q.COMPUTE_BF16 if dtype == BF else q.COMPUTE_FP32
+    for fill in (0, 255):
+        for op in (0, 1):
+            n = q.qlora_linear_workspace_bytes(w, R, r, op, compute)
+            buf = torch.full((n + 512,), fill, dtype=torch.uint8, device="cuda")
+            if op == 0:
+                got = q.qlora_linear_fwd(w, X, A, B, 16.0, ws=buf[:n])
+                assert torch.equal(got[0], Y) and torch.equal(got[1], Ug)
+            else:
+                got = q.qlora_linear_bwd(w, X, dY, A, B, 16.0, ws=buf[:n])
+                assert all(torch.equal(a, b) for a, b in zip(got, full))
+            assert bool((buf[n:] == fill).all())
+    for k in range(3):
+        part = q.qlora_linear_bwd(w, X, dY, A, B, 16.0, want_dx=k == 0, want_da=k == 1, want_db=k == 2)
+        assert torch.equal(part[k], full[k])
+
+
+@pytest.mark.parametrize("R,O,I,r,dtype", COPIES)
+def test_activations_in_parts_keep_all_bits(R, O, I, r, dtype):
+    """Sums of one term each: the activation's bits times a power of two come through (as in
+    test_adapter_keeps_all_bits)."""
+    W, X, dY, A, B = make(R, O, I, r, dtype)
+    w, _, _ = weight(torch.zeros_like(W))
+    rows = torch.arange(R, device="cuda")
+    at = rows * 37 % I
+    one = torch.zeros_like(X)
+    one[rows, at] = X[rows, at]
+    A = 2.0 ** (torch.arange(r * I, device="cuda") % 11 - 5).float().view(r, I)
+    _, Ug = q.qlora_linear_fwd(w, one, A, torch.zeros_like(B), float(r))
+    u = X[rows, at].double()[:, None] * A.double()[:, at].T
+    close(Ug, u, 2 * U * u.abs())
+    t = R - 1
+    one = torch.zeros_like(dY)
+    one[t] = dY[t]
+    Uin = 2.0 ** (torch.arange(R * r, device="cuda") % 7 - 3).float().view(R, r)
+    _, _, dB = q.qlora_linear_bwd(w, X, one, A, B, float(r), U=Uin)
+    ref = dY[t].double()[:, None] * Uin[t].double()[None, :]
+    close(dB, ref, 2 * U * ref.abs())
