@@ -377,7 +377,8 @@ qlora_status qlora_grad_norm(const qlora_tensor* tensors, int32_t count, float m
  * zero); a block whose maximum is below FLT_MIN gets codes of 0.  A NaN
  * gradient in a step that is not skipped makes its block of 256 states NaN.
  * tensors: HOST array (see qlora_grad_norm).  control (DEVICE, nullable):
- * gives scale, skip and t; when NULL, t >= 1 is the argument.  Requires
+ * gives scale, skip and t (t < 1, before the first qlora_grad_norm, changes
+ * nothing); when NULL, t >= 1 is the argument.  Requires
  * 0 <= beta < 1, eps > 0, finite lr and weight_decay >= 0.  In place; with
  * more tensors than fit one launch (about 500) it takes several.
  */

@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int lane = threadIdx.x & 31;
   float scale = 1.0f, step_size = a.step_size, inv_rbc2 = a.inv_rbc2;
   if (a.control) {
-    if (a.control->skip) {
+    if (a.control->skip || a.control->step < 1) {
       if (a.follows && threadIdx.x == 0) griddep_wait();
       return;
     }

@@ -368,3 +368,28 @@ def test_a_training_step_on_an_int8_base():
     assert all(torch.equal(a, w.codes) for a, (w, _, _) in zip(codes, layers))
     out = q.qlora_merge(*layers[0], alpha)
     assert bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_control_block_without_a_step_changes_nothing(bits):
+    T = arrays(SIZES, bits, seed=41)
+    before = snapshot(T)
+    q.qlora_adamw_step(T, control=q.step_control(), **HP)
+    for a, b in zip(before, snapshot(T)):
+        assert all(x is None or np.array_equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_norm_on_a_stream_of_its_own_keeps_its_workspace(bits):
+    """The workspace that a call allocates is not handed out while its stream still uses it."""
+    T = arrays([300_000] * 40, bits, seed=43)
+    want = q.qlora_grad_norm(T, 1.0, q.step_control()).clone()
+    side = torch.cuda.Stream()
+    out = [q.step_control() for _ in range(6)]
+    torch.cuda.synchronize()
+    for c in out:
+        q.qlora_grad_norm(T, 1.0, c, stream=side)
+        for _ in range(4):
+            torch.full((q.qlora_grad_norm_workspace_bytes(T),), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert all(torch.equal(c, want) for c in out)
