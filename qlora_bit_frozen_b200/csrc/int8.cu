@@ -156,7 +156,9 @@ __device__ __forceinline__ float top_of(uint4 v, float top) {
 // codes, so the row is read once, and the next row is on its way while this one
 // is reduced.  The column factors of those vectors stay in registers over all
 // the rows that the CTA takes (from shared memory they cost more than a third
-// of the row's time).
+// of the row's time).  16384 x 5120 in bf16 47 us (252 MB, 5.4 TB/s); 8192 x
+// 12288 with factors 74 us (302 MB, 4.1 TB/s): instruction issue, half of all
+// slots, and a barrier a row hold it below HBM's rate there.
 template <int NV, bool FACTOR>
 constexpr int rows_threads() {  // most threads: 64, 85 or 102 registers each
   return !FACTOR || NV == 1 ? 1024 : NV == 2 ? 768 : 640;
@@ -237,7 +239,49 @@ __global__ void __launch_bounds__(rows_threads<NV, FACTOR>()) rows_kernel(const 
   }
 }
 
-// Any other row: one CTA per row, read twice.
+// Other rows of up to 512 columns: a warp takes a row, 16 values a lane in
+// registers.  8747 x 171 in fp32 8 us, a CTA a row 16.  (For longer rows a CTA that
+// keeps 16 values a thread took twice the time of reading the row again.)
+constexpr int kAny = 16;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) rows_short_kernel(const RowsArgs a) {
+  clear_part(a.clear, blockIdx.x, gridDim.x);
+  const int first = threadIdx.x & 31, step = 32;
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (row >= a.R) return;
+  const T* p = (const T*)a.P + row * a.K;
+  const int K = (int)a.K, end = (int)int8_pitch(a.K);
+  uint64_t x[kAny / 2];
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kAny; i += 2) {
+    float v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = first + (i + h) * step;
+      v[h] = k < K ? to_f32(p[k]) : 0.0f;
+      if (a.f && k < K) v[h] = __fmul_rn(v[h], __ldg(a.f + k));
+    }
+    x[i / 2] = pack2(v[0], v[1]);
+    top = top3(top, v[0], v[1]);
+  }
+  const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+  const float s = row_scale(bits);
+  if (first == 0) {
+    a.scale[row] = s;
+    if (a.bad && bits >= 0x7f800000u) *a.bad = 1;
+  }
+  uint32_t c[kAny / 4];
+  codes_of<kAny>(x, s, reciprocal(s), c);
+  int8_t* q = a.codes + row * a.pitch;
+#pragma unroll
+  for (int i = 0; i < kAny; ++i) {
+    const int k = first + i * step;
+    if (k < end) q[k] = (int8_t)(k < K ? c[i / 4] >> (8 * (i & 3)) : 0);
+  }
+}
+
+// Longer ones: one CTA per row, read twice.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rows_any_kernel(const RowsArgs a) {
   __shared__ uint32_t buf[32];
@@ -308,6 +352,9 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) {
       case 2: rows_go<T, 2>(a, clear, threads, st); break;
       default: rows_go<T, 4>(a, clear, threads, st); break;
     }
+  } else if (a.K <= 32 * kAny) {
+    const int64_t ctas = (a.R + kThreads / 32 - 1) / (kThreads / 32);
+    rows_short_kernel<T><<<(unsigned)(ctas > clear ? ctas : clear), kThreads, 0, st>>>(a);
   } else {
     rows_any_kernel<T><<<(unsigned)(a.R > clear ? a.R : clear), kThreads, 0, st>>>(a);
   }
@@ -540,9 +587,10 @@ __device__ __forceinline__ void few_tokens(const FewArgs& a, const FewJob& job, 
 
 // One token a CTA: latency is what bounds it, a pass over a row beside eight
 // factor rows (or columns), a block reduction, and a second pass for the codes.
-// Four tokens a CTA (fp32 or unaligned activations by themselves): a quarter of
-// the factor's reads from L2, which are what bounds that.  The last CTAs of the
-// grid clear.
+// One token of 4096 columns, rank 8: 4.6 us.  Four tokens a CTA (fp32 or
+// unaligned activations by themselves): a quarter of the factor's reads from L2,
+// which are what bounds that (747 tokens of 13568 columns in fp32: 28 us).  The
+// last CTAs of the grid clear.
 template <typename T, bool WIDE, int TOK>
 __global__ void __launch_bounds__(512) few_kernel(const FewArgs a) {
   __shared__ float sums[16][8 * TOK];
