@@ -360,7 +360,7 @@ class OptimTensors:
 
     The tensors are kept and used in place: keep writing gradients into the
     same storage (or build a new object for new tensors).  No two parameters
-    or states may overlap."""
+    or states may overlap, nor a gradient with one of them."""
 
     def __init__(self, grads: Sequence[torch.Tensor], params: Optional[Sequence[torch.Tensor]] = None,
                  m: Optional[Sequence[torch.Tensor]] = None, v: Optional[Sequence[torch.Tensor]] = None,
@@ -414,13 +414,19 @@ class OptimTensors:
 
     def _refuse_overlap(self):
         spans = []
-        for name in ("params", "m", "v", "m_scale", "v_scale"):
+        for name in ("params", "m", "v", "m_scale", "v_scale", "grads"):
             for x in getattr(self, name) or ():
                 if x.numel() > 0:
-                    spans.append((x.data_ptr(), x.data_ptr() + x.numel() * x.element_size()))
+                    spans.append((x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(), name != "grads"))
         spans.sort()
-        if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
-            raise ValueError("OptimTensors: parameters or states overlap (a tensor listed twice?)")
+        written = read = 0  # where what came before ends
+        for start, end, writes in spans:
+            if start < written or (writes and start < read):
+                raise ValueError("OptimTensors: parameters or states overlap (a tensor listed twice?)")
+            if writes:
+                written = max(written, end)
+            else:
+                read = max(read, end)
 
     @classmethod
     def with_states(cls, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],

@@ -569,3 +569,24 @@ def test_activations_in_parts_keep_all_bits(R, O, I, r, dtype):
     _, _, dB = q.qlora_linear_bwd(w, X, one, A, B, float(r), U=Uin)
     ref = dY[t].double()[:, None] * Uin[t].double()[None, :]
     close(dB, ref, 2 * U * ref.abs())
+
+
+def test_two_graphs_share_a_workspace():
+    """Each captured call leaves nothing in the workspace that the other's replay could meet."""
+    cases, ws = [], q.workspace(1 << 27)
+    for R, O, I, r, dtype in ((300, 1024, 768, 16, BF), (2100, 640, 520, 40, BF), (5, 1024, 1030, 8, F32)):
+        W, X, dY, A, B = make(R, O, I, r, dtype)
+        w, _, _ = weight(W)
+        want = q.qlora_linear_fwd(w, X, A, B, 16.0) + q.qlora_linear_bwd(w, X, dY, A, B, 16.0)
+        got = [torch.zeros_like(x) for x in want]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            q.qlora_linear_fwd(w, X, A, B, 16.0, Y=got[0], U_out=got[1], ws=ws)
+            q.qlora_linear_bwd(w, X, dY, A, B, 16.0, dX=got[2], dA=got[3], dB=got[4], ws=ws)
+        cases.append((graph, got, want, (w, X, dY, A, B)))
+    for k in (0, 1, 2, 1, 0, 2, 2, 0):
+        graph, got, want, _ = cases[k]
+        for x in got:
+            x.fill_(7)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -393,3 +393,13 @@ def test_a_norm_on_a_stream_of_its_own_keeps_its_workspace(bits):
             torch.full((q.qlora_grad_norm_workspace_bytes(T),), 255, dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     assert all(torch.equal(c, want) for c in out)
+
+
+def test_what_is_written_overlaps_nothing():
+    buf = torch.zeros(4096, device="cuda")
+    z = lambda n: torch.zeros(n, device="cuda")  # noqa: E731
+    for p, g in ((buf[:512], buf[256:768]), (buf[256:768], buf[:512]), (buf[:512], buf[:512]), (buf[100:200], buf[:512])):
+        with pytest.raises(ValueError):
+            q.OptimTensors([g], [p], [z(p.numel())], [z(p.numel())])
+    # beside each other, and one gradient for two parameters, are fine
+    q.OptimTensors([buf[512:1024]] * 2, [buf[:512], buf[1024:1536]], [z(512), z(512)], [z(512), z(512)])
