@@ -966,14 +966,15 @@ struct Plan {
 // of one SM (512 cycles: what the products of a 128 x 256 half tile take, and
 // also what the 32 KB of a 128 x 128 stream step take from L2).  The pair
 // kernel pays whole rounds of tiles over the CTA pairs, with the adapter's steps,
-// and the last tile's epilogue; the stream kernel pays whole rounds of tiles over
-// the SMs, or, with tiles shared, an equal run of steps and the meeting of the
-// partial sums, which grows with the token tile.  A tile takes no less than its
-// epilogue: about nine steps for the pair kernel's, and for the stream kernel's as
-// many as its adapter term reads from shared memory (nine at 128 tokens and rank
-// 8).  On both sides of the choice: 777 tokens of 2048 x 1024 at rank 8, stream
-// 11.6 us, pair 13; 79 tokens of 4084 x 2704 at rank 64, stream 41, pair 18 + 4
-// for packing its factors.
+// the last tile's epilogue and the packing of its factors (8); the stream kernel
+// pays whole rounds of tiles over the SMs and the last one's epilogue, or, with
+// tiles shared, an equal run of steps and the meeting of the partial sums, which
+// grows with the token tile.  A tile takes no less than its epilogue: about nine
+// steps for the pair kernel's, and for the stream kernel's as many as its adapter
+// term reads from shared memory (nine at 128 tokens and rank 8).  Whole forward
+// calls on both sides of the choice, stream and pair: 200 tokens of 4096 x 1024 13.7
+// and 16.2 us at rank 8, 25.8 and 19.4 at rank 32; of 4096 x 4096 23.5 and 26.1, 43.0
+// and 37.6; 800 tokens of 4096 x 1024 24.4 and 19.4 at rank 8.
 Plan plan_for(int64_t R, int64_t N, int64_t K, int r) {
   const int64_t sms = sm_count(), KB = up(K, kBK), RT = rank_pad(r);
   Plan p;
@@ -981,9 +982,9 @@ Plan plan_for(int64_t R, int64_t N, int64_t K, int r) {
   const int64_t pair_tiles = up(R, 256) * up(N, 256), tiles = up(R, p.bn) * up(N, 128);
   const int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
   const int64_t pair_tile = KB + adapter_steps(r), pair_least = 9;
-  const int64_t cost_pair = up(pair_tiles, pairs) * (pair_tile > pair_least ? pair_tile : pair_least) + 10;
-  const int64_t least = p.bn * RT / 112;  // epilogue of a stream tile, in steps
-  const int64_t cost_whole = up(tiles, sms) * (KB > least ? KB : least) + 5;
+  const int64_t cost_pair = up(pair_tiles, pairs) * (pair_tile > pair_least ? pair_tile : pair_least) + 18;
+  const int64_t least = (R < p.bn ? R : p.bn) * RT / 112;  // epilogue of a stream tile, in steps
+  const int64_t cost_whole = up(tiles, sms) * (KB > least ? KB : least) + (KB > least ? least : KB) + 5;
   const int64_t run = up(tiles * KB, sms), ends = up(tiles, sms) * 2 * least;
   const int64_t cost_shared = (run > ends ? run : ends) + 4 + p.bn / 8;
   p.shared = cost_shared < cost_whole;
