@@ -17,14 +17,14 @@
 // start on 16 bytes) are copied in bf16 parts first, where that pays: the parts'
 // products meet in the same sums.  The backward of 8192 tokens of 4096 x 4096 in
 // fp32 at rank 64: 465 us, by fp32 FMAs 3250.
-
+//
 // Each product's chunks, tile after tile, are dealt out in equal runs over the
 // SMs; the partial sums of a tile that several CTAs share are added up in CTA
 // order by a second, small launch.  (By the last CTA of a tile, that held up its
 // own run: 73 us where this takes 50.)  The runs do not depend on what else is in
 // the launch: a gradient has the same bits whichever others are wanted.  Bound
-// by HBM on the large matrix: V of 8192 x 12288 and U of 8192 x 4096 at rank 32 in
-// 42 us (268 MB, 6.4 TB/s), dA and dB of the same in 48.
+// by HBM on the large matrix: V of 8192 x 12288 at rank 32 in 42 us (201 MB, 4.8
+// TB/s), dB of the same with dA of 8192 x 4096 in 48 (268 MB, 5.6 TB/s).
 #include "common.cuh"
 #include "int8.h"
 #include "int8_dev.cuh"
