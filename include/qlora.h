@@ -397,7 +397,10 @@ qlora_status qlora_adamw_step(const qlora_tensor* tensors, int32_t count, int32_
  * small per-call scratch (status header, tickets, U / V, split partials),
  * the bf16 backward from 2048 tokens on includes a bf16 copy of the decoded
  * weight (2 O I bytes): the input gradient decodes the weight into it once
- * per call and its GEMM reads it there.  The workspace is scratch for one
+ * per call and its GEMM reads it there.  INT8 weights: it holds the rows'
+ * codes (a byte a value) and, where many tokens are fp32 or bf16 of a width
+ * that is no multiple of 8, a copy of X (and dY) in bf16 parts (6 or 2 bytes
+ * a value).  0 for what the calls refuse.  The workspace is scratch for one
  * call at a time; the weight itself stays packed.
  */
 size_t qlora_linear_workspace_bytes(const qlora_weight* w, int64_t R, int32_t r, int32_t op,
