@@ -86,14 +86,21 @@ def workspace(nbytes: int, device="cuda") -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+def _on_stream(stream, dev):
+    """Allocations and copies of a call are made on the stream that it runs on:
+    memory of another stream's pool may still be in use there, and a copy made
+    there is not ordered before the call."""
+    if stream is None:
+        return _HERE
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
+
 def _scratch(nbytes: int, dev, stream) -> torch.Tensor:
     """The workspace of one call, allocated for the stream that the call runs on
     (else it could be handed out again while that stream still uses it)."""
-    if stream is None:
-        return workspace(nbytes, dev)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
-    with torch.cuda.stream(stream):
+    with _on_stream(stream, dev):
         return workspace(nbytes, dev)
 
 
@@ -193,17 +200,18 @@ def qlora_quantize_nf4(W: torch.Tensor, B: int = 64, C: int = 256, stream=None) 
     lib = _ffi.load()
     if W.dim() != 2 or W.dtype != torch.float32 or not W.is_cuda:
         raise ValueError("W must be a CUDA float32 matrix")
-    W = W.contiguous()
     O, I = W.shape
     N = O * I
     M = -(-N // B)
     S = -(-M // C)
     dev = W.device
-    codes = torch.empty((N + 1) // 2, dtype=torch.uint8, device=dev)
-    q = torch.empty(M, dtype=torch.uint8, device=dev)
-    t = torch.empty(S, dtype=torch.float32, device=dev)
-    mu = torch.empty(1, dtype=torch.float32, device=dev)
-    ws = workspace(lib.qlora_quantize_nf4_workspace_bytes(N, B, C), dev)
+    with _on_stream(stream, dev):
+        W = W.contiguous()
+        codes = torch.empty((N + 1) // 2, dtype=torch.uint8, device=dev)
+        q = torch.empty(M, dtype=torch.uint8, device=dev)
+        t = torch.empty(S, dtype=torch.float32, device=dev)
+        mu = torch.empty(1, dtype=torch.float32, device=dev)
+        ws = workspace(lib.qlora_quantize_nf4_workspace_bytes(N, B, C), dev)
     st = lib.qlora_quantize_nf4(_ptr(W), O, I, B, C, _ptr(codes), _ptr(q), _ptr(t), _ptr(mu), _ptr(ws),
                                 ws.numel(), _stream(stream))
     _check(st, "qlora_quantize_nf4")
@@ -217,16 +225,17 @@ def qlora_quantize_nf4_noalloc(W: torch.Tensor, B: int = 64, C: int = 256, strea
     lib = _ffi.load()
     if W.dim() != 2 or W.dtype != torch.float32 or not W.is_cuda:
         raise ValueError("W must be a CUDA float32 matrix")
-    W = W.contiguous()
     O, I = W.shape
     N = O * I
     M = -(-N // B)
     S = -(-M // C)
     dev = W.device
-    codes = torch.empty((N + 1) // 2, dtype=torch.uint8, device=dev)
-    q = torch.empty(M, dtype=torch.uint8, device=dev)
-    t = torch.empty(S, dtype=torch.float32, device=dev)
-    mu = torch.empty(1, dtype=torch.float32, device=dev)
+    with _on_stream(stream, dev):
+        W = W.contiguous()
+        codes = torch.empty((N + 1) // 2, dtype=torch.uint8, device=dev)
+        q = torch.empty(M, dtype=torch.uint8, device=dev)
+        t = torch.empty(S, dtype=torch.float32, device=dev)
+        mu = torch.empty(1, dtype=torch.float32, device=dev)
     st = lib.qlora_quantize_nf4_noalloc(_ptr(W), O, I, B, C, _ptr(codes), _ptr(q), _ptr(t), _ptr(mu),
                                         _stream(stream))
     _check(st, "qlora_quantize_nf4_noalloc")
@@ -243,14 +252,15 @@ def qlora_quantize_nf4_fp32scale(W: torch.Tensor, B: int = 64, stream=None) -> Q
     lib = _ffi.load()
     if W.dim() != 2 or W.dtype != torch.float32 or not W.is_cuda:
         raise ValueError("W must be a CUDA float32 matrix")
-    W = W.contiguous()
     O, I = W.shape
     N = O * I
     M = -(-N // B)
     dev = W.device
-    codes = torch.empty((N + 1) // 2, dtype=torch.uint8, device=dev)
-    scale = torch.empty(M, dtype=torch.float32, device=dev)
-    ws = workspace(lib.qlora_quantize_nf4_fp32scale_workspace_bytes(N, B), dev)
+    with _on_stream(stream, dev):
+        W = W.contiguous()
+        codes = torch.empty((N + 1) // 2, dtype=torch.uint8, device=dev)
+        scale = torch.empty(M, dtype=torch.float32, device=dev)
+        ws = workspace(lib.qlora_quantize_nf4_fp32scale_workspace_bytes(N, B), dev)
     st = lib.qlora_quantize_nf4_fp32scale(_ptr(W), O, I, B, _ptr(codes), _ptr(scale), _ptr(ws), ws.numel(),
                                           _stream(stream))
     _check(st, "qlora_quantize_nf4_fp32scale")
@@ -262,15 +272,16 @@ def qlora_quantize_affine(W: torch.Tensor, bits: int = 4, G: int = 64, stream=No
     lib = _ffi.load()
     if W.dim() != 2 or W.dtype != torch.float32 or not W.is_cuda:
         raise ValueError("W must be a CUDA float32 matrix")
-    W = W.contiguous()
     O, I = W.shape
     N = O * I
     ng = -(-N // G)
     dev = W.device
-    codes = torch.empty(N if bits == 8 else (N + 1) // 2, dtype=torch.uint8, device=dev)
-    scale = torch.empty(ng, dtype=torch.float32, device=dev)
-    bias = torch.empty(ng, dtype=torch.float32, device=dev)
-    ws = workspace(lib.qlora_quantize_affine_workspace_bytes(N, bits, G), dev)
+    with _on_stream(stream, dev):
+        W = W.contiguous()
+        codes = torch.empty(N if bits == 8 else (N + 1) // 2, dtype=torch.uint8, device=dev)
+        scale = torch.empty(ng, dtype=torch.float32, device=dev)
+        bias = torch.empty(ng, dtype=torch.float32, device=dev)
+        ws = workspace(lib.qlora_quantize_affine_workspace_bytes(N, bits, G), dev)
     st = lib.qlora_quantize_affine(_ptr(W), O, I, bits, G, _ptr(codes), _ptr(scale), _ptr(bias), _ptr(ws),
                                    ws.numel(), _stream(stream))
     _check(st, "qlora_quantize_affine")
@@ -289,13 +300,14 @@ def qlora_quantize_int8(W: torch.Tensor, stream=None) -> QuantizedWeight:
     lib = _ffi.load()
     if W.dim() != 2 or W.dtype != torch.float32 or not W.is_cuda:
         raise ValueError("W must be a CUDA float32 matrix")
-    W = W.contiguous()
     O, I = W.shape
     dev = W.device
-    codes = torch.empty((O, qlora_int8_pitch(I)), dtype=torch.int8, device=dev)
-    scale = torch.empty(O, dtype=torch.float32, device=dev)
-    with _on(dev):
+    with _on_stream(stream, dev):
+        W = W.contiguous()
+        codes = torch.empty((O, qlora_int8_pitch(I)), dtype=torch.int8, device=dev)
+        scale = torch.empty(O, dtype=torch.float32, device=dev)
         ws = workspace(lib.qlora_quantize_int8_workspace_bytes(O, I), dev)
+    with _on(dev):
         st = lib.qlora_quantize_int8(_ptr(W), O, I, _ptr(codes), _ptr(scale), _ptr(ws), ws.numel(),
                                      _stream(stream))
     _check(st, "qlora_quantize_int8")

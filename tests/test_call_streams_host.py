@@ -1,0 +1,85 @@
+"""Where a call that is given a stream allocates and copies, seen on the CPU:
+tensors that say they are CUDA ones, a library that records what it is given,
+and a note of the stream that is current at every allocation and copy."""
+import contextlib
+
+import pytest
+import torch
+
+import qlora_bit_frozen_b200 as q
+
+
+
+class Side:
+    cuda_stream = 77
+
+
+SIDE = Side()
+
+
+class Cuda(torch.Tensor):
+    """A CPU tensor that says it is a CUDA one, and notes where it is copied."""
+    is_cuda = True
+
+    def contiguous(self):
+        if not self.is_contiguous():
+            Cuda.seen.append(("copy", Cuda.stream))
+        return super().contiguous()
+
+    def new_empty(self, *a, **kw):
+        Cuda.seen.append(("new", Cuda.stream))
+        return super().new_empty(*a, **kw)
+
+
+def cuda(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(Cuda)
+
+
+class Library:
+    """Every status is OK, every size 512 bytes; notes the calls' last argument, the stream."""
+    def __init__(self):
+        self.streams = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            if name.endswith("_bytes"):
+                return 512
+            self.streams.append(args[-1])
+            return 0
+        return call
+
+
+@pytest.fixture
+def here(monkeypatch):
+    Cuda.seen, Cuda.stream = [], None
+    lib = Library()
+    empty = torch.empty
+
+    def noted(*a, **kw):
+        Cuda.seen.append(("empty", Cuda.stream))
+        return empty(*a, **kw).as_subclass(Cuda)
+
+    @contextlib.contextmanager
+    def on_stream(s):
+        before, Cuda.stream = Cuda.stream, s
+        yield
+        Cuda.stream = before
+
+    monkeypatch.setattr(q._ffi, "load", lambda: lib)
+    monkeypatch.setattr(torch, "empty", noted)
+    monkeypatch.setattr(torch.cuda, "stream", on_stream)
+    monkeypatch.setattr(q, "_on", lambda dev: contextlib.nullcontext())
+    return lib
+
+
+@pytest.mark.parametrize("call", [
+    lambda W: q.qlora_quantize_int8(W, stream=SIDE),
+    lambda W: q.qlora_quantize_nf4(W, 16, 4, stream=SIDE),
+    lambda W: q.qlora_quantize_nf4_noalloc(W, 16, 4, stream=SIDE),
+    lambda W: q.qlora_quantize_nf4_fp32scale(W, 16, stream=SIDE),
+    lambda W: q.qlora_quantize_affine(W, 4, 16, stream=SIDE)],
+    ids=["int8", "nf4", "nf4_noalloc", "nf4_fp32scale", "affine"])
+def test_quantizers_copy_and_allocate_on_their_stream(here, call):
+    call(cuda(32, 48).t())
+    assert ("copy", SIDE) in Cuda.seen and len(Cuda.seen) >= 3
+    assert {s for _, s in Cuda.seen} == {SIDE} and here.streams == [77]
