@@ -88,20 +88,13 @@ def workspace(nbytes: int, device="cuda") -> torch.Tensor:
 
 def _on_stream(stream, dev):
     """Allocations and copies of a call are made on the stream that it runs on:
-    memory of another stream's pool may still be in use there, and a copy made
-    there is not ordered before the call."""
+    memory of another stream's pool may still be in use there or be handed out
+    again there too early, and a copy made there is not ordered before the call."""
     if stream is None:
         return _HERE
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
     return torch.cuda.stream(stream)
-
-
-def _scratch(nbytes: int, dev, stream) -> torch.Tensor:
-    """The workspace of one call, allocated for the stream that the call runs on
-    (else it could be handed out again while that stream still uses it)."""
-    with _on_stream(stream, dev):
-        return workspace(nbytes, dev)
 
 
 @dataclass
@@ -318,7 +311,8 @@ def qlora_dequantize(w: QuantizedWeight, out: Optional[torch.Tensor] = None, str
     """Diagnostic fp32 reconstruction of the whole weight (never used by fwd/bwd)."""
     lib = _ffi.load()
     if out is None:
-        out = torch.empty((w.O, w.I), dtype=torch.float32, device=w.codes.device)
+        with _on_stream(stream, w.codes.device):
+            out = torch.empty((w.O, w.I), dtype=torch.float32, device=w.codes.device)
     _need("qlora_dequantize", "out", out, w.codes.device, (w.O, w.I), torch.float32)
     cw = w.c_struct()
     _check(lib.qlora_dequantize(ctypes.byref(cw), _ptr(out), _stream(stream)), "qlora_dequantize")
@@ -334,7 +328,8 @@ def qlora_merge(w: QuantizedWeight, A: torch.Tensor, B: torch.Tensor, alpha: flo
             or tuple(B.shape) != (w.O, r) or not A.is_contiguous() or not B.is_contiguous():
         raise ValueError("A must be contiguous fp32 [r x I] and B contiguous fp32 [O x r]")
     if out is None:
-        out = torch.empty((w.O, w.I), dtype=torch.float32, device=w.codes.device)
+        with _on_stream(stream, w.codes.device):
+            out = torch.empty((w.O, w.I), dtype=torch.float32, device=w.codes.device)
     dev = w.codes.device
     _need("qlora_merge", "A", A, dev)
     _need("qlora_merge", "B", B, dev)
@@ -478,7 +473,8 @@ def qlora_grad_norm(tensors: OptimTensors, max_norm: float, control: torch.Tenso
     _need(f, "control", control, dev, (4,), torch.int32)
     with _on(dev):
         if ws is None:
-            ws = _scratch(qlora_grad_norm_workspace_bytes(tensors), dev, stream)
+            with _on_stream(stream, dev):
+                ws = workspace(qlora_grad_norm_workspace_bytes(tensors), dev)
         _need(f, "ws", ws, dev)
         st = _ffi.load().qlora_grad_norm(tensors._c, len(tensors.grads), float(max_norm), _ptr(control),
                                          _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
@@ -528,13 +524,14 @@ def qlora_linear_fwd(w: QuantizedWeight, X: torch.Tensor, A: torch.Tensor, B: to
     R = X.shape[0]
     r = A.shape[0]
     compute = _compute_of(X)
-    if Y is None:
-        Y = X.new_empty((R, w.O))
-    if U_out is None and want_u:
-        U_out = A.new_empty((R, r))
     cw = ctypes.byref(w.c_struct())
-    if ws is None:
-        ws = _scratch(lib.qlora_linear_workspace_bytes(cw, R, r, OP_FWD, compute), X.device, stream)
+    with _on_stream(stream, X.device):
+        if Y is None:
+            Y = X.new_empty((R, w.O))
+        if U_out is None and want_u:
+            U_out = A.new_empty((R, r))
+        if ws is None:
+            ws = workspace(lib.qlora_linear_workspace_bytes(cw, R, r, OP_FWD, compute), X.device)
     dev, f = w.codes.device, "qlora_linear_fwd"
     _need(f, "X", X, dev, (R, w.I))
     _need(f, "A", A, dev, (r, w.I), torch.float32)
@@ -560,15 +557,16 @@ def qlora_linear_bwd(w: QuantizedWeight, X: Optional[torch.Tensor], dY: torch.Te
     r = A.shape[0]
     compute = _compute_of(dY)
     dev = dY.device
-    if want_dx and dX is None:
-        dX = torch.empty((R, w.I), dtype=dY.dtype, device=dev)
-    if want_da and dA is None:
-        dA = torch.empty((r, w.I), dtype=torch.float32, device=dev)
-    if want_db and dB is None:
-        dB = torch.empty((w.O, r), dtype=torch.float32, device=dev)
     cw = ctypes.byref(w.c_struct())
-    if ws is None:
-        ws = _scratch(lib.qlora_linear_workspace_bytes(cw, R, r, OP_BWD, compute), dev, stream)
+    with _on_stream(stream, dev):
+        if want_dx and dX is None:
+            dX = torch.empty((R, w.I), dtype=dY.dtype, device=dev)
+        if want_da and dA is None:
+            dA = torch.empty((r, w.I), dtype=torch.float32, device=dev)
+        if want_db and dB is None:
+            dB = torch.empty((w.O, r), dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = workspace(lib.qlora_linear_workspace_bytes(cw, R, r, OP_BWD, compute), dev)
     wd, f = w.codes.device, "qlora_linear_bwd"
     _need(f, "dY", dY, wd, (R, w.O))
     _need(f, "X", X, wd, (R, w.I), dY.dtype)

@@ -35,3 +35,26 @@ def test_a_transposed_weight_beside_a_busy_stream(call, raw):
     busy()
     got = call(W.t(), stream=side.cuda_stream if raw else side)
     assert all(torch.equal(a, b) for a, b in zip(buffers(got), buffers(want)))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "nf4"])
+@pytest.mark.parametrize("R", [3, 700])
+def test_outputs_beside_a_busy_stream(fmt, R):
+    """Outputs that a call allocates are not memory that the current stream has yet to write."""
+    O, I, r = 640, 512, 8
+    W, X, dY, A, B = (normal(1, O, I), normal(2, R, I, dtype=BF), normal(3, R, O, dtype=BF), normal(4, r, I),
+                      normal(5, O, r))
+    w = q.qlora_quantize_int8(W) if fmt == "int8" else q.qlora_quantize_nf4(W)
+    calls = [lambda s: q.qlora_linear_fwd(w, X, A, B, 16.0, stream=s),
+             lambda s: q.qlora_linear_bwd(w, X, dY, A, B, 16.0, stream=s),
+             lambda s: (q.qlora_dequantize(w, stream=s),), lambda s: (q.qlora_merge(w, A, B, 16.0, stream=s),)]
+    for call in calls:
+        want = call(None)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        busy()
+        for x in want:  # written after the work above, and given back at once
+            torch.full_like(x, 7)
+        got = call(side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

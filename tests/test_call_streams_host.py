@@ -83,3 +83,18 @@ def test_quantizers_copy_and_allocate_on_their_stream(here, call):
     call(cuda(32, 48).t())
     assert ("copy", SIDE) in Cuda.seen and len(Cuda.seen) >= 3
     assert {s for _, s in Cuda.seen} == {SIDE} and here.streams == [77]
+
+
+def weight(O=32, I=48):
+    return q.QuantizedWeight(q.FMT_INT8, O, I, I, 0, 8, cuda(O, I, dtype=torch.int8), scale=cuda(O))
+
+
+@pytest.mark.parametrize("call", [
+    lambda w, X, A, B: q.qlora_linear_fwd(w, X, A, B, 1.0, stream=SIDE),
+    lambda w, X, A, B: q.qlora_linear_bwd(w, X, cuda(4, 32), A, B, 1.0, stream=SIDE),
+    lambda w, X, A, B: q.qlora_dequantize(w, stream=SIDE),
+    lambda w, X, A, B: q.qlora_merge(w, A, B, 1.0, stream=SIDE)],
+    ids=["forward", "backward", "dequantize", "merge"])
+def test_outputs_are_allocated_on_the_stream_of_the_call(here, call):
+    call(weight(), cuda(4, 48), cuda(8, 48), cuda(32, 8))
+    assert Cuda.seen and {s for _, s in Cuda.seen} == {SIDE} and here.streams == [77]
