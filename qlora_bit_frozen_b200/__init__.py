@@ -205,8 +205,9 @@ def qlora_quantize_nf4(W: torch.Tensor, B: int = 64, C: int = 256, stream=None) 
         t = torch.empty(S, dtype=torch.float32, device=dev)
         mu = torch.empty(1, dtype=torch.float32, device=dev)
         ws = workspace(lib.qlora_quantize_nf4_workspace_bytes(N, B, C), dev)
-    st = lib.qlora_quantize_nf4(_ptr(W), O, I, B, C, _ptr(codes), _ptr(q), _ptr(t), _ptr(mu), _ptr(ws),
-                                ws.numel(), _stream(stream))
+    with _on(dev):
+        st = lib.qlora_quantize_nf4(_ptr(W), O, I, B, C, _ptr(codes), _ptr(q), _ptr(t), _ptr(mu), _ptr(ws),
+                                    ws.numel(), _stream(stream))
     _check(st, "qlora_quantize_nf4")
     return QuantizedWeight(FMT_NF4_DQ, O, I, B, C, 4, codes, q, t, mu)
 
@@ -229,8 +230,9 @@ def qlora_quantize_nf4_noalloc(W: torch.Tensor, B: int = 64, C: int = 256, strea
         q = torch.empty(M, dtype=torch.uint8, device=dev)
         t = torch.empty(S, dtype=torch.float32, device=dev)
         mu = torch.empty(1, dtype=torch.float32, device=dev)
-    st = lib.qlora_quantize_nf4_noalloc(_ptr(W), O, I, B, C, _ptr(codes), _ptr(q), _ptr(t), _ptr(mu),
-                                        _stream(stream))
+    with _on(dev):
+        st = lib.qlora_quantize_nf4_noalloc(_ptr(W), O, I, B, C, _ptr(codes), _ptr(q), _ptr(t), _ptr(mu),
+                                            _stream(stream))
     _check(st, "qlora_quantize_nf4_noalloc")
     return QuantizedWeight(FMT_NF4_DQ, O, I, B, C, 4, codes, q, t, mu)
 
@@ -254,8 +256,9 @@ def qlora_quantize_nf4_fp32scale(W: torch.Tensor, B: int = 64, stream=None) -> Q
         codes = torch.empty((N + 1) // 2, dtype=torch.uint8, device=dev)
         scale = torch.empty(M, dtype=torch.float32, device=dev)
         ws = workspace(lib.qlora_quantize_nf4_fp32scale_workspace_bytes(N, B), dev)
-    st = lib.qlora_quantize_nf4_fp32scale(_ptr(W), O, I, B, _ptr(codes), _ptr(scale), _ptr(ws), ws.numel(),
-                                          _stream(stream))
+    with _on(dev):
+        st = lib.qlora_quantize_nf4_fp32scale(_ptr(W), O, I, B, _ptr(codes), _ptr(scale), _ptr(ws), ws.numel(),
+                                              _stream(stream))
     _check(st, "qlora_quantize_nf4_fp32scale")
     return QuantizedWeight(FMT_NF4_FP32SCALE, O, I, B, 0, 4, codes, scale=scale)
 
@@ -275,8 +278,9 @@ def qlora_quantize_affine(W: torch.Tensor, bits: int = 4, G: int = 64, stream=No
         scale = torch.empty(ng, dtype=torch.float32, device=dev)
         bias = torch.empty(ng, dtype=torch.float32, device=dev)
         ws = workspace(lib.qlora_quantize_affine_workspace_bytes(N, bits, G), dev)
-    st = lib.qlora_quantize_affine(_ptr(W), O, I, bits, G, _ptr(codes), _ptr(scale), _ptr(bias), _ptr(ws),
-                                   ws.numel(), _stream(stream))
+    with _on(dev):
+        st = lib.qlora_quantize_affine(_ptr(W), O, I, bits, G, _ptr(codes), _ptr(scale), _ptr(bias), _ptr(ws),
+                                       ws.numel(), _stream(stream))
     _check(st, "qlora_quantize_affine")
     return QuantizedWeight(FMT_AFFINE, O, I, G, 0, bits, codes, scale=scale, bias=bias)
 
@@ -315,7 +319,9 @@ def qlora_dequantize(w: QuantizedWeight, out: Optional[torch.Tensor] = None, str
             out = torch.empty((w.O, w.I), dtype=torch.float32, device=w.codes.device)
     _need("qlora_dequantize", "out", out, w.codes.device, (w.O, w.I), torch.float32)
     cw = w.c_struct()
-    _check(lib.qlora_dequantize(ctypes.byref(cw), _ptr(out), _stream(stream)), "qlora_dequantize")
+    with _on(w.codes.device):
+        st = lib.qlora_dequantize(ctypes.byref(cw), _ptr(out), _stream(stream))
+    _check(st, "qlora_dequantize")
     return out
 
 
@@ -335,8 +341,9 @@ def qlora_merge(w: QuantizedWeight, A: torch.Tensor, B: torch.Tensor, alpha: flo
     _need("qlora_merge", "B", B, dev)
     _need("qlora_merge", "out", out, dev, (w.O, w.I), torch.float32)
     cw = w.c_struct()
-    _check(lib.qlora_merge(ctypes.byref(cw), _ptr(A), _ptr(B), r, float(alpha), _ptr(out), _stream(stream)),
-           "qlora_merge")
+    with _on(dev):
+        st = lib.qlora_merge(ctypes.byref(cw), _ptr(A), _ptr(B), r, float(alpha), _ptr(out), _stream(stream))
+    _check(st, "qlora_merge")
     return out
 
 
@@ -349,8 +356,9 @@ def qlora_adam_step(params: torch.Tensor, grads: torch.Tensor, m: torch.Tensor, 
         if x.dtype != torch.float32 or not x.is_contiguous() or x.numel() != n:
             raise ValueError("params, grads, m and v must be contiguous fp32 tensors of one size")
         _need("qlora_adam_step", "params/grads/m/v", x, params.device)
-    st = _ffi.load().qlora_adam_step(_ptr(params), _ptr(grads), _ptr(m), _ptr(v), n, int(t), float(lr),
-                                     float(beta1), float(beta2), float(eps), int(page_elems), _stream(stream))
+    with _on(params.device):
+        st = _ffi.load().qlora_adam_step(_ptr(params), _ptr(grads), _ptr(m), _ptr(v), n, int(t), float(lr),
+                                         float(beta1), float(beta2), float(eps), int(page_elems), _stream(stream))
     _check(st, "qlora_adam_step")
 
 
@@ -587,12 +595,14 @@ def qlora_linear_bwd(w: QuantizedWeight, X: Optional[torch.Tensor], dY: torch.Te
 
 def qlora_workspace_status(ws: torch.Tensor, stream=None) -> int:
     """Device error word of the last call that used ws (synchronizes)."""
-    return int(_ffi.load().qlora_workspace_status(_ptr(ws), _stream(stream)))
+    with _on(ws.device):
+        return int(_ffi.load().qlora_workspace_status(_ptr(ws), _stream(stream)))
 
 
 def qlora_selftest_wait_timeout(limit_us: int = 1000, stream=None, device="cuda") -> int:
     ws = workspace(256, device)
-    return int(_ffi.load().qlora_selftest_wait_timeout(_ptr(ws), ws.numel(), int(limit_us), _stream(stream)))
+    with _on(ws.device):
+        return int(_ffi.load().qlora_selftest_wait_timeout(_ptr(ws), ws.numel(), int(limit_us), _stream(stream)))
 
 
 def qlora_kernel_launch_count() -> int:

@@ -98,3 +98,33 @@ def weight(O=32, I=48):
 def test_outputs_are_allocated_on_the_stream_of_the_call(here, call):
     call(weight(), cuda(4, 48), cuda(8, 48), cuda(32, 8))
     assert Cuda.seen and {s for _, s in Cuda.seen} == {SIDE} and here.streams == [77]
+
+
+@pytest.mark.parametrize("call", [
+    lambda w, W, A, B: q.qlora_quantize_int8(W),
+    lambda w, W, A, B: q.qlora_quantize_nf4(W, 16, 4),
+    lambda w, W, A, B: q.qlora_quantize_nf4_noalloc(W, 16, 4),
+    lambda w, W, A, B: q.qlora_quantize_nf4_fp32scale(W, 16),
+    lambda w, W, A, B: q.qlora_quantize_affine(W, 4, 16),
+    lambda w, W, A, B: q.qlora_dequantize(w),
+    lambda w, W, A, B: q.qlora_merge(w, A, B, 1.0),
+    lambda w, W, A, B: q.qlora_adam_step(A, A, A, A, 1, 1e-3),
+    lambda w, W, A, B: q.qlora_workspace_status(A),
+    lambda w, W, A, B: q.qlora_linear_fwd(w, cuda(4, 48), A, B, 1.0),
+    lambda w, W, A, B: q.qlora_linear_bwd(w, cuda(4, 48), cuda(4, 32), A, B, 1.0)],
+    ids=["int8", "nf4", "nf4_noalloc", "nf4_fp32scale", "affine", "dequantize", "merge", "adam", "status", "forward",
+         "backward"])
+def test_calls_run_on_the_device_of_their_tensors(here, call, monkeypatch):
+    """Also where another device is the current one: its current stream, and the launch there."""
+    at = []
+
+    @contextlib.contextmanager
+    def on(dev):
+        at.append(dev)
+        yield
+        at.pop()
+
+    monkeypatch.setattr(q, "_on", on)
+    monkeypatch.setattr(q, "_stream", lambda s: list(at))
+    call(weight(), cuda(32, 48), cuda(8, 48), cuda(32, 8))
+    assert here.streams == [[torch.device("cpu")]]
