@@ -52,9 +52,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// Whether `ok` holds for all THREADS epilogue threads (barrier 1).
+// Barrier 1 of the THREADS epilogue threads.  The barrier is one instruction of a
+// whole warp, so lanes that took different ways (a loop over elements, a wait that
+// ended later) meet first; so do the lanes before all_of's.
+template <int THREADS>
+__device__ __forceinline__ void epi_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+// Whether `ok` holds for all of them.
 template <int THREADS>
 __device__ __forceinline__ bool all_of(bool ok) {
+  __syncwarp();
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"

@@ -825,7 +825,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             su[e] = j < p.e.r ? p.e.s * __ldcg(p.U + t * p.e.r + j) : 0.0f;
           }
         staged = 0;
-        asm volatile("bar.sync 1, %0;" ::"n"(kStreamEpi) : "memory");
+        epi_sync<kStreamEpi>();
         sums.template run<RT>(p, side, su);
       }
     }
@@ -861,7 +861,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       }
       const float sw = !DX && in ? __ldg(p.e.ws + n) : 1.0f;
       if (tt != staged) {
-        asm volatile("bar.sync 1, %0;" ::"n"(kStreamEpi) : "memory");  // the last tile's are read
+        epi_sync<kStreamEpi>();  // the last tile's are read
         stage_side(t0, toks);
         staged = tt;
       }
@@ -886,13 +886,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             if (c0 + j < toks) atomicAdd(part + (c0 + j) * 128, (int)acc[j]);
         }
         __threadfence();
-        asm volatile("bar.sync 1, %0;" ::"n"(kStreamEpi) : "memory");
+        epi_sync<kStreamEpi>();
         if (warp == 2 && lane == 0)
           *last_flag = atomicAdd(p.tickets + tile, (uint32_t)steps) + (uint32_t)steps == (uint32_t)p.KB;
-        asm volatile("bar.sync 1, %0;" ::"n"(kStreamEpi) : "memory");
+        epi_sync<kStreamEpi>();
         finish = *last_flag != 0;
         __threadfence();
-        asm volatile("bar.sync 1, %0;" ::"n"(kStreamEpi) : "memory");  // all have read the flag
+        epi_sync<kStreamEpi>();  // all have read the flag
       }
       if (finish) {
         // eight tokens at a time (columns past the last token hold sums of
@@ -920,17 +920,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             }
             v[j] = __fadd_rn(__fmul_rn(__fmul_rn((float)(int)acc[j], side[BN * RT + c0 + j]), sw), sum2(d));
           }
-          if (!in) continue;
           const int64_t o = (t0 + c0) * p.e.N + n;
-          if (p.e.bf16) {
+          if (in && p.e.bf16) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               if (c0 + j < toks) ((__nv_bfloat16*)p.e.out)[o + j * p.e.N] = __float2bfloat16_rn(v[j]);
-          } else {
+          } else if (in) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               if (c0 + j < toks) ((float*)p.e.out)[o + j * p.e.N] = v[j];
           }
+          __syncwarp();  // lanes past N beside lanes that store: the next load of TMEM is one of the whole warp
         }
       }
       tc_fence_before();
