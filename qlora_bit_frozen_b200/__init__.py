@@ -374,8 +374,12 @@ class OptimTensors:
     (zeros stand for zero states).  with_states() allocates zero states.
 
     The tensors are kept and used in place: keep writing gradients into the
-    same storage (or build a new object for new tensors).  No two parameters
-    or states may overlap, nor a gradient with one of them."""
+    same storage (or build a new object for new tensors).  Their storage is
+    held, so that it stays valid where a listed tensor is given another one
+    (`p.data = ...`, `module.to(...)`); the calls then refuse: each looks at one
+    tensor of every list, in turn, so that they notice at once where all have
+    moved, and after at most as many calls as there are tensors where one has.
+    No two parameters or states may overlap, nor a gradient with one of them."""
 
     def __init__(self, grads: Sequence[torch.Tensor], params: Optional[Sequence[torch.Tensor]] = None,
                  m: Optional[Sequence[torch.Tensor]] = None, v: Optional[Sequence[torch.Tensor]] = None,
@@ -397,6 +401,8 @@ class OptimTensors:
             raise ValueError("OptimTensors: 8-bit states need both m_scale and v_scale")
         self.state_bits = 8 if self.m_scale is not None else 32
         self._c = (qlora_tensor * max(n, 1))()
+        self._at = []  # of each index, its tensors and where they are
+        self._turn = [0, 0]  # of the norm, of the step
         f = "OptimTensors"
         for i, g in enumerate(self.grads):
             if g.dtype not in _DTYPES:
@@ -404,6 +410,7 @@ class OptimTensors:
             _need(f, f"grads[{i}]", g, self.device)
             c = self._c[i]
             c.grad, c.n, c.grad_type = g.data_ptr(), g.numel(), _DTYPES[g.dtype]
+            self._at.append([(g, g.data_ptr(), "grads")])
             if self.params is None:
                 continue
             p = self.params[i]
@@ -422,10 +429,22 @@ class OptimTensors:
                 if x[i].numel() != size:
                     raise ValueError(f"{f}: {name}[{i}] must have {size} values, got {x[i].numel()}")
                 setattr(c, name, x[i].data_ptr())
+                self._at[i].append((x[i], x[i].data_ptr(), name))
             c.param, c.param_type = p.data_ptr(), _DTYPES[p.dtype]
+            self._at[i].append((p, p.data_ptr(), "params"))
         if self.params is not None:
             self._refuse_overlap()
+        self._held = [x.untyped_storage() for at in self._at for x, _, _ in at]
         self._norm_ws = None  # workspace bytes of qlora_grad_norm
+
+    def _in_place(self, where: str, step: bool):
+        """One tensor of each of the call's lists, in turn, is where it was."""
+        i = self._turn[step]
+        for x, ptr, name in self._at[i] if step else self._at[i][:1]:
+            if x.data_ptr() != ptr:
+                raise ValueError(f"{where}: {name}[{i}] has other storage than when it was listed: "
+                                 "build a new OptimTensors")
+        self._turn[step] = i + 1 if i + 1 < len(self._at) else 0
 
     def _refuse_overlap(self):
         spans = []
@@ -479,6 +498,8 @@ def qlora_grad_norm(tensors: OptimTensors, max_norm: float, control: torch.Tenso
     dev = tensors.device if tensors.device is not None else control.device
     f = "qlora_grad_norm"
     _need(f, "control", control, dev, (4,), torch.int32)
+    if tensors._at:
+        tensors._in_place(f, step=False)
     with _on(dev):
         if ws is None:
             with _on_stream(stream, dev):
@@ -503,6 +524,7 @@ def qlora_adamw_step(tensors: OptimTensors, t: int = 0, lr: float = 1e-3, beta1:
     if dev is None:
         return
     _need(f, "control", control, dev, (4,), torch.int32)
+    tensors._in_place(f, step=True)
     with _on(dev):
         st = _ffi.load().qlora_adamw_step(tensors._c, len(tensors.grads), tensors.state_bits, int(t), float(lr),
                                           float(beta1), float(beta2), float(eps), float(weight_decay),

@@ -128,3 +128,75 @@ def test_calls_run_on_the_device_of_their_tensors(here, call, monkeypatch):
     monkeypatch.setattr(q, "_stream", lambda s: list(at))
     call(weight(), cuda(32, 48), cuda(8, 48), cuda(32, 8))
     assert here.streams == [[torch.device("cpu")]]
+
+
+def listed(n, state_bits=32):
+    params, grads = [cuda(300) for _ in range(n)], [cuda(300) for _ in range(n)]
+    return params, grads, q.OptimTensors.with_states(params, grads, state_bits)
+
+
+@pytest.fixture
+def steps(here, monkeypatch):
+    zeros = torch.zeros
+    monkeypatch.setattr(torch, "zeros", lambda *a, **kw: zeros(*a, **kw).as_subclass(Cuda))
+    control = zeros(4, dtype=torch.int32).as_subclass(Cuda)
+
+    def norm(T):
+        q.qlora_grad_norm(T, 1.0, control, stream=SIDE)
+
+    def adamw(T):
+        q.qlora_adamw_step(T, t=1, stream=SIDE)
+
+    return norm, adamw
+
+
+@pytest.mark.parametrize("state_bits", [8, 32])
+def test_listed_tensors_that_move_are_refused(here, steps, state_bits):
+    norm, adamw = steps
+    for step, lists in ((norm, ("grads",)), (adamw, ("params", "grads", "m", "v"))):
+        for name in lists:
+            params, grads, T = listed(5, state_bits)
+            for _ in range(7):
+                step(T)
+            every = getattr(T, name)
+            for x in every:  # as module.to() and the like do
+                x.data = x.data.clone()
+            launched = len(here.streams)
+            with pytest.raises(ValueError, match=name):
+                step(T)
+            assert len(here.streams) == launched
+            params, grads, T = listed(5, state_bits)
+            one = getattr(T, name)[3]
+            one.data = one.data.clone()
+            with pytest.raises(ValueError, match=name):
+                for _ in range(5):
+                    step(T)
+            with pytest.raises(ValueError, match=name):  # and so is every call after that
+                step(T)
+    for k in range(4):  # both calls a step, as they are used
+        params, grads, T = listed(4, state_bits)
+        params[k].data = params[k].data.clone()
+        with pytest.raises(ValueError, match="params"):
+            for _ in range(4):
+                norm(T)
+                adamw(T)
+
+
+def test_storage_of_listed_tensors_is_held(here, steps):
+    """What the calls point at stays valid when a tensor is given other storage."""
+    import gc
+    import weakref
+
+    import numpy as np
+
+    array = np.zeros(300, np.float32)
+    alive = weakref.ref(array)
+    p = torch.Tensor._make_subclass(Cuda, torch.from_numpy(array))  # (no view, which would hold it too)
+    T = q.OptimTensors.with_states([p], [cuda(300)])
+    p.data = torch.zeros(300)
+    del array
+    gc.collect()
+    assert alive() is not None
+    del T
+    gc.collect()
+    assert alive() is None
