@@ -376,9 +376,11 @@ class OptimTensors:
     The tensors are kept and used in place: keep writing gradients into the
     same storage (or build a new object for new tensors).  Their storage is
     held, so that it stays valid where a listed tensor is given another one
-    (`p.data = ...`, `module.to(...)`); the calls then refuse: each looks at one
-    tensor of every list, in turn, so that they notice at once where all have
-    moved, and after at most as many calls as there are tensors where one has.
+    (`p.data = ...`, `module.to(...)`).  For moved parameters and gradients the
+    calls then refuse: each looks at one of each, in turn, so that they notice at
+    once where all have moved, and where one has after at most as many calls as
+    there are tensors.  (States that move are not noticed: the listed storage is
+    stepped on.)
     No two parameters or states may overlap, nor a gradient with one of them."""
 
     def __init__(self, grads: Sequence[torch.Tensor], params: Optional[Sequence[torch.Tensor]] = None,
@@ -401,17 +403,20 @@ class OptimTensors:
             raise ValueError("OptimTensors: 8-bit states need both m_scale and v_scale")
         self.state_bits = 8 if self.m_scale is not None else 32
         self._c = (qlora_tensor * max(n, 1))()
-        self._at = []  # of each index, its tensors and where they are
+        self._at = []  # of each index, where its gradient and its parameter are
         self._turn = [0, 0]  # of the norm, of the step
+        self._held = []
         f = "OptimTensors"
         for i, g in enumerate(self.grads):
             if g.dtype not in _DTYPES:
                 raise ValueError(f"{f}: grads must be float32 or bfloat16, got {g.dtype}")
             _need(f, f"grads[{i}]", g, self.device)
             c = self._c[i]
-            c.grad, c.n, c.grad_type = g.data_ptr(), g.numel(), _DTYPES[g.dtype]
-            self._at.append([(g, g.data_ptr(), "grads")])
+            at = g.data_ptr()
+            c.grad, c.n, c.grad_type = at, g.numel(), _DTYPES[g.dtype]
+            self._held.append(g.untyped_storage())
             if self.params is None:
+                self._at.append(((g.data_ptr, at),))
                 continue
             p = self.params[i]
             if p.dtype not in _DTYPES:
@@ -429,20 +434,22 @@ class OptimTensors:
                 if x[i].numel() != size:
                     raise ValueError(f"{f}: {name}[{i}] must have {size} values, got {x[i].numel()}")
                 setattr(c, name, x[i].data_ptr())
-                self._at[i].append((x[i], x[i].data_ptr(), name))
+                self._held.append(x[i].untyped_storage())
             c.param, c.param_type = p.data_ptr(), _DTYPES[p.dtype]
-            self._at[i].append((p, p.data_ptr(), "params"))
+            self._held.append(p.untyped_storage())
+            self._at.append(((g.data_ptr, at), (p.data_ptr, p.data_ptr())))
         if self.params is not None:
             self._refuse_overlap()
-        self._held = [x.untyped_storage() for at in self._at for x, _, _ in at]
         self._norm_ws = None  # workspace bytes of qlora_grad_norm
 
     def _in_place(self, where: str, step: bool):
-        """One tensor of each of the call's lists, in turn, is where it was."""
+        """One gradient and, for a step, one parameter, in turn, is where it was."""
         i = self._turn[step]
-        for x, ptr, name in self._at[i] if step else self._at[i][:1]:
-            if x.data_ptr() != ptr:
-                raise ValueError(f"{where}: {name}[{i}] has other storage than when it was listed: "
+        now = self._at[i]
+        for k in range(1 + step):
+            data_ptr, was = now[k]
+            if data_ptr() != was:
+                raise ValueError(f"{where}: {('grads', 'params')[k]}[{i}] has other storage than when it was listed: "
                                  "build a new OptimTensors")
         self._turn[step] = i + 1 if i + 1 < len(self._at) else 0
 
