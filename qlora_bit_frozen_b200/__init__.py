@@ -51,9 +51,10 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> int:
+def _stream(stream, dev) -> int:
+    """The given stream, or the current one of the call's device."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(dev.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -207,7 +208,7 @@ def qlora_quantize_nf4(W: torch.Tensor, B: int = 64, C: int = 256, stream=None) 
         ws = workspace(lib.qlora_quantize_nf4_workspace_bytes(N, B, C), dev)
     with _on(dev):
         st = lib.qlora_quantize_nf4(_ptr(W), O, I, B, C, _ptr(codes), _ptr(q), _ptr(t), _ptr(mu), _ptr(ws),
-                                    ws.numel(), _stream(stream))
+                                    ws.numel(), _stream(stream, dev))
     _check(st, "qlora_quantize_nf4")
     return QuantizedWeight(FMT_NF4_DQ, O, I, B, C, 4, codes, q, t, mu)
 
@@ -232,7 +233,7 @@ def qlora_quantize_nf4_noalloc(W: torch.Tensor, B: int = 64, C: int = 256, strea
         mu = torch.empty(1, dtype=torch.float32, device=dev)
     with _on(dev):
         st = lib.qlora_quantize_nf4_noalloc(_ptr(W), O, I, B, C, _ptr(codes), _ptr(q), _ptr(t), _ptr(mu),
-                                            _stream(stream))
+                                            _stream(stream, dev))
     _check(st, "qlora_quantize_nf4_noalloc")
     return QuantizedWeight(FMT_NF4_DQ, O, I, B, C, 4, codes, q, t, mu)
 
@@ -258,7 +259,7 @@ def qlora_quantize_nf4_fp32scale(W: torch.Tensor, B: int = 64, stream=None) -> Q
         ws = workspace(lib.qlora_quantize_nf4_fp32scale_workspace_bytes(N, B), dev)
     with _on(dev):
         st = lib.qlora_quantize_nf4_fp32scale(_ptr(W), O, I, B, _ptr(codes), _ptr(scale), _ptr(ws), ws.numel(),
-                                              _stream(stream))
+                                              _stream(stream, dev))
     _check(st, "qlora_quantize_nf4_fp32scale")
     return QuantizedWeight(FMT_NF4_FP32SCALE, O, I, B, 0, 4, codes, scale=scale)
 
@@ -280,7 +281,7 @@ def qlora_quantize_affine(W: torch.Tensor, bits: int = 4, G: int = 64, stream=No
         ws = workspace(lib.qlora_quantize_affine_workspace_bytes(N, bits, G), dev)
     with _on(dev):
         st = lib.qlora_quantize_affine(_ptr(W), O, I, bits, G, _ptr(codes), _ptr(scale), _ptr(bias), _ptr(ws),
-                                       ws.numel(), _stream(stream))
+                                       ws.numel(), _stream(stream, dev))
     _check(st, "qlora_quantize_affine")
     return QuantizedWeight(FMT_AFFINE, O, I, G, 0, bits, codes, scale=scale, bias=bias)
 
@@ -306,7 +307,7 @@ def qlora_quantize_int8(W: torch.Tensor, stream=None) -> QuantizedWeight:
         ws = workspace(lib.qlora_quantize_int8_workspace_bytes(O, I), dev)
     with _on(dev):
         st = lib.qlora_quantize_int8(_ptr(W), O, I, _ptr(codes), _ptr(scale), _ptr(ws), ws.numel(),
-                                     _stream(stream))
+                                     _stream(stream, dev))
     _check(st, "qlora_quantize_int8")
     return QuantizedWeight(FMT_INT8, O, I, max(I, 1), 0, 8, codes, scale=scale)
 
@@ -320,7 +321,7 @@ def qlora_dequantize(w: QuantizedWeight, out: Optional[torch.Tensor] = None, str
     _need("qlora_dequantize", "out", out, w.codes.device, (w.O, w.I), torch.float32)
     cw = w.c_struct()
     with _on(w.codes.device):
-        st = lib.qlora_dequantize(ctypes.byref(cw), _ptr(out), _stream(stream))
+        st = lib.qlora_dequantize(ctypes.byref(cw), _ptr(out), _stream(stream, w.codes.device))
     _check(st, "qlora_dequantize")
     return out
 
@@ -342,7 +343,7 @@ def qlora_merge(w: QuantizedWeight, A: torch.Tensor, B: torch.Tensor, alpha: flo
     _need("qlora_merge", "out", out, dev, (w.O, w.I), torch.float32)
     cw = w.c_struct()
     with _on(dev):
-        st = lib.qlora_merge(ctypes.byref(cw), _ptr(A), _ptr(B), r, float(alpha), _ptr(out), _stream(stream))
+        st = lib.qlora_merge(ctypes.byref(cw), _ptr(A), _ptr(B), r, float(alpha), _ptr(out), _stream(stream, dev))
     _check(st, "qlora_merge")
     return out
 
@@ -358,7 +359,8 @@ def qlora_adam_step(params: torch.Tensor, grads: torch.Tensor, m: torch.Tensor, 
         _need("qlora_adam_step", "params/grads/m/v", x, params.device)
     with _on(params.device):
         st = _ffi.load().qlora_adam_step(_ptr(params), _ptr(grads), _ptr(m), _ptr(v), n, int(t), float(lr),
-                                         float(beta1), float(beta2), float(eps), int(page_elems), _stream(stream))
+                                         float(beta1), float(beta2), float(eps), int(page_elems),
+                                         _stream(stream, params.device))
     _check(st, "qlora_adam_step")
 
 
@@ -407,37 +409,38 @@ class OptimTensors:
         self._turn = [0, 0]  # of the norm, of the step
         self._held = []
         f = "OptimTensors"
+        bits8 = self.state_bits == 8
+        states = [(name, x, dt, per) for name, x, dt, per in (
+            ("m", self.m, torch.int8 if bits8 else torch.float32, 1),
+            ("v", self.v, torch.uint8 if bits8 else torch.float32, 1),
+            ("m_scale", self.m_scale, torch.float32, STATE_BLOCK),
+            ("v_scale", self.v_scale, torch.float32, STATE_BLOCK)) if x is not None]
         for i, g in enumerate(self.grads):
             if g.dtype not in _DTYPES:
                 raise ValueError(f"{f}: grads must be float32 or bfloat16, got {g.dtype}")
             _need(f, f"grads[{i}]", g, self.device)
             c = self._c[i]
-            at = g.data_ptr()
-            c.grad, c.n, c.grad_type = at, g.numel(), _DTYPES[g.dtype]
+            grad, values = g.data_ptr(), g.numel()
+            c.grad, c.n, c.grad_type = grad, values, _DTYPES[g.dtype]
             self._held.append(g.untyped_storage())
             if self.params is None:
-                self._at.append(((g.data_ptr, at),))
+                self._at.append(((g.data_ptr, grad),))
                 continue
             p = self.params[i]
             if p.dtype not in _DTYPES:
                 raise ValueError(f"{f}: params must be float32 or bfloat16, got {p.dtype}")
             _need(f, f"params[{i}]", p, self.device, g.shape)
-            bits8 = self.state_bits == 8
-            blocks = -(-g.numel() // STATE_BLOCK)
-            for name, dt, size in (("m", torch.int8 if bits8 else torch.float32, g.numel()),
-                                   ("v", torch.uint8 if bits8 else torch.float32, g.numel()),
-                                   ("m_scale", torch.float32, blocks), ("v_scale", torch.float32, blocks)):
-                x = getattr(self, name)
-                if x is None:
-                    continue
-                _need(f, f"{name}[{i}]", x[i], self.device, dtype=dt)
-                if x[i].numel() != size:
-                    raise ValueError(f"{f}: {name}[{i}] must have {size} values, got {x[i].numel()}")
-                setattr(c, name, x[i].data_ptr())
-                self._held.append(x[i].untyped_storage())
-            c.param, c.param_type = p.data_ptr(), _DTYPES[p.dtype]
+            for name, x, dt, per in states:
+                x, size = x[i], -(-values // per)
+                _need(f, f"{name}[{i}]", x, self.device, dtype=dt)
+                if x.numel() != size:
+                    raise ValueError(f"{f}: {name}[{i}] must have {size} values, got {x.numel()}")
+                setattr(c, name, x.data_ptr())
+                self._held.append(x.untyped_storage())
+            param = p.data_ptr()
+            c.param, c.param_type = param, _DTYPES[p.dtype]
             self._held.append(p.untyped_storage())
-            self._at.append(((g.data_ptr, at), (p.data_ptr, p.data_ptr())))
+            self._at.append(((g.data_ptr, grad), (p.data_ptr, param)))
         if self.params is not None:
             self._refuse_overlap()
         self._norm_ws = None  # workspace bytes of qlora_grad_norm
@@ -513,7 +516,7 @@ def qlora_grad_norm(tensors: OptimTensors, max_norm: float, control: torch.Tenso
                 ws = workspace(qlora_grad_norm_workspace_bytes(tensors), dev)
         _need(f, "ws", ws, dev)
         st = _ffi.load().qlora_grad_norm(tensors._c, len(tensors.grads), float(max_norm), _ptr(control),
-                                         _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+                                         _ptr(ws), ws.numel() * ws.element_size(), _stream(stream, dev))
     _check(st, f)
     return control
 
@@ -535,7 +538,7 @@ def qlora_adamw_step(tensors: OptimTensors, t: int = 0, lr: float = 1e-3, beta1:
     with _on(dev):
         st = _ffi.load().qlora_adamw_step(tensors._c, len(tensors.grads), tensors.state_bits, int(t), float(lr),
                                           float(beta1), float(beta2), float(eps), float(weight_decay),
-                                          _ptr(control), _stream(stream))
+                                          _ptr(control), _stream(stream, dev))
     _check(st, f)
 
 
@@ -578,7 +581,7 @@ def qlora_linear_fwd(w: QuantizedWeight, X: torch.Tensor, A: torch.Tensor, B: to
     _need(f, "ws", ws, dev)
     with _on(dev):
         st = lib.qlora_linear_fwd(cw, _ptr(X), R, _ptr(A), _ptr(B), r, float(alpha), compute,
-                                  _ptr(Y), _ptr(U_out), _ptr(ws), ws.numel(), _stream(stream))
+                                  _ptr(Y), _ptr(U_out), _ptr(ws), ws.numel(), _stream(stream, dev))
     _check(st, "qlora_linear_fwd")
     return Y, U_out
 
@@ -617,7 +620,7 @@ def qlora_linear_bwd(w: QuantizedWeight, X: Optional[torch.Tensor], dY: torch.Te
     with _on(wd):
         st = lib.qlora_linear_bwd(cw, _ptr(X), _ptr(dY), R, _ptr(A), _ptr(B), r, float(alpha),
                                   _ptr(U), compute, _ptr(dX if want_dx else None), _ptr(dA if want_da else None),
-                                  _ptr(dB if want_db else None), _ptr(ws), ws.numel(), _stream(stream))
+                                  _ptr(dB if want_db else None), _ptr(ws), ws.numel(), _stream(stream, wd))
     _check(st, "qlora_linear_bwd")
     return (dX if want_dx else None), (dA if want_da else None), (dB if want_db else None)
 
@@ -625,13 +628,14 @@ def qlora_linear_bwd(w: QuantizedWeight, X: Optional[torch.Tensor], dY: torch.Te
 def qlora_workspace_status(ws: torch.Tensor, stream=None) -> int:
     """Device error word of the last call that used ws (synchronizes)."""
     with _on(ws.device):
-        return int(_ffi.load().qlora_workspace_status(_ptr(ws), _stream(stream)))
+        return int(_ffi.load().qlora_workspace_status(_ptr(ws), _stream(stream, ws.device)))
 
 
 def qlora_selftest_wait_timeout(limit_us: int = 1000, stream=None, device="cuda") -> int:
     ws = workspace(256, device)
     with _on(ws.device):
-        return int(_ffi.load().qlora_selftest_wait_timeout(_ptr(ws), ws.numel(), int(limit_us), _stream(stream)))
+        return int(_ffi.load().qlora_selftest_wait_timeout(_ptr(ws), ws.numel(), int(limit_us),
+                                                           _stream(stream, ws.device)))
 
 
 def qlora_kernel_launch_count() -> int:

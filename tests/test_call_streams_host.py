@@ -125,9 +125,9 @@ def test_calls_run_on_the_device_of_their_tensors(here, call, monkeypatch):
         at.pop()
 
     monkeypatch.setattr(q, "_on", on)
-    monkeypatch.setattr(q, "_stream", lambda s: list(at))
+    monkeypatch.setattr(q, "_stream", lambda s, dev: at + [dev])
     call(weight(), cuda(32, 48), cuda(8, 48), cuda(32, 8))
-    assert here.streams == [[torch.device("cpu")]]
+    assert here.streams == [2 * [torch.device("cpu")]]
 
 
 def listed(n, state_bits=32):
