@@ -347,7 +347,8 @@ size_t qlora_grad_norm_workspace_bytes(const qlora_tensor* tensors, int32_t coun
 /*
  * Global L2 norm of all gradients, and the decisions taken on it:
  *   norm  = fp32(sqrt(sum of grad^2)), squares and sums in 64 bits, in an
- *           order that depends on the sizes alone (deterministic);
+ *           order that depends on the sizes, on the arrays' alignment and on
+ *           the GPU's number of SMs (the same call gives the same bits);
  *   scale = max_norm / norm where max_norm > 0 and norm > max_norm, else 1;
  *   skip  = norm is NaN or Inf (a NaN or Inf gradient, or a norm above
  *           FLT_MAX); scale is then 1;
@@ -375,7 +376,15 @@ qlora_status qlora_grad_norm(const qlora_tensor* tensors, int32_t count, float m
  *   k = round(255 sqrt(sqrt(v) fp32(1 / v_scale))), at least 1 where v > 0
  * (so no moving value is divided by a second moment that was rounded to
  * zero); a block whose maximum is below FLT_MIN gets codes of 0.  A NaN
- * gradient in a step that is not skipped makes its block of 256 states NaN.
+ * gradient in a step that is not skipped makes its block of 256 states NaN,
+ * and so, one step later, does a second moment above FLT_MAX (|g| above
+ * 1.8e19).
+ * A code is the nearest one, so a state that a step moves by less than half
+ * a code (a code k of v is 4/k of its value wide) stays where it is: with
+ * b2 = 0.999, where v falls by 0.1% a step at most, a value whose gradients
+ * become smaller keeps its old second moment unless its block's maximum
+ * falls with it (gradients of half a block cut to 0.3: sqrt(v) still three
+ * times too large after 3000 steps; with b2 = 0.99 it follows to 3%).
  * tensors: HOST array (see qlora_grad_norm).  control (DEVICE, nullable):
  * gives scale, skip and t (t < 1, before the first qlora_grad_norm, changes
  * nothing); when NULL, t >= 1 is the argument.  Requires
@@ -400,7 +409,10 @@ qlora_status qlora_adamw_step(const qlora_tensor* tensors, int32_t count, int32_
  * per call and its GEMM reads it there.  INT8 weights: it holds the rows'
  * codes (a byte a value) and, where many tokens are fp32 or bf16 of a width
  * that is no multiple of 8, a copy of X (and dY) in bf16 parts (6 or 2 bytes
- * a value).  0 for what the calls refuse.  The workspace is scratch for one
+ * a value).  (There is none for bf16 arrays of other widths that do not
+ * start on 16 bytes, which this query does not see: their U, V, dA and dB
+ * are taken by fp32 FMAs, several times slower for many tokens.)
+ * 0 for what the calls refuse.  The workspace is scratch for one
  * call at a time; the weight itself stays packed.
  */
 size_t qlora_linear_workspace_bytes(const qlora_weight* w, int64_t R, int32_t r, int32_t op,

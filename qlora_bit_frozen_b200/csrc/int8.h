@@ -99,9 +99,10 @@ cudaError_t launch_int8_tc(const Int8Call& c, const int8_t* xq, const float* xs,
                            uint32_t* hdr, cudaStream_t st);
 
 // int8_side.cu: the adapter's thin products over bf16 matrices: P [R x N] itself
-// or a copy of it in bf16 parts (one of bf16 values whose rows do not start on 16
-// bytes, three of fp32 values), a row's parts one after the other, `pitch` columns
-// each.  parts 0: the fp32 kernels take P.
+// or a copy of it in bf16 parts (one of bf16 values whose N is no multiple of 8,
+// three of fp32 values), a row's parts one after the other, `pitch` columns each.
+// parts 0: the fp32 kernels take P (few rows, and bf16 of other N whose P does not
+// start on 16 bytes: the workspace is sized without the pointers).
 struct SideMatrix {
   const void* P;   // [R x parts * pitch]
   int64_t N, pitch;

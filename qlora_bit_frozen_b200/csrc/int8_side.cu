@@ -13,8 +13,8 @@
 // warps drain it into fp32 registers while the other one fills.  Measured error
 // 2e-7 of the result where one running sum over 8192 tokens had 3e-6 to 9e-6.
 //
-// Matrices that TMA does not take as they are (fp32 values, or rows that do not
-// start on 16 bytes) are copied in bf16 parts first, where that pays: the parts'
+// Matrices that TMA does not take as they are (fp32 values, or bf16 of a width that
+// is no multiple of 8) are copied in bf16 parts first, where that pays: the parts'
 // products meet in the same sums.  The backward of 8192 tokens of 4096 x 4096 in
 // fp32 at rank 64: 465 us, by fp32 FMAs 3250.
 //
@@ -518,6 +518,9 @@ bool side_takes(const void* P, int64_t R, int64_t N) {
 // bf16), the fp32 kernels their products (eight columns of the factor at least).
 // 8192 x 4096 in fp32 at rank 16 (2^29): U in 102 us with the copy, 141 by FMAs;
 // at rank 8 100 and 70.  8191 x 4097 in bf16 at rank 8 (2^28): 48 and 110.
+// A bf16 matrix of other N has no copy, also where its base is unaligned (8192 x
+// 4096 x 4096, backward: 175 us aligned and 566 unaligned at rank 8, 212 and 4890 at
+// rank 64): its room would be reserved for every aligned one.
 bool side_copies(bool bf16, int64_t R, int64_t N, int32_t r) {
   if (R <= 256 || (bf16 && N % 8 == 0)) return false;
   return (double)R * (double)N * ((r + 7) / 8 * 8) >= (bf16 ? 134217728.0 : 536870912.0);

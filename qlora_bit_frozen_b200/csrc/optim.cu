@@ -282,9 +282,10 @@ __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, ui
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// One block.  Bound by HBM with 32-bit states; with 8-bit ones by instructions
-// as much as by HBM (16 bytes a value), which is why all but the division and
-// the root work on pairs, and the codes' roots are the approximate ones: their
+// One block.  Bound by HBM with 32-bit states; with 8-bit ones (16 bytes a value)
+// nothing is full, 68% of the issue slots and half of HBM's rate: a warp has one
+// block on its way at a time, so arithmetic and memory take turns.  All but the
+// division and the root work on pairs, and the codes' roots are the approximate ones: their
 // products are within 255 (2^-22 + 2^-24) of the definition's, so they round to
 // the same integer unless within 1e-4 of a half; only then (2e-4, one test for
 // the lane's eight values) are the exact roots taken.  64 M values, fp32 parameters
