@@ -63,7 +63,7 @@ _HERE = contextlib.nullcontext()
 
 def _on(dev):
     """Makes the tensors' device the current one for a call."""
-    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return _HERE if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _need(where: str, name: str, t: Optional[torch.Tensor], dev, shape=None, dtype=None):
