@@ -87,14 +87,16 @@ def workspace(nbytes: int, device="cuda") -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
-def _on_stream(stream, dev):
+def _on_stream(stream, dev, *given):
     """Allocations and copies of a call are made on the stream that it runs on:
     memory of another stream's pool may still be in use there or be handed out
-    again there too early, and a copy made there is not ordered before the call."""
-    if stream is None:
+    again there too early, and a copy made there is not ordered before the call.
+    (Nothing to do where all buffers are given: the switch takes microseconds.)"""
+    if stream is None or (given and all(t is not None for t in given)):
         return _HERE
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = _stream(stream, dev)
+        stream = torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev)
     return torch.cuda.stream(stream)
 
 
@@ -565,7 +567,7 @@ def qlora_linear_fwd(w: QuantizedWeight, X: torch.Tensor, A: torch.Tensor, B: to
     r = A.shape[0]
     compute = _compute_of(X)
     cw = ctypes.byref(w.c_struct())
-    with _on_stream(stream, X.device):
+    with _on_stream(stream, X.device, Y, U_out if want_u else Y, ws):
         if Y is None:
             Y = X.new_empty((R, w.O))
         if U_out is None and want_u:
@@ -598,7 +600,7 @@ def qlora_linear_bwd(w: QuantizedWeight, X: Optional[torch.Tensor], dY: torch.Te
     compute = _compute_of(dY)
     dev = dY.device
     cw = ctypes.byref(w.c_struct())
-    with _on_stream(stream, dev):
+    with _on_stream(stream, dev, dX if want_dx else dY, dA if want_da else dY, dB if want_db else dY, ws):
         if want_dx and dX is None:
             dX = torch.empty((R, w.I), dtype=dY.dtype, device=dev)
         if want_da and dA is None:

@@ -68,6 +68,7 @@ def here(monkeypatch):
     monkeypatch.setattr(q._ffi, "load", lambda: lib)
     monkeypatch.setattr(torch, "empty", noted)
     monkeypatch.setattr(torch.cuda, "stream", on_stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda raw, device: {77: SIDE}[raw])
     monkeypatch.setattr(q, "_on", lambda dev: contextlib.nullcontext())
     return lib
 
@@ -98,6 +99,18 @@ def weight(O=32, I=48):
 def test_outputs_are_allocated_on_the_stream_of_the_call(here, call):
     call(weight(), cuda(4, 48), cuda(8, 48), cuda(32, 8))
     assert Cuda.seen and {s for _, s in Cuda.seen} == {SIDE} and here.streams == [77]
+
+
+@pytest.mark.parametrize("stream", [SIDE, 77])
+def test_no_switch_of_streams_where_all_buffers_are_given(here, monkeypatch, stream):
+    """Any stream that says its handle does, and the switch is left out."""
+    monkeypatch.setattr(torch.cuda, "stream", None)
+    w, X, A, B, ws = weight(), cuda(4, 48), cuda(8, 48), cuda(32, 8), cuda(512)
+    q.qlora_linear_fwd(w, X, A, B, 1.0, Y=cuda(4, 32), U_out=cuda(4, 8), ws=ws, stream=stream)
+    q.qlora_linear_fwd(w, X, A, B, 1.0, Y=cuda(4, 32), want_u=False, ws=ws, stream=stream)
+    q.qlora_linear_bwd(w, X, cuda(4, 32), A, B, 1.0, dX=cuda(4, 48), dA=cuda(8, 48), dB=cuda(32, 8), ws=ws, stream=stream)
+    q.qlora_linear_bwd(w, X, cuda(4, 32), A, B, 1.0, dX=cuda(4, 48), want_da=False, want_db=False, ws=ws, stream=stream)
+    assert here.streams == [77] * 4
 
 
 @pytest.mark.parametrize("call", [
