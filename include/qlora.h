@@ -445,7 +445,8 @@ size_t qlora_linear_workspace_bytes(const qlora_weight* w, int64_t R, int32_t r,
  * token that holds a NaN or Inf gives a row of NaN; other tokens do not see
  * it.  U (and, in the backward, V, dA and dB) use all 24 bits of the fp32
  * factors and of fp32 activations (split into three bf16 parts, or multiplied
- * in fp32), and so does the adapter's term in Y and dX.
+ * in fp32), and so does the adapter's term in Y and dX.  (Magnitudes from
+ * 3.396e38 on, which bf16 rounds to Inf, may count as Inf there.)
  * Requires codes on a 16-byte boundary, 1 <= O, I <= 131072 (above which the
  * 32-bit sum could overflow: QLORA_ERR_UNSUPPORTED) and R <= 2^28.
  */
